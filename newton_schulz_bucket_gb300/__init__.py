@@ -12,7 +12,20 @@ from typing import Dict, List, Sequence
 from . import _capi as _c
 from ._capi import MuonError  # noqa: F401
 
-__all__ = ["MuonPlan", "describe", "assign_owners", "load_library", "MuonError", "QUINTIC"]
+_LAYERS = ("linear", "linear_backward", "expert_linear", "expert_linear_backward", "gate", "gate_backward",
+           "dispatch", "dispatch_backward", "combine", "combine_backward", "check_ops_error")
+
+__all__ = ["MuonPlan", "describe", "assign_owners", "load_library", "MuonError", "QUINTIC", *_LAYERS]
+
+
+def __getattr__(name):
+    # the layer operators need torch; planning does not, so they load on first use
+    if name in _LAYERS or name == "layers":
+        from importlib import import_module
+        mod = import_module(".layers", __name__)
+        globals().update({n: getattr(mod, n) for n in _LAYERS})
+        return mod if name == "layers" else globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 

@@ -37,6 +37,20 @@ MUON_FLAG_NESTEROV = 16
 MUON_FLAG_MERGE_TRANSPOSED = 32
 MUON_MAX_SCHEDULE_ROWS = 64
 
+# include/muon_ops.h
+MUON_DTYPE_F32 = 0
+MUON_DTYPE_F16 = 1
+MUON_DTYPE_BF16 = 2
+MUON_ACT_NONE = 0
+MUON_ACT_RELU = 1
+MUON_ACT_SILU = 2
+MUON_ACT_GELU = 3
+MUON_ACT_GELU_TANH = 4
+MUON_W_IN_OUT = 0
+MUON_W_OUT_IN = 1
+MUON_MAX_EXPERTS = 1024
+MUON_MAX_TOP_K = 32
+
 
 class muon_shape_t(C.Structure):
     _fields_ = [("ndim", C.c_int32), ("reserved_", C.c_int32), ("dims", C.c_int64 * 3)]
@@ -56,6 +70,17 @@ class muon_group_info_t(C.Structure):
                 ("workspace_bytes", C.c_int64)]
 
 
+class muon_linear_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("activation", C.c_int32), ("experts", C.c_int32),
+                ("w_layout", C.c_int32), ("rows", C.c_int64), ("in", C.c_int64), ("out", C.c_int64),
+                ("x_stride", C.c_int64), ("w_stride", C.c_int64), ("w_expert_stride", C.c_int64),
+                ("residual_stride", C.c_int64), ("dy_stride", C.c_int64), ("x", C.c_void_p),
+                ("w", C.c_void_p), ("bias", C.c_void_p), ("residual", C.c_void_p),
+                ("offsets", C.c_void_p), ("preact", C.c_void_p), ("dy", C.c_void_p), ("y", C.c_void_p),
+                ("preact_out", C.c_void_p), ("dx", C.c_void_p), ("dw", C.c_void_p), ("db", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
 # test hooks declared in include/muon_testing.h
 EXPORTED_TESTING = ["muon_testing_tc_gemm", "muon_testing_skinny_max_clusters",
                     "muon_testing_tile_walk", "muon_testing_tile_walk_pair",
@@ -69,6 +94,12 @@ EXPORTED = ["muon_default_options", "muon_plan_describe", "muon_plan_create", "m
             "muon_plan_check_error", "muon_plan_group_elapsed_ms", "muon_step_skinny_static",
             "muon_status_string",
             "muon_last_error", "muon_version"]
+
+# every symbol include/muon_ops.h declares
+EXPORTED_OPS = ["muon_linear_workspace", "muon_linear", "muon_linear_backward", "muon_gate",
+                "muon_gate_backward", "muon_dispatch_workspace", "muon_dispatch",
+                "muon_dispatch_backward", "muon_combine", "muon_combine_backward",
+                "muon_ops_check_error"]
 
 _lib = None
 
@@ -128,6 +159,19 @@ def load() -> C.CDLL:
     L.muon_testing_tc_pair_form.restype = i32
     L.muon_testing_wait_probe.argtypes = [i32, i64, vp]
     L.muon_testing_wait_probe.restype = C.c_int
+    L.muon_linear_workspace.argtypes = [C.POINTER(muon_linear_args), i32, C.POINTER(C.c_size_t)]
+    L.muon_linear.argtypes = [C.POINTER(muon_linear_args), vp]
+    L.muon_linear_backward.argtypes = [C.POINTER(muon_linear_args), vp]
+    L.muon_gate.argtypes = [i32, i64, i32, i32, i32, vp, i64, vp, vp, vp]
+    L.muon_gate_backward.argtypes = [i32, i64, i32, i32, i32, vp, vp, i64, vp, vp, vp]
+    L.muon_dispatch_workspace.argtypes = [i64, i32, i32, C.POINTER(C.c_size_t)]
+    L.muon_dispatch.argtypes = [i32, i64, i64, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, C.c_size_t, vp]
+    L.muon_dispatch_backward.argtypes = [i32, i64, i64, i32, vp, i64, vp, vp, vp]
+    L.muon_combine.argtypes = [i32, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp]
+    L.muon_combine_backward.argtypes = [i32, i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.muon_ops_check_error.argtypes = []
+    for name in EXPORTED_OPS:
+        getattr(L, name).restype = C.c_int
     L.muon_status_string.argtypes = [C.c_int]
     L.muon_status_string.restype = C.c_char_p
     L.muon_last_error.argtypes = []
