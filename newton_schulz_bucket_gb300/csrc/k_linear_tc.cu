@@ -1,0 +1,677 @@
+// A layer's product on the tensor cores: D(m, n) = act(sum_k A(m, k) B(k, n) +
+// bias) + residual in fp16 / bf16 operands with fp32 sums.
+//
+// A cluster of two CTAs computes one 256 x BN tile with tcgen05.mma
+// cta_group::2, as the Newton-Schulz products do: each CTA stages its 128 rows
+// of A and its half of B's columns in a ring of TMA tiles, the leader issues the
+// MMAs, and both hold 128 rows of the accumulator in TMEM (two accumulators,
+// so that the epilogue of one tile runs under the products of the next).
+// Either operand may be stored along k or across it; the three layouts that a
+// layer needs are instantiated: y = x W and dx = dz W^T read A along k, dw =
+// x^T dz reads both across k, so no operand is ever transposed in memory.
+//
+// Experts.  Row ranges come from a device array, so every role walks the
+// ranges itself.  GROUP_ROWS: an expert's rows are tiled from its first row;
+// rows past its end are loaded (they are the next expert's) and not stored.
+// GROUP_SUM: the sum over an expert's rows ends inside a 64-row block of the
+// ring, whose other rows belong to the next expert, and may hold NaN there: a
+// helper warp overwrites them in shared memory with zeros, in both operands,
+// before the block is handed to the MMAs.
+//
+// Epilogue: eight warps, 32 x 32 blocks through a swizzled staging block so
+// that global accesses run along rows (16 bytes a lane, or one element a lane
+// where rows are not 16-byte aligned).
+#include <cuda.h>
+
+#include <mutex>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "mbarrier.cuh"
+#include "tcgen05.cuh"
+
+namespace muon {
+
+namespace {
+
+constexpr int BM = 256;     // rows of a pair's tile
+constexpr int BK = 64;      // one 128-byte swizzle row of k
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, epilogue, range-tail helper
+
+__device__ int g_err;       // the operators' error word (one per device)
+
+struct TcProduct {
+  int mode, experts, splits;
+  const int32_t* offsets;
+  int M, N, K;
+  int tiles_m, tiles_n;     // of the whole output (GROUP_ROWS: tiles_n only)
+  int bf16, act, vec;       // vec: rows of every epilogue tensor start on 16 bytes
+  void* D;
+  const void* bias;
+  const void* residual;
+  int64_t r_m;
+  void* preact;
+  float* part;              // splits > 1: [splits][M][part_pitch] sums
+  int64_t part_pitch;
+  int* err;
+};
+
+template <int BN>
+struct Smem {
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr uint32_t kA = 128 * BK * 2;
+  static constexpr uint32_t kB = BN / 2 * BK * 2;
+  static constexpr uint32_t kStage = kA + kB;
+  static constexpr uint32_t kBars = kStages * kStage;  // full, empty, fix, tfull, tempty, done; TMEM slot, abort
+  static constexpr uint32_t kEpi = kBars + 256;
+  static constexpr uint32_t kTotal = kEpi + kEpiWarps * 4096 + 1024;  // + alignment slack
+  static_assert((3 * kStages + 5) * 8 + 8 <= 256 && kTotal <= 227 * 1024, "shared memory layout");
+};
+
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
+  const int v = __ldg(p.offsets + e);
+  return v < 0 ? 0 : (v > hi ? hi : v);
+}
+
+// One output tile's work: rows m0 .. m_end - 1 (256 at most), columns n0 ..,
+// sum over k0 .. k1 - 1.
+struct Item {
+  int e, m0, m_end, n0, k0, k1, split;
+};
+
+// 8 tile rows share a sweep over the tile columns, so that the tiles in
+// flight reuse a compact set of panels through L2.
+__device__ __forceinline__ void raster(int r, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int GM = 8;
+  const int group = r / (GM * tiles_n), first = group * GM;
+  const int gsz = min(tiles_m - first, GM);
+  r -= group * GM * tiles_n;
+  tm = first + r % gsz;
+  tn = r / gsz;
+}
+
+// Walks this pair's tiles: every role of both CTAs sees the same sequence.
+template <int BN>
+struct Walk {
+  int t, step;
+  int e, lo, hi, base, cnt;  // current range, its first tile and tile count
+  __device__ __forceinline__ Walk(const TcProduct& p)
+      : t(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), base(0), cnt(0) {}
+  __device__ __forceinline__ bool next(const TcProduct& p, Item& it) {
+    int tm, tn;
+    it.split = 0;
+    if (p.mode == GROUP_ROWS) {
+      while (t >= base + cnt) {
+        base += cnt;
+        if (++e >= p.experts) return false;
+        lo = range_at(p, e, p.M);
+        hi = range_at(p, e + 1, p.M);
+        cnt = hi > lo ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
+      }
+      raster(t - base, (hi - lo + BM - 1) / BM, p.tiles_n, tm, tn);
+      it.e = e;
+      it.m0 = lo + tm * BM;
+      it.m_end = hi;
+      it.k0 = 0;
+      it.k1 = p.K;
+    } else {
+      const int per = p.tiles_m * p.tiles_n;
+      const int g = t / per;
+      if (g >= (p.mode == GROUP_SUM ? p.experts : p.splits)) return false;
+      raster(t - g * per, p.tiles_m, p.tiles_n, tm, tn);
+      it.m0 = tm * BM;
+      it.m_end = p.M;
+      if (p.mode == GROUP_SUM) {
+        it.e = g;
+        it.k0 = range_at(p, g, p.K);
+        it.k1 = max(it.k0, range_at(p, g + 1, p.K));
+      } else {
+        it.e = 0;
+        it.split = g;
+        const int kb = (p.K + BK - 1) / BK;
+        it.k0 = (int)((int64_t)kb * g / p.splits) * BK;
+        it.k1 = g + 1 == p.splits ? p.K : (int)((int64_t)kb * (g + 1) / p.splits) * BK;
+      }
+    }
+    it.n0 = tn * BN;
+    t += step;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float ld16(const void* p, int64_t i, int bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+              : __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void st16(void* p, int64_t i, float v, int bf16) {
+  if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float* f, int bf16) {
+  if (bf16) {
+    bf16x8_to_f32(u, f);
+  } else {
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(h[i]);
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f, int bf16) {
+  if (bf16) return f32_to_bf16x8(f);
+  uint4 u;
+  __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+  return u;
+}
+__device__ __forceinline__ void activate8(float* v, int act) {
+  switch (act) {
+    case ACT_NONE: break;
+    case ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_RELU);
+      break;
+    case ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_SILU);
+      break;
+    case ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_GELU);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_GELU_TANH);
+  }
+}
+
+// A warp's 32 x 32 block from TMEM into its staging block, row = lane, the
+// 16-byte pieces of row r at piece index ^ (r & 7): both this write and the
+// reads along rows below are free of bank conflicts.
+__device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane, bool zero) {
+  uint32_t r[32];
+  tmem_ld32(taddr, r);
+  uint4* row = reinterpret_cast<uint4*>(sw + lane * 32);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    row[q ^ (lane & 7)] = zero ? make_uint4(0, 0, 0, 0)
+                               : make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+  __syncwarp();
+}
+
+// Rows row0 .. row0 + 31 (those < m_end) and columns col0 .. col0 + 31 (those
+// < N) of the output from the staging block.
+__device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int e, int row0,
+                                            int m_end, int col0, int64_t d_base) {
+  const int64_t N = p.N;
+  if (p.vec && col0 + 32 <= p.N) {
+    const int q = lane & 3, c = col0 + q * 8;
+    float b[8];
+    if (p.bias) {
+      unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + e * N + c)), b, p.bf16);
+    }
+    uint4 res[4];
+    if (p.residual) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int row = row0 + it * 8 + (lane >> 2);
+        if (row < m_end)
+          res[it] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int rr = it * 8 + (lane >> 2), row = row0 + rr;
+      const uint4* src = reinterpret_cast<const uint4*>(sw + rr * 32);
+      float v[8];
+      u4_to_f4x2(src[(2 * q) ^ (rr & 7)], src[(2 * q + 1) ^ (rr & 7)], v);
+      if (row >= m_end) continue;
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
+      }
+      if (p.preact)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * N + c) = pack8(v, p.bf16);
+      activate8(v, p.act);
+      if (p.residual) {
+        float r[8];
+        unpack8(res[it], r, p.bf16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + d_base + row * N + c) = pack8(v, p.bf16);
+    }
+  } else if (col0 + lane < p.N) {
+    const int c = col0 + lane;
+    const float b = p.bias ? ld16(p.bias, e * N + c, p.bf16) : 0.f;
+    for (int rr = 0; rr < 32 && row0 + rr < m_end; ++rr) {
+      const int64_t row = row0 + rr;
+      float v = sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)] + b;
+      if (p.preact) st16(p.preact, row * N + c, v, p.bf16);
+      v = activate<true>(v, p.act);
+      if (p.residual) v += ld16(p.residual, row * p.r_m + c, p.bf16);
+      st16(p.D, d_base + row * N + c, v, p.bf16);
+    }
+  }
+  __syncwarp();  // the block is overwritten next
+}
+
+// The same block of one part of a split sum, in fp32 (pitch a multiple of 32).
+__device__ __forceinline__ void write_part(const TcProduct& p, const float* sw, int lane, int row0, int col0,
+                                           int split) {
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int rr = it * 4 + (lane >> 3), row = row0 + rr, q = lane & 7;
+    const uint4 u = reinterpret_cast<const uint4*>(sw + rr * 32)[q ^ (rr & 7)];
+    if (row < p.M && col0 < p.part_pitch)
+      *reinterpret_cast<uint4*>(p.part + ((int64_t)split * p.M + row) * p.part_pitch + col0 + q * 4) = u;
+  }
+  __syncwarp();
+}
+
+// n elements of 16 bits to zero, by all epilogue threads of the grid.
+__device__ void zero_span(void* base, int64_t from, int64_t to, int64_t tid, int64_t n_threads) {
+  uint16_t* p = static_cast<uint16_t*>(base);
+  while (from < to && (reinterpret_cast<uintptr_t>(p + from) & 15)) {
+    if (tid == 0) p[from] = 0;
+    ++from;
+  }
+  const int64_t v = (to - from) / 8;
+  for (int64_t i = tid; i < v; i += n_threads) reinterpret_cast<uint4*>(p + from)[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = from + v * 8 + tid; i < to; i += n_threads) p[i] = 0;
+}
+
+template <bool AMN, bool BMN, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                const __grid_constant__ TcProduct p) {
+  using L = Smem<BN>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const uint32_t bar0 = saddr(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+  auto fix = [&](int s) { return bar0 + 8u * (2 * S + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (3 * S + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (3 * S + 2 + a); };
+  const uint32_t done = bar0 + 8u * (3 * S + 4);
+  constexpr uint32_t kCols = 2 * BN;  // two accumulators
+  const bool group_sum = p.mode == GROUP_SUM;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      // GROUP_SUM: a block may be handed over by each CTA's helper, so each CTA arrives
+      mbar_init(full(s), group_sum ? 2 : 1);
+      mbar_init(empty(s), 1);
+      mbar_init(fix(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), 2 * kEpiWarps); }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapA) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapB) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_barrier();  // both CTAs' barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  Walk<BN> walk(p);
+  Item it;
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---- TMA producer (both CTAs) ----
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        const int arow = it.m0 + (int)rank * 128, bcol = it.n0 + (int)rank * (BN / 2);
+        const int be = p.mode == GROUP_ROWS ? it.e : 0;
+        for (int k = it.k0; k < it.k1; k += BK) {
+          if (!(ok = mbar_wait(empty(s), ph ^ 1, abort_flag, p.err, 1))) break;
+          const uint32_t sa = saddr(smem + s * L::kStage), sb = sa + L::kA;
+          const bool tail = group_sum && it.k1 - k < BK;
+          uint32_t bar;  // where this CTA's copies are counted: the leader's ring, or its own helper
+          if (tail) {
+            bar = fix(s);
+            mbar_expect_tx(bar, L::kStage);
+          } else {
+            bar = map_to(full(s), 0);
+            if (rank == 0) mbar_expect_tx(full(s), 2 * L::kStage);
+            else if (group_sum) mbar_arrive_cluster(bar);
+          }
+          if (AMN) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tma_load_3d_pair(sa + c * (64 * BK * 2), &mapA, bar, arow + c * 64, k, 0);
+          } else {
+            tma_load_3d_pair(sa, &mapA, bar, k, arow, 0);
+          }
+          if (BMN) {
+#pragma unroll
+            for (int c = 0; c < BN / 128; ++c)
+              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, bcol + c * 64, k, be);
+          } else {
+            tma_load_3d_pair(sb, &mapB, bar, k, bcol, be);
+          }
+          if (++s == S) { s = 0; ph ^= 1; }
+        }
+      }
+      if (!ok) {  // gave up: let the copies in flight land before the block leaves
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 21)) {}
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {  // ---- MMA issuer (leader only) ----
+      const uint32_t idesc = instr_desc(p.bf16 ? 1u : 0u, BM, BN, BMN, AMN);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        if (!(ok = mbar_wait(tempty(acc), aph ^ 1, abort_flag, p.err, 2))) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        for (int k = it.k0; k < it.k1; k += BK) {
+          if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
+          tc_fence_after();
+          const uint32_t sa = saddr(smem + s * L::kStage), sb = sa + L::kA;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = AMN ? smem_desc(sa + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sa + kk * 32, 16, 1024);
+            const uint64_t bd = BMN ? smem_desc(sb + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sb + kk * 32, 16, 1024);
+            umma_pair(d_tmem, ad, bd, idesc, k != it.k0 || kk != 0);
+          }
+          umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
+          if (++s == S) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        umma_commit_pair(tfull(acc), 3);
+        if (++acc == 2) { acc = 0; aph ^= 1; }
+      }
+      // every MMA issued has completed before TMEM and shared memory go away
+      // (waited for even after an abort, so the wait ignores the abort flag)
+      umma_commit_pair(done, 1);
+      volatile int keep_waiting = 0;
+      mbar_wait(done, 0, &keep_waiting, p.err, 16);
+    }
+  } else if (warp < 2 + kEpiWarps) {  // ---- epilogue ----
+    const int quarter = warp & 3;     // TMEM lanes this warp may read
+    const int half = (warp - 2) >> 2; // which half of the tile's columns
+    float* sw = reinterpret_cast<float*>(smem + L::kEpi) + (warp - 2) * 1024;
+    int acc = 0;
+    uint32_t aph = 0;
+    while (walk.next(p, it)) {
+      if (!mbar_wait(tfull(acc), aph, abort_flag, p.err, 8)) break;
+      tc_fence_after();
+      const int row0 = it.m0 + (int)rank * 128 + quarter * 32;
+      const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
+#pragma unroll 1
+      for (int ch = half * (BN / 64); ch < (half + 1) * (BN / 64); ++ch) {
+        const int col0 = it.n0 + ch * 32;
+        if (col0 >= p.N || row0 >= it.m_end) break;  // the same for the whole warp
+        stage_block(tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ch * 32), sw,
+                    lane, it.k0 >= it.k1);
+        if (p.splits > 1) write_part(p, sw, lane, row0, col0, it.split);
+        else write_block(p, sw, lane, it.e, row0, it.m_end, col0, d_base);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to(tempty(acc), 0));
+      if (++acc == 2) { acc = 0; aph ^= 1; }
+    }
+    if (p.mode == GROUP_ROWS) {  // rows of no expert
+      const int64_t from = (int64_t)range_at(p, p.experts, p.M) * p.N, to = (int64_t)p.M * p.N;
+      const int64_t tid = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 64;
+      const int64_t n_threads = (int64_t)gridDim.x * (32 * kEpiWarps);
+      zero_span(p.D, from, to, tid, n_threads);
+      if (p.preact) zero_span(p.preact, from, to, tid, n_threads);
+    }
+  } else if (group_sum) {  // ---- helper: zeros behind a range's end ----
+    int s = 0;
+    uint32_t fph = 0;  // parity of each stage's fix barrier
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      const int blocks = (it.k1 - it.k0 + BK - 1) / BK, rem = (it.k1 - it.k0) % BK;
+      if (rem) {
+        const int st = (s + blocks - 1) % S;
+        if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32))) break;
+        fph ^= 1u << st;
+        uint8_t* stage = smem + st * L::kStage;
+        for (int box = 0; box < (int)(L::kStage / (64 * BK * 2)); ++box)  // 64 rows of k, 128 bytes each
+          for (int i = rem * 8 + lane; i < BK * 8; i += 32)
+            reinterpret_cast<uint4*>(stage + box * (64 * BK * 2))[i] = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(map_to(full(st), 0));
+      }
+      s = (s + blocks) % S;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // neither CTA leaves while the pair's MMAs or copies may touch it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols) : "memory");
+  }
+}
+
+// Joins the parts of a split sum, in order, and runs the epilogue.
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p) {
+  const int64_t per_row = (p.N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= per_row * p.M) return;
+  const int64_t row = i / per_row, c = (i - row * per_row) * 8;
+  float v[8] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.part + ((int64_t)s * p.M + row) * p.part_pitch + c);
+    float f[8];
+    u4_to_f4x2(src[0], src[1], f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += f[k];
+  }
+  const int n = (int)min((int64_t)8, p.N - c);
+  if (p.vec && n == 8) {
+    float b[8];
+    if (p.bias) {
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + c), b, p.bf16);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += b[k];
+    }
+    if (p.preact) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * p.N + c) = pack8(v, p.bf16);
+    activate8(v, p.act);
+    if (p.residual) {
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c), b, p.bf16);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += b[k];
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * p.N + c) = pack8(v, p.bf16);
+    return;
+  }
+  for (int k = 0; k < n; ++k) {
+    float z = v[k];
+    if (p.bias) z += ld16(p.bias, c + k, p.bf16);
+    if (p.preact) st16(p.preact, row * p.N + c + k, z, p.bf16);
+    z = activate<true>(z, p.act);
+    if (p.residual) z += ld16(p.residual, row * p.r_m + c + k, p.bf16);
+    st16(p.D, row * p.N + c + k, z, p.bf16);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t stride, int64_t batch_stride,
+                                                  uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols) {
+  const int64_t r = blockIdx.x, b = blockIdx.z;
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= pitch) return;
+  const uint16_t* s = src + b * batch_stride + r * stride + c;
+  uint16_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = c + i < cols ? s[i] : (uint16_t)0;
+  *reinterpret_cast<uint4*>(dst + (b * rows + r) * pitch + c) = *reinterpret_cast<const uint4*>(h);
+}
+
+int num_sms() {
+  static int n = [] {
+    int dev = 0, v = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    return v > 0 ? v : 152;
+  }();
+  return n;
+}
+
+bool aligned_rows(const void* p, int64_t stride) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+}
+
+template <bool AMN, bool BMN, int BN>
+cudaError_t run(const Product& p, const TcProduct& q, cudaStream_t s) {
+  auto fn = k_linear_tc<AMN, BMN, BN>;
+  static bool ready[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !ready[dev]) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<BN>::kTotal);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) ready[dev] = true;
+    }
+  }
+  const int type = q.bf16 ? NS_BF16 : NS_F16;
+  const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
+  CUtensorMap ma, mb;
+  e = AMN ? tc_encode_map(&ma, p.A, type, p.M, p.K, 1, p.a_k, p.K * p.a_k, 64, 64)
+          : tc_encode_map(&ma, p.A, type, p.K, p.M, 1, p.a_m, p.M * p.a_m, 64, 128);
+  if (e != cudaSuccess) return e;
+  const int64_t between = mats > 1 ? p.b_e : (BMN ? p.K * p.b_k : p.N * p.b_n);
+  e = BMN ? tc_encode_map(&mb, p.B, type, p.N, p.K, mats, p.b_k, between, 64, 64)
+          : tc_encode_map(&mb, p.B, type, p.K, p.N, mats, p.b_n, between, 64, BN / 2);
+  if (e != cudaSuccess) return e;
+  int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+  if (p.mode == GROUP_ROWS) tiles = (p.M / BM + (p.M < p.experts ? p.M : p.experts)) * q.tiles_n;  // at most
+  else tiles *= p.mode == GROUP_SUM ? p.experts : q.splits;
+  const int64_t pairs = tiles < 1 ? 1 : (tiles < num_sms() / 2 ? tiles : num_sms() / 2);
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)(2 * pairs));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = Smem<BN>::kTotal;
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, fn, ma, mb, q);
+}
+
+template <int BN>
+cudaError_t run_layout(const Product& p, const TcProduct& q, cudaStream_t s) {
+  if (p.a_k != 1) return run<true, true, BN>(p, q, s);
+  return p.b_k == 1 ? run<false, false, BN>(p, q, s) : run<false, true, BN>(p, q, s);
+}
+
+}  // namespace
+
+cudaError_t ops_error_word(int** err) {
+  static int* addr[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!addr[dev]) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_err);
+    if (e != cudaSuccess) return e;
+    addr[dev] = static_cast<int*>(p);
+  }
+  *err = addr[dev];
+  return cudaSuccess;
+}
+
+// Tile width and parts of the sum with the least estimated time: a block of 64
+// steps of the sum takes a pair about 0.27 us on a 256 x 256 tile and 0.15 us
+// on a 256 x 128 one, a tile's start and end about 1 us; parts cost a launch
+// and their traffic through L2 / HBM at about 5 TB/s.
+TilePlan tile_plan(const Product& p) {
+  const int64_t pairs = 76;
+  const int64_t kb = (p.K + BK - 1) / BK;
+  TilePlan best{256, 1, 0};
+  double best_t = 1e30;
+  for (int bn : {256, 128}) {
+    const int64_t tn = (p.N + bn - 1) / bn;
+    int64_t tiles = (p.M + BM - 1) / BM * tn;
+    double per_kb = bn == 256 ? 0.27 : 0.15, blocks = (double)kb;
+    if (p.mode == GROUP_ROWS) tiles = ((p.M + p.experts * (BM / 2)) / BM + 1) * tn;  // half a tile lost per range
+    if (p.mode == GROUP_SUM) { tiles *= p.experts; blocks = (double)kb / p.experts + 0.5; }
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (p.mode != GROUP_NONE || kb / s < 4)) break;
+      const double waves = (double)((tiles * s + pairs - 1) / pairs);
+      double t = waves * (blocks / s * per_kb + 1.0);
+      if (s > 1) t += 3.0 + (double)p.M * p.N * 8.0 * s / 5e6;
+      if (t < best_t) { best_t = t; best.bn = bn; best.splits = s; }
+    }
+  }
+  if (best.splits > 1) best.part_bytes = (int64_t)best.splits * p.M * ((p.N + 31) / 32 * 32) * 4;
+  return best;
+}
+
+cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, cudaStream_t s) {
+  TcProduct q{};
+  q.mode = p.mode; q.experts = p.experts; q.splits = t.splits; q.offsets = p.offsets;
+  q.M = (int)p.M; q.N = (int)p.N; q.K = (int)p.K;
+  q.tiles_m = (int)((p.M + BM - 1) / BM);
+  q.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
+  q.bf16 = p.dtype == DT_BF16;
+  q.act = p.act;
+  q.D = p.D; q.bias = p.bias; q.residual = p.residual; q.r_m = p.r_m; q.preact = p.preact;
+  q.vec = aligned_rows(p.D, p.N) && (!p.bias || aligned_rows(p.bias, p.N)) &&
+          (!p.residual || aligned_rows(p.residual, p.r_m)) && (!p.preact || aligned_rows(p.preact, p.N));
+  q.part = part;
+  q.part_pitch = (p.N + 31) / 32 * 32;
+  q.err = p.err;
+  cudaError_t e = t.bn == 256 ? run_layout<256>(p, q, s) : run_layout<128>(p, q, s);
+  if (e == cudaSuccess && t.splits > 1) {
+    const int64_t n = (p.N + 7) / 8 * p.M;
+    k_linear_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
+                            int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
+  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)batch);
+  k_pad_rows<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(src), stride, batch_stride,
+                                  static_cast<uint16_t*>(dst), pitch, rows, cols);
+  return cudaGetLastError();
+}
+
+}  // namespace muon

@@ -61,16 +61,6 @@ struct TcArgs {
   int* err;
 };
 
-// ---- TMA ----
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 template <int BN>
 struct TcSmem {
   static constexpr uint32_t kA = BM * BK * 2;          // 16 KB
@@ -446,58 +436,6 @@ struct TcSmem2 {
   static_assert(kTotal <= 227 * 1024, "pair GEMM shared memory exceeds the per-CTA limit");
 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The shared::cluster address of the same shared variable in CTA `rank`.
-__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// A tile copy whose completion is counted on an mbarrier that may sit in the
-// peer CTA of the pair (`mbar` a shared::cluster address).
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
-                                                 int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives once on the mbarrier at the same shared offset in every CTA of
-// `mask` when the MMAs this thread issued so far have completed.
-__device__ __forceinline__ void umma_commit_pair(uint32_t mbar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(mbar),
-      "h"(mask)
-      : "memory");
-}
-// Arrival of an epilogue warp on the leader's `tempty` barrier.  It only
-// hands the TMEM accumulator back: the tcgen05 fences around it order the
-// warp's tcgen05.ld reads before the leader's next MMAs, and the epilogue's
-// global stores need no ordering with it, so the arrival is relaxed (a
-// release at cluster scope would first wait for those stores to drain).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 template <typename TY, int OP>
 __global__ void __launch_bounds__(kThreads2, 1)
     k_tc_gemm2(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
@@ -680,22 +618,10 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// 3-D map over [B][rows][inner] (logical extents; pitch in elements), 128-byte
-// swizzle, zero fill outside the extents.
+// 3-D map over [B][rows][inner] with matrices back to back (tc_encode_map).
 cudaError_t make_map(CUtensorMap* m, const void* base, int ns_type, int64_t inner, int64_t rows,
                      int64_t B, int64_t pitch, uint32_t box0, uint32_t box1) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)B};
-  const cuuint64_t strides[2] = {(cuuint64_t)(pitch * 2), (cuuint64_t)(rows * pitch * 2)};
-  const cuuint32_t box[3] = {box0, box1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(m, ns_type == NS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                        3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return tc_encode_map(m, base, ns_type, inner, rows, B, pitch, rows * pitch, box0, box1);
 }
 
 template <int BN, int TM = BM>
@@ -802,6 +728,22 @@ int tc_bn_update(int64_t n) { return n >= 256 ? 256 : 128; }
 bool tc_pair(int64_t m) { return m >= 256; }
 
 }  // namespace
+
+cudaError_t tc_encode_map(CUtensorMap* m, const void* base, int ns_type, int64_t inner, int64_t rows,
+                          int64_t B, int64_t pitch, int64_t batch, uint32_t box0, uint32_t box1) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)B};
+  const cuuint64_t strides[2] = {(cuuint64_t)(pitch * 2), (cuuint64_t)(batch * 2)};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, ns_type == NS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 int32_t tc_tile_walk(int32_t op, int64_t m, int64_t n, int32_t bm, int32_t bn, int32_t* tm,
                      int32_t* tn, int32_t cap) {

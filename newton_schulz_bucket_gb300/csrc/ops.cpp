@@ -148,7 +148,7 @@ Product dx_product(const muon_linear_args* a, const void* dz, int64_t dz_stride)
 }
 
 // dw = x^T dz, or for OUT_IN its transpose dz^T x
-Product dw_product(const muon_linear_args* a, const void* dz, int64_t dz_stride) {
+Product dw_product(const muon_linear_args* a, const void* x, int64_t x_stride, const void* dz, int64_t dz_stride) {
   Product p{};
   p.dtype = a->dtype;
   p.mode = a->experts ? GROUP_SUM : GROUP_NONE;
@@ -158,19 +158,66 @@ Product dw_product(const muon_linear_args* a, const void* dz, int64_t dz_stride)
   const bool io = a->w_layout == MUON_W_IN_OUT;
   p.M = io ? a->in : a->out;
   p.N = io ? a->out : a->in;
-  p.A = io ? a->x : dz; p.a_m = 1; p.a_k = io ? a->x_stride : dz_stride;
-  p.B = io ? dz : a->x; p.b_k = io ? dz_stride : a->x_stride; p.b_n = 1;
+  p.A = io ? x : dz; p.a_m = 1; p.a_k = io ? x_stride : dz_stride;
+  p.B = io ? dz : x; p.b_k = io ? dz_stride : x_stride; p.b_n = 1;
   p.D = a->dw;
   return p;
 }
 
+// An operand of the tensor-core form: as it is where TMA can read it (base and
+// row pitch multiples of 16 bytes), else a copy with padded rows in scratch.
+// (r, c) strides of the operand are (stride, 1) over rows x cols, batch apart.
+struct Operand {
+  const void* p;
+  int64_t stride, batch_stride;
+};
+Operand tma_operand(Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch, cudaStream_t s,
+                    cudaError_t* e) {
+  const bool ok = (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
+                  (batch == 1 || o.batch_stride % 8 == 0);
+  if (ok) return o;
+  const int64_t pitch = (cols + 7) / 8 * 8;
+  void* dst = c.take((size_t)(batch * rows * pitch * 2));
+  if (launch && *e == cudaSuccess) *e = launch_pad_rows(o.p, o.stride, o.batch_stride, dst, pitch, rows, cols, batch, s);
+  return {dst, pitch, rows * pitch};
+}
+
+// One product: fp32 in FMA, 16-bit types on the tensor cores.
+cudaError_t run_product(Product p, Carve& c, bool launch, cudaStream_t s) {
+  if (p.dtype == DT_F32) return launch ? launch_linear_simt(p, s) : cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  const bool a_along = p.a_k == 1, b_along = p.b_k == 1;
+  const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
+  const Operand a = tma_operand({p.A, a_along ? p.a_m : p.a_k, 0}, a_along ? p.M : p.K, a_along ? p.K : p.M, 1, c,
+                                launch, s, &e);
+  const Operand b = tma_operand({p.B, b_along ? p.b_n : p.b_k, p.b_e}, b_along ? p.N : p.K, b_along ? p.K : p.N, mats,
+                                c, launch, s, &e);
+  p.A = a.p;
+  (a_along ? p.a_m : p.a_k) = a.stride;
+  p.B = b.p;
+  (b_along ? p.b_n : p.b_k) = b.stride;
+  p.b_e = b.batch_stride;
+  const TilePlan t = tile_plan(p);
+  float* part = t.part_bytes ? static_cast<float*>(c.take((size_t)t.part_bytes)) : nullptr;
+  if (!launch || e != cudaSuccess) return e;
+  e = ops_error_word(&p.err);
+  return e == cudaSuccess ? launch_linear_tc(p, t, part, s) : e;
+}
+
 muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, bool launch, cudaStream_t s) {
   if (!backward) {
-    if (!launch || a->rows == 0) return MUON_OK;
-    return cuda_status("muon_linear", launch_linear_simt(forward_product(a), s));
+    if (a->rows == 0) return MUON_OK;
+    return cuda_status("muon_linear", run_product(forward_product(a), c, launch, s));
   }
+  const char* what = "muon_linear_backward";
   const int64_t b = dtype_size(a->dtype);
   const int64_t mats = a->experts ? a->experts : 1;
+  if (a->rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (launch && a->dw) e = cudaMemsetAsync(a->dw, 0, (size_t)(mats * a->in * a->out * b), s);
+    if (launch && a->db && e == cudaSuccess) e = cudaMemsetAsync(a->db, 0, (size_t)(mats * a->out * b), s);
+    return cuda_status(what, e);
+  }
   const bool act = a->activation != ACT_NONE, products = a->dx || a->dw;
   GradPrep g{};
   g.dtype = a->dtype; g.act = a->activation; g.experts = a->experts; g.offsets = a->offsets;
@@ -181,20 +228,17 @@ muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, boo
   if (act && products) g.dz = c.take((size_t)(a->rows * g.dz_stride * b));
   if (a->db)
     g.part = static_cast<float*>(c.take(((a->rows + kGradChunk - 1) / kGradChunk + mats) * a->out * sizeof(float)));
-  if (!launch) return MUON_OK;
-  if (a->rows == 0) {
-    cudaError_t e = cudaSuccess;
-    if (a->dw) e = cudaMemsetAsync(a->dw, 0, (size_t)(mats * a->in * a->out * b), s);
-    if (a->db && e == cudaSuccess) e = cudaMemsetAsync(a->db, 0, (size_t)(mats * a->out * b), s);
-    return cuda_status("muon_linear_backward", e);
-  }
   cudaError_t e = cudaSuccess;
-  if (act || a->db) e = launch_grad_prep(g, s);
-  const void* dz = act ? g.dz : a->dy;
-  const int64_t dz_stride = act ? g.dz_stride : a->dy_stride;
-  if (a->dx && e == cudaSuccess) e = launch_linear_simt(dx_product(a, dz, dz_stride), s);
-  if (a->dw && e == cudaSuccess) e = launch_linear_simt(dw_product(a, dz, dz_stride), s);
-  return cuda_status("muon_linear_backward", e);
+  if (launch && (act || a->db)) e = launch_grad_prep(g, s);
+  Operand dz{act ? g.dz : a->dy, act ? g.dz_stride : a->dy_stride, 0};
+  Operand x{a->x, a->x_stride, 0};
+  if (a->dtype != DT_F32) {  // padded once for both products
+    if (products) dz = tma_operand(dz, a->rows, a->out, 1, c, launch, s, &e);
+    if (a->dw) x = tma_operand(x, a->rows, a->in, 1, c, launch, s, &e);
+  }
+  if (a->dx && e == cudaSuccess) e = run_product(dx_product(a, dz.p, dz.stride), c, launch, s);
+  if (a->dw && e == cudaSuccess) e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), c, launch, s);
+  return cuda_status(what, e);
 }
 
 muon_status_t linear_entry(const muon_linear_args* a, bool backward, void* stream) {
@@ -387,8 +431,15 @@ muon_status_t muon_combine_backward(int32_t dtype, int64_t tokens, int64_t hidde
 }
 
 muon_status_t muon_ops_check_error(void) {
-  const cudaError_t e = cudaDeviceSynchronize();
-  return cuda_status("muon_ops_check_error", e);
+  const char* what = "muon_ops_check_error";
+  int* err = nullptr;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = ops_error_word(&err);
+  int word = 0;
+  if (e == cudaSuccess) e = cudaMemcpy(&word, err, sizeof word, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && word) e = cudaMemset(err, 0, sizeof word);
+  if (e != cudaSuccess) return cuda_status(what, e);
+  return word ? fail(MUON_ERR_TIMEOUT, "%s: a bounded wait ran out in an earlier call (code %d)", what, word) : MUON_OK;
 }
 
 }  // extern "C"

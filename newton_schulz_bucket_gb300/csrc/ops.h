@@ -56,6 +56,19 @@ struct GradPrep {
   void* db;                    // [ranges][cols]
 };
 
+// How the tensor-core form runs a product (chosen on the host from sizes).
+struct TilePlan {
+  int bn;                      // columns of a pair's tile: 256 or 128
+  int splits;                  // parts of the sum (GROUP_NONE), joined by a second kernel
+  int64_t part_bytes;          // scratch of the parts
+};
+TilePlan tile_plan(const Product& p);
+cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, cudaStream_t s);
+// 16-bit rows copied to a pitch that TMA can read: rows of every matrix.
+cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
+                            int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
+cudaError_t ops_error_word(int** err);  // device address of the error word of the current device
+
 constexpr int kGradChunk = 128;  // rows of one partial column sum
 
 cudaError_t launch_linear_simt(const Product& p, cudaStream_t s);
