@@ -1,26 +1,34 @@
 // A layer's product on the tensor cores: D(m, n) = act(sum_k A(m, k) B(k, n) +
 // bias) + residual in fp16 / bf16 operands with fp32 sums.
 //
-// A cluster of two CTAs computes one 256 x BN tile with tcgen05.mma
+// A cluster of two CTAs computes one 256 x N tile (N <= 256) with tcgen05.mma
 // cta_group::2, as the Newton-Schulz products do: each CTA stages its 128 rows
-// of A and its half of B's columns in a ring of TMA tiles, the leader issues the
-// MMAs, and both hold 128 rows of the accumulator in TMEM (two accumulators,
-// so that the epilogue of one tile runs under the products of the next).
-// Either operand may be stored along k or across it; the three layouts that a
-// layer needs are instantiated: y = x W and dx = dz W^T read A along k, dw =
-// x^T dz reads both across k, so no operand is ever transposed in memory.
+// of the M operand and its half of the N operand's rows in a ring of TMA tiles,
+// the leader issues the MMAs, and both hold 128 rows of the accumulator in
+// TMEM (two accumulators, so that the epilogue of one tile runs under the
+// products of the next).  Operands may be stored along the sum or across it, so
+// none is ever transposed in memory.
+//
+// Rows form (y = x W, dx = dz W^T).  The weight matrix is the M operand and
+// the token rows are the N operand, i.e. a tile is 256 features x N tokens.  N
+// is chosen per tile from the rows there are, in steps of 32: a single token
+// streams the weights through 32-column MMAs, and an expert with 257 rows costs
+// two tiles of 160 and 128 columns, not two of 256.  An accumulator lane is a
+// feature, so a warp's stores run along a token's row for any width and
+// alignment.
+//
+// Sum form (dw = x^T dz).  Both operands are stored across the sum (tokens);
+// tiles are 256 x 256 or 256 x 128.  Output blocks go through a swizzled
+// staging block so that stores are 16 bytes a lane along rows.
 //
 // Experts.  Row ranges come from a device array, so every role walks the
 // ranges itself.  GROUP_ROWS: an expert's rows are tiled from its first row;
-// rows past its end are loaded (they are the next expert's) and not stored.
-// GROUP_SUM: the sum over an expert's rows ends inside a 64-row block of the
-// ring, whose other rows belong to the next expert, and may hold NaN there: a
-// helper warp overwrites them in shared memory with zeros, in both operands,
-// before the block is handed to the MMAs.
-//
-// Epilogue: eight warps, 32 x 32 blocks through a swizzled staging block so
-// that global accesses run along rows (16 bytes a lane, or one element a lane
-// where rows are not 16-byte aligned).
+// rows past its end are loaded (they are the next expert's), multiplied into
+// accumulator columns of their own, and not stored.  GROUP_SUM: the sum over an
+// expert's rows ends inside a 64-row block of the ring, whose other rows belong
+// to the next expert, and may hold NaN there: a helper warp overwrites them in
+// shared memory with zeros, in both operands, before the block is handed to
+// the MMAs.
 #include <cuda.h>
 
 #include <mutex>
@@ -34,7 +42,7 @@ namespace muon {
 
 namespace {
 
-constexpr int BM = 256;     // rows of a pair's tile
+constexpr int BM = 256;     // features (rows form) or output rows (sum form) of a pair's tile
 constexpr int BK = 64;      // one 128-byte swizzle row of k
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, epilogue, range-tail helper
@@ -44,28 +52,31 @@ __device__ int g_err;       // the operators' error word (one per device)
 struct TcProduct {
   int mode, experts, splits;
   const int32_t* offsets;
-  int M, N, K;
-  int tiles_m, tiles_n;     // of the whole output (GROUP_ROWS: tiles_n only)
-  int bf16, act, vec;       // vec: rows of every epilogue tensor start on 16 bytes
-  void* D;
+  int rows, K;              // rows form: token rows; the sum's length (GROUP_SUM: all rows)
+  int M, N;                 // rows form: features (M); sum form: the output
+  int tiles_m, tiles_n;     // sum form; rows form: feature tiles (tiles_m)
+  int box_rows;             // rows form: token rows of one TMA copy
+  int bf16, act, vec;       // vec (sum form): output rows start on 16 bytes
+  void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert
   const void* bias;
   const void* residual;
   int64_t r_m;
   void* preact;
-  float* part;              // splits > 1: [splits][M][part_pitch] sums
+  float* part;              // splits > 1: [splits][output rows][part_pitch] sums
   int64_t part_pitch;
   int* err;
 };
 
+// Ring and staging of one CTA.  Rows form: BN = 0.
 template <int BN>
 struct Smem {
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kStages = BN == 0 ? 7 : (BN == 256 ? 6 : 8);
   static constexpr uint32_t kA = 128 * BK * 2;
-  static constexpr uint32_t kB = BN / 2 * BK * 2;
+  static constexpr uint32_t kB = (BN == 0 ? 128 : BN / 2) * BK * 2;
   static constexpr uint32_t kStage = kA + kB;
   static constexpr uint32_t kBars = kStages * kStage;  // full, empty, fix, tfull, tempty, done; TMEM slot, abort
   static constexpr uint32_t kEpi = kBars + 256;
-  static constexpr uint32_t kTotal = kEpi + kEpiWarps * 4096 + 1024;  // + alignment slack
+  static constexpr uint32_t kTotal = kEpi + (BN == 0 ? 0 : kEpiWarps * 4096) + 1024;  // + alignment slack
   static_assert((3 * kStages + 5) * 8 + 8 <= 256 && kTotal <= 227 * 1024, "shared memory layout");
 };
 
@@ -78,11 +89,17 @@ __device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
   return v < 0 ? 0 : (v > hi ? hi : v);
 }
 
-// One output tile's work: rows m0 .. m_end - 1 (256 at most), columns n0 ..,
-// sum over k0 .. k1 - 1.
+// One tile's work.  Rows form: features m0 .., token rows n0 .. n_end - 1 (256
+// at most).  Sum form: output rows m0 .., columns n0 ...  Sum over k0 .. k1 - 1.
 struct Item {
-  int e, m0, m_end, n0, k0, k1, split;
+  int e, m0, n0, n_end, k0, k1, split;
 };
+
+// Token tiles of a range of n rows: as few as 256 allows, of even size in
+// steps of 32 (n > 256 (tiles - 1) >= size (tiles - 1), so none is empty).
+__device__ __forceinline__ int token_tile(int n, int tiles) { return ((n + tiles - 1) / tiles + 31) / 32 * 32; }
+// Columns of a tile's MMA.
+__device__ __forceinline__ int mma_cols(const Item& it) { return (it.n_end - it.n0 + 31) / 32 * 32; }
 
 // 8 tile rows share a sweep over the tile columns, so that the tiles in
 // flight reuse a compact set of panels through L2.
@@ -99,46 +116,51 @@ __device__ __forceinline__ void raster(int r, int tiles_m, int tiles_n, int& tm,
 template <int BN>
 struct Walk {
   int t, step;
-  int e, lo, hi, base, cnt;  // current range, its first tile and tile count
+  int e, lo, hi, base, cnt, tt;  // current range, its first item, item and token tile counts
   __device__ __forceinline__ Walk(const TcProduct& p)
-      : t(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), base(0), cnt(0) {}
+      : t(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), base(0), cnt(0), tt(0) {}
+  __device__ __forceinline__ void part_of_sum(const TcProduct& p, int split, Item& it) {
+    const int kb = (p.K + BK - 1) / BK;
+    it.split = split;
+    it.k0 = (int)((int64_t)kb * split / p.splits) * BK;
+    it.k1 = split + 1 == p.splits ? p.K : (int)((int64_t)kb * (split + 1) / p.splits) * BK;
+  }
   __device__ __forceinline__ bool next(const TcProduct& p, Item& it) {
     int tm, tn;
-    it.split = 0;
-    if (p.mode == GROUP_ROWS) {
+    if constexpr (BN == 0) {
       while (t >= base + cnt) {
         base += cnt;
-        if (++e >= p.experts) return false;
-        lo = range_at(p, e, p.M);
-        hi = range_at(p, e + 1, p.M);
-        cnt = hi > lo ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
+        if (++e >= (p.mode == GROUP_ROWS ? p.experts : 1)) return false;
+        lo = p.mode == GROUP_ROWS ? range_at(p, e, p.rows) : 0;
+        hi = p.mode == GROUP_ROWS ? range_at(p, e + 1, p.rows) : p.rows;
+        tt = hi > lo ? (hi - lo + 255) / 256 : 0;
+        cnt = tt * p.tiles_m * p.splits;
       }
-      raster(t - base, (hi - lo + BM - 1) / BM, p.tiles_n, tm, tn);
+      const int per = tt * p.tiles_m, g = (t - base) / per;
+      raster(t - base - g * per, p.tiles_m, tt, tm, tn);
+      const int size = token_tile(hi - lo, tt);
       it.e = e;
-      it.m0 = lo + tm * BM;
-      it.m_end = hi;
-      it.k0 = 0;
-      it.k1 = p.K;
+      it.m0 = tm * BM;
+      it.n0 = lo + tn * size;
+      it.n_end = min(hi, it.n0 + size);
+      part_of_sum(p, g, it);
     } else {
-      const int per = p.tiles_m * p.tiles_n;
-      const int g = t / per;
+      const int per = p.tiles_m * p.tiles_n, g = t / per;
       if (g >= (p.mode == GROUP_SUM ? p.experts : p.splits)) return false;
       raster(t - g * per, p.tiles_m, p.tiles_n, tm, tn);
       it.m0 = tm * BM;
-      it.m_end = p.M;
+      it.n0 = tn * BN;
+      it.n_end = p.N;
       if (p.mode == GROUP_SUM) {
         it.e = g;
+        it.split = 0;
         it.k0 = range_at(p, g, p.K);
         it.k1 = max(it.k0, range_at(p, g + 1, p.K));
       } else {
         it.e = 0;
-        it.split = g;
-        const int kb = (p.K + BK - 1) / BK;
-        it.k0 = (int)((int64_t)kb * g / p.splits) * BK;
-        it.k1 = g + 1 == p.splits ? p.K : (int)((int64_t)kb * (g + 1) / p.splits) * BK;
+        part_of_sum(p, g, it);
       }
     }
-    it.n0 = tn * BN;
     t += step;
     return true;
   }
@@ -173,25 +195,56 @@ __device__ __forceinline__ uint4 pack8(const float* f, int bf16) {
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
   return u;
 }
-__device__ __forceinline__ void activate8(float* v, int act) {
-  switch (act) {
+template <int N>
+__device__ __forceinline__ void activate_n(float* v, int act) {
+  switch (act) {  // outside the loop over values
     case ACT_NONE: break;
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_RELU);
+      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_RELU);
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_SILU);
+      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_SILU);
       break;
     case ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_GELU);
+      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_GELU);
       break;
     default:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activate<true>(v[i], ACT_GELU_TANH);
+      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_GELU_TANH);
   }
+}
+
+// Rows form, one warp: feature f (this lane's) of tokens t0 .. t0 + n - 1 (n
+// <= 32) from 32 accumulator columns.  Each store covers 32 features of one
+// token's row.
+template <typename T>
+__device__ __forceinline__ void write_tokens(const TcProduct& p, float* v, int e, int64_t f, int64_t t0, int n) {
+  const int64_t at = t0 * p.M + f;
+  if (p.bias) {
+    const float b = to_f32(static_cast<const T*>(p.bias)[e * (int64_t)p.M + f]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += b;
+  }
+  if (p.preact) {
+    T* z = static_cast<T*>(p.preact) + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) z[(int64_t)i * p.M] = from_f32<T>(v[i]);
+  }
+  activate_n<32>(v, p.act);
+  if (p.residual) {
+    const T* r = static_cast<const T*>(p.residual) + t0 * p.r_m + f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) v[i] += to_f32(r[i * p.r_m]);
+  }
+  T* y = static_cast<T*>(p.D) + at;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < n) y[(int64_t)i * p.M] = from_f32<T>(v[i]);
 }
 
 // A warp's 32 x 32 block from TMEM into its staging block, row = lane, the
@@ -208,59 +261,26 @@ __device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane,
   __syncwarp();
 }
 
-// Rows row0 .. row0 + 31 (those < m_end) and columns col0 .. col0 + 31 (those
-// < N) of the output from the staging block.
-__device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int e, int row0,
-                                            int m_end, int col0, int64_t d_base) {
+// Sum form: rows row0 .. row0 + 31 (those < M) and columns col0 .. col0 + 31
+// (those < N) of the output from the staging block.
+__device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int row0, int col0,
+                                            int64_t d_base) {
   const int64_t N = p.N;
   if (p.vec && col0 + 32 <= p.N) {
     const int q = lane & 3, c = col0 + q * 8;
-    float b[8];
-    if (p.bias) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + e * N + c)), b, p.bf16);
-    }
-    uint4 res[4];
-    if (p.residual) {
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int row = row0 + it * 8 + (lane >> 2);
-        if (row < m_end)
-          res[it] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c);
-      }
-    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int rr = it * 8 + (lane >> 2), row = row0 + rr;
       const uint4* src = reinterpret_cast<const uint4*>(sw + rr * 32);
       float v[8];
       u4_to_f4x2(src[(2 * q) ^ (rr & 7)], src[(2 * q + 1) ^ (rr & 7)], v);
-      if (row >= m_end) continue;
-      if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += b[i];
-      }
-      if (p.preact)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * N + c) = pack8(v, p.bf16);
-      activate8(v, p.act);
-      if (p.residual) {
-        float r[8];
-        unpack8(res[it], r, p.bf16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + d_base + row * N + c) = pack8(v, p.bf16);
+      if (row < p.M)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + d_base + row * N + c) = pack8(v, p.bf16);
     }
   } else if (col0 + lane < p.N) {
     const int c = col0 + lane;
-    const float b = p.bias ? ld16(p.bias, e * N + c, p.bf16) : 0.f;
-    for (int rr = 0; rr < 32 && row0 + rr < m_end; ++rr) {
-      const int64_t row = row0 + rr;
-      float v = sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)] + b;
-      if (p.preact) st16(p.preact, row * N + c, v, p.bf16);
-      v = activate<true>(v, p.act);
-      if (p.residual) v += ld16(p.residual, row * p.r_m + c, p.bf16);
-      st16(p.D, d_base + row * N + c, v, p.bf16);
-    }
+    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
+      st16(p.D, d_base + (row0 + rr) * N + c, sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)], p.bf16);
   }
   __syncwarp();  // the block is overwritten next
 }
@@ -290,7 +310,8 @@ __device__ void zero_span(void* base, int64_t from, int64_t to, int64_t tid, int
   for (int64_t i = from + v * 8 + tid; i < to; i += n_threads) p[i] = 0;
 }
 
-template <bool AMN, bool BMN, int BN>
+// BN = 0: rows form (M operand stored across the sum if AMN); else sum form.
+template <bool AMN, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ TcProduct p) {
@@ -310,8 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull = [&](int a) { return bar0 + 8u * (3 * S + a); };
   auto tempty = [&](int a) { return bar0 + 8u * (3 * S + 2 + a); };
   const uint32_t done = bar0 + 8u * (3 * S + 4);
-  constexpr uint32_t kCols = 2 * BN;  // two accumulators
-  const bool group_sum = p.mode == GROUP_SUM;
+  constexpr bool kRows = BN == 0;
+  constexpr int kAccCols = kRows ? 256 : BN;
+  constexpr uint32_t kCols = 2 * kAccCols;  // two accumulators
+  const bool group_sum = !kRows && p.mode == GROUP_SUM;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -346,8 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       while (ok && walk.next(p, it)) {
-        const int arow = it.m0 + (int)rank * 128, bcol = it.n0 + (int)rank * (BN / 2);
-        const int be = p.mode == GROUP_ROWS ? it.e : 0;
+        const int arow = it.m0 + (int)rank * 128;
+        // rows form: this CTA's half of the tile's tokens, in boxes of box_rows
+        const int half = kRows ? mma_cols(it) / 2 : BN / 2;
+        const int brow = it.n0 + (int)rank * half;
+        const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
+        const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
         for (int k = it.k0; k < it.k1; k += BK) {
           if (!(ok = mbar_wait(empty(s), ph ^ 1, abort_flag, p.err, 1))) break;
           const uint32_t sa = saddr(smem + s * L::kStage), sb = sa + L::kA;
@@ -355,24 +382,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t bar;  // where this CTA's copies are counted: the leader's ring, or its own helper
           if (tail) {
             bar = fix(s);
-            mbar_expect_tx(bar, L::kStage);
+            mbar_expect_tx(bar, bytes);
           } else {
             bar = map_to(full(s), 0);
-            if (rank == 0) mbar_expect_tx(full(s), 2 * L::kStage);
+            if (rank == 0) mbar_expect_tx(full(s), 2 * bytes);
             else if (group_sum) mbar_arrive_cluster(bar);
           }
           if (AMN) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tma_load_3d_pair(sa + c * (64 * BK * 2), &mapA, bar, arow + c * 64, k, 0);
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d_pair(sa + c * (64 * BK * 2), &mapA, bar, arow + c * 64, k, kRows ? it.e : 0);
           } else {
-            tma_load_3d_pair(sa, &mapA, bar, k, arow, 0);
+            tma_load_3d_pair(sa, &mapA, bar, k, arow, it.e);
           }
-          if (BMN) {
+          if constexpr (kRows) {
+            for (int c = 0; c < boxes; ++c)
+              tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, 0);
+          } else {
 #pragma unroll
             for (int c = 0; c < BN / 128; ++c)
-              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, bcol + c * 64, k, be);
-          } else {
-            tma_load_3d_pair(sb, &mapB, bar, k, bcol, be);
+              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, 0);
           }
           if (++s == S) { s = 0; ph ^= 1; }
         }
@@ -384,14 +413,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {  // ---- MMA issuer (leader only) ----
-      const uint32_t idesc = instr_desc(p.bf16 ? 1u : 0u, BM, BN, BMN, AMN);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       while (ok && walk.next(p, it)) {
         if (!(ok = mbar_wait(tempty(acc), aph ^ 1, abort_flag, p.err, 2))) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
+        const uint32_t idesc = instr_desc(p.bf16 ? 1u : 0u, BM, kRows ? mma_cols(it) : BN, !kRows, AMN);
         for (int k = it.k0; k < it.k1; k += BK) {
           if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
           tc_fence_after();
@@ -399,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = AMN ? smem_desc(sa + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sa + kk * 32, 16, 1024);
-            const uint64_t bd = BMN ? smem_desc(sb + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sb + kk * 32, 16, 1024);
+            const uint64_t bd = !kRows ? smem_desc(sb + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sb + kk * 32, 16, 1024);
             umma_pair(d_tmem, ad, bd, idesc, k != it.k0 || kk != 0);
           }
           umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
@@ -418,22 +447,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 2 + kEpiWarps) {  // ---- epilogue ----
     const int quarter = warp & 3;     // TMEM lanes this warp may read
     const int half = (warp - 2) >> 2; // which half of the tile's columns
-    float* sw = reinterpret_cast<float*>(smem + L::kEpi) + (warp - 2) * 1024;
     int acc = 0;
     uint32_t aph = 0;
     while (walk.next(p, it)) {
       if (!mbar_wait(tfull(acc), aph, abort_flag, p.err, 8)) break;
       tc_fence_after();
+      const uint32_t tacc = tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(quarter * 32) << 16);
       const int row0 = it.m0 + (int)rank * 128 + quarter * 32;
-      const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
+      if constexpr (kRows) {
+        // the warps of a quarter take turns at 32 tokens
+        for (int c = half * 32; row0 < p.M && it.n0 + c < it.n_end; c += 64) {
+          float v[32];
+          __syncwarp();  // lanes without a feature skip the rest of the loop
+          tmem_ld32(tacc + (uint32_t)c, reinterpret_cast<uint32_t*>(v));
+          const int n = min(32, it.n_end - it.n0 - c), f = row0 + lane;
+          const int64_t t0 = it.n0 + c;
+          if (f >= p.M) continue;
+          if (p.splits > 1) {
+            float* dst = p.part + ((int64_t)it.split * p.rows + t0) * p.part_pitch + f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < n) dst[i * p.part_pitch] = v[i];
+          } else if (p.bf16) {
+            write_tokens<__nv_bfloat16>(p, v, it.e, f, t0, n);
+          } else {
+            write_tokens<__half>(p, v, it.e, f, t0, n);
+          }
+        }
+      } else {
+        float* sw = reinterpret_cast<float*>(smem + L::kEpi) + (warp - 2) * 1024;
+        const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
 #pragma unroll 1
-      for (int ch = half * (BN / 64); ch < (half + 1) * (BN / 64); ++ch) {
-        const int col0 = it.n0 + ch * 32;
-        if (col0 >= p.N || row0 >= it.m_end) break;  // the same for the whole warp
-        stage_block(tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(ch * 32), sw,
-                    lane, it.k0 >= it.k1);
-        if (p.splits > 1) write_part(p, sw, lane, row0, col0, it.split);
-        else write_block(p, sw, lane, it.e, row0, it.m_end, col0, d_base);
+        for (int ch = half * (BN / 64); ch < (half + 1) * (BN / 64); ++ch) {
+          const int col0 = it.n0 + ch * 32;
+          if (col0 >= p.N || row0 >= p.M) break;  // the same for the whole warp
+          stage_block(tacc + (uint32_t)(ch * 32), sw, lane, it.k0 >= it.k1);
+          if (p.splits > 1) write_part(p, sw, lane, row0, col0, it.split);
+          else write_block(p, sw, lane, row0, col0, d_base);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -441,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++acc == 2) { acc = 0; aph ^= 1; }
     }
     if (p.mode == GROUP_ROWS) {  // rows of no expert
-      const int64_t from = (int64_t)range_at(p, p.experts, p.M) * p.N, to = (int64_t)p.M * p.N;
+      const int64_t from = (int64_t)range_at(p, p.experts, p.rows) * p.M, to = (int64_t)p.rows * p.M;
       const int64_t tid = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 64;
       const int64_t n_threads = (int64_t)gridDim.x * (32 * kEpiWarps);
       zero_span(p.D, from, to, tid, n_threads);
@@ -477,45 +528,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of a split sum, in order, and runs the epilogue.
-__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p) {
-  const int64_t per_row = (p.N + 7) / 8;
+// Joins the parts of a split sum, in order, and runs the epilogue: output
+// [rows][cols], 8 columns a thread.  Row ranges: a row's expert by bisection.
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p, int rows, int cols) {
+  const int64_t per_row = (cols + 7) / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= per_row * p.M) return;
+  if (i >= per_row * rows) return;
   const int64_t row = i / per_row, c = (i - row * per_row) * 8;
+  int e = 0;
+  if (p.mode == GROUP_ROWS) {
+    if (row >= range_at(p, p.experts, rows)) return;  // of no expert: cleared by the product's kernel
+    int a = 0, b = p.experts;  // offsets[a] <= row < offsets[b]
+    while (b - a > 1) {
+      const int m = (a + b) / 2;
+      if (range_at(p, m, rows) <= row) a = m;
+      else b = m;
+    }
+    e = a;
+  }
   float v[8] = {};
   for (int s = 0; s < p.splits; ++s) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.part + ((int64_t)s * p.M + row) * p.part_pitch + c);
+    const uint4* src = reinterpret_cast<const uint4*>(p.part + ((int64_t)s * rows + row) * p.part_pitch + c);
     float f[8];
     u4_to_f4x2(src[0], src[1], f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] += f[k];
   }
-  const int n = (int)min((int64_t)8, p.N - c);
+  const int n = (int)min((int64_t)8, cols - c);
+  const int64_t bi = (int64_t)e * cols + c;
   if (p.vec && n == 8) {
     float b[8];
     if (p.bias) {
-      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + c), b, p.bf16);
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + bi), b, p.bf16);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    if (p.preact) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * p.N + c) = pack8(v, p.bf16);
-    activate8(v, p.act);
+    if (p.preact) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * cols + c) = pack8(v, p.bf16);
+    activate_n<8>(v, p.act);
     if (p.residual) {
       unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c), b, p.bf16);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * p.N + c) = pack8(v, p.bf16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * cols + c) = pack8(v, p.bf16);
     return;
   }
   for (int k = 0; k < n; ++k) {
     float z = v[k];
-    if (p.bias) z += ld16(p.bias, c + k, p.bf16);
-    if (p.preact) st16(p.preact, row * p.N + c + k, z, p.bf16);
+    if (p.bias) z += ld16(p.bias, bi + k, p.bf16);
+    if (p.preact) st16(p.preact, row * cols + c + k, z, p.bf16);
     z = activate<true>(z, p.act);
     if (p.residual) z += ld16(p.residual, row * p.r_m + c + k, p.bf16);
-    st16(p.D, row * p.N + c + k, z, p.bf16);
+    st16(p.D, row * cols + c + k, z, p.bf16);
   }
 }
 
@@ -545,9 +609,10 @@ bool aligned_rows(const void* p, int64_t stride) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
 }
 
-template <bool AMN, bool BMN, int BN>
-cudaError_t run(const Product& p, const TcProduct& q, cudaStream_t s) {
-  auto fn = k_linear_tc<AMN, BMN, BN>;
+// The kernel with its function attributes set (once per device).
+template <bool AMN, int BN>
+cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcProduct& q, int64_t items, cudaStream_t s) {
+  auto fn = k_linear_tc<AMN, BN>;
   static bool ready[64] = {};
   static std::mutex mu;
   int dev = 0;
@@ -561,22 +626,9 @@ cudaError_t run(const Product& p, const TcProduct& q, cudaStream_t s) {
       if (dev < 64) ready[dev] = true;
     }
   }
-  const int type = q.bf16 ? NS_BF16 : NS_F16;
-  const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
-  CUtensorMap ma, mb;
-  e = AMN ? tc_encode_map(&ma, p.A, type, p.M, p.K, 1, p.a_k, p.K * p.a_k, 64, 64)
-          : tc_encode_map(&ma, p.A, type, p.K, p.M, 1, p.a_m, p.M * p.a_m, 64, 128);
-  if (e != cudaSuccess) return e;
-  const int64_t between = mats > 1 ? p.b_e : (BMN ? p.K * p.b_k : p.N * p.b_n);
-  e = BMN ? tc_encode_map(&mb, p.B, type, p.N, p.K, mats, p.b_k, between, 64, 64)
-          : tc_encode_map(&mb, p.B, type, p.K, p.N, mats, p.b_n, between, 64, BN / 2);
-  if (e != cudaSuccess) return e;
-  int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-  if (p.mode == GROUP_ROWS) tiles = (p.M / BM + (p.M < p.experts ? p.M : p.experts)) * q.tiles_n;  // at most
-  else tiles *= p.mode == GROUP_SUM ? p.experts : q.splits;
-  const int64_t pairs = tiles < 1 ? 1 : (tiles < num_sms() / 2 ? tiles : num_sms() / 2);
+  const int64_t most = num_sms() / 2;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)(2 * pairs));
+  lc.gridDim = dim3((unsigned)(2 * (items < 1 ? 1 : (items < most ? items : most))));
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = Smem<BN>::kTotal;
   lc.stream = s;
@@ -590,11 +642,37 @@ cudaError_t run(const Product& p, const TcProduct& q, cudaStream_t s) {
   return cudaLaunchKernelEx(&lc, fn, ma, mb, q);
 }
 
-template <int BN>
-cudaError_t run_layout(const Product& p, const TcProduct& q, cudaStream_t s) {
-  if (p.a_k != 1) return run<true, true, BN>(p, q, s);
-  return p.b_k == 1 ? run<false, false, BN>(p, q, s) : run<false, true, BN>(p, q, s);
+// Rows form of D[p.M rows][p.N features]: M operand p.B (the weights).
+cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
+  const int type = q.bf16 ? NS_BF16 : NS_F16;
+  const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
+  const bool across = p.b_k != 1;  // weights stored across the sum
+  const int64_t between = mats > 1 ? p.b_e : (across ? p.K * p.b_k : p.N * p.b_n);
+  CUtensorMap mw, mx;
+  cudaError_t e = across ? tc_encode_map(&mw, p.B, type, p.N, p.K, mats, p.b_k, between, 64, 64)
+                         : tc_encode_map(&mw, p.B, type, p.K, p.N, mats, p.b_n, between, 64, 128);
+  if (e == cudaSuccess)
+    e = tc_encode_map(&mx, p.A, type, p.K, p.M, 1, p.a_m, p.M * p.a_m, 64, (uint32_t)q.box_rows);
+  if (e != cudaSuccess) return e;
+  int64_t tt = (p.M + 255) / 256;
+  if (p.mode == GROUP_ROWS) tt = p.M / 256 + (p.M < p.experts ? p.M : p.experts);  // at most
+  const int64_t items = tt * q.tiles_m * q.splits;
+  return across ? launch<true, 0>(mw, mx, q, items, s) : launch<false, 0>(mw, mx, q, items, s);
 }
+
+template <int BN>
+cudaError_t run_sum(const Product& p, const TcProduct& q, cudaStream_t s) {
+  const int type = q.bf16 ? NS_BF16 : NS_F16;
+  CUtensorMap ma, mb;
+  cudaError_t e = tc_encode_map(&ma, p.A, type, p.M, p.K, 1, p.a_k, p.K * p.a_k, 64, 64);
+  if (e == cudaSuccess) e = tc_encode_map(&mb, p.B, type, p.N, p.K, 1, p.b_k, p.K * p.b_k, 64, 64);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)q.tiles_m * q.tiles_n * (p.mode == GROUP_SUM ? p.experts : q.splits);
+  return launch<true, BN>(ma, mb, q, items, s);
+}
+
+// y and dx sum along the rows of A; dw sums across them.
+bool rows_form(const Product& p) { return p.a_k == 1; }
 
 }  // namespace
 
@@ -616,27 +694,41 @@ cudaError_t ops_error_word(int** err) {
   return cudaSuccess;
 }
 
-// Tile width and parts of the sum with the least estimated time: a block of 64
-// steps of the sum takes a pair about 0.27 us on a 256 x 256 tile and 0.15 us
-// on a 256 x 128 one, a tile's start and end about 1 us; parts cost a launch
-// and their traffic through L2 / HBM at about 5 TB/s.
+// Tile width (sum form) and parts of the sum with the least estimated time: a
+// block of 64 steps of the sum takes a pair about 0.27 us on a 256 x 256 tile
+// (0.15 us on 256 x 128, in proportion for fewer tokens, at least the 0.1 us in
+// which its weights arrive), a tile's start and end about 1 us; parts cost a
+// launch and their traffic at about 5 TB/s.
 TilePlan tile_plan(const Product& p) {
   const int64_t pairs = 76;
   const int64_t kb = (p.K + BK - 1) / BK;
-  TilePlan best{256, 1, 0};
+  TilePlan best{0, 1, 0};
   double best_t = 1e30;
+  const bool rows = rows_form(p);
   for (int bn : {256, 128}) {
-    const int64_t tn = (p.N + bn - 1) / bn;
-    int64_t tiles = (p.M + BM - 1) / BM * tn;
+    if (rows && bn == 128) break;
+    int64_t tiles;
     double per_kb = bn == 256 ? 0.27 : 0.15, blocks = (double)kb;
-    if (p.mode == GROUP_ROWS) tiles = ((p.M + p.experts * (BM / 2)) / BM + 1) * tn;  // half a tile lost per range
-    if (p.mode == GROUP_SUM) { tiles *= p.experts; blocks = (double)kb / p.experts + 0.5; }
+    if (rows) {
+      const int64_t tm = (p.N + BM - 1) / BM;
+      int64_t tt = (p.M + 255) / 256, ranges = 1;
+      if (p.mode == GROUP_ROWS) {
+        ranges = p.M < p.experts ? p.M : p.experts;
+        tt = ranges * ((p.M / ranges + 255) / 256);
+      }
+      tiles = tm * tt;
+      const double cols = (double)p.M / tt;
+      per_kb = 0.27 * cols / 256 > 0.1 ? 0.27 * cols / 256 : 0.1;
+    } else {
+      tiles = (p.M + BM - 1) / BM * ((p.N + bn - 1) / bn);
+      if (p.mode == GROUP_SUM) { tiles *= p.experts; blocks = (double)kb / p.experts + 0.5; }
+    }
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && (p.mode != GROUP_NONE || kb / s < 4)) break;
       const double waves = (double)((tiles * s + pairs - 1) / pairs);
       double t = waves * (blocks / s * per_kb + 1.0);
       if (s > 1) t += 3.0 + (double)p.M * p.N * 8.0 * s / 5e6;
-      if (t < best_t) { best_t = t; best.bn = bn; best.splits = s; }
+      if (t < best_t) { best_t = t; best.bn = rows ? 0 : bn; best.splits = s; }
     }
   }
   if (best.splits > 1) best.part_bytes = (int64_t)best.splits * p.M * ((p.N + 31) / 32 * 32) * 4;
@@ -646,9 +738,21 @@ TilePlan tile_plan(const Product& p) {
 cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, cudaStream_t s) {
   TcProduct q{};
   q.mode = p.mode; q.experts = p.experts; q.splits = t.splits; q.offsets = p.offsets;
-  q.M = (int)p.M; q.N = (int)p.N; q.K = (int)p.K;
-  q.tiles_m = (int)((p.M + BM - 1) / BM);
-  q.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
+  q.K = (int)p.K;
+  if (t.bn == 0) {
+    q.rows = (int)p.M;
+    q.M = (int)p.N;
+    q.tiles_m = (int)((p.N + BM - 1) / BM);
+    // token rows of one copy: a tile's half of them (16 to 128), so that few
+    // rows do not drag others in
+    const int64_t typical = p.mode == GROUP_ROWS ? 2 * p.M / p.experts + 1 : p.M;
+    q.box_rows = typical <= 32 ? 16 : (typical <= 64 ? 32 : (typical <= 128 ? 64 : 128));
+  } else {
+    q.M = (int)p.M;
+    q.N = (int)p.N;
+    q.tiles_m = (int)((p.M + BM - 1) / BM);
+    q.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
+  }
   q.bf16 = p.dtype == DT_BF16;
   q.act = p.act;
   q.D = p.D; q.bias = p.bias; q.residual = p.residual; q.r_m = p.r_m; q.preact = p.preact;
@@ -657,10 +761,10 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
   q.part = part;
   q.part_pitch = (p.N + 31) / 32 * 32;
   q.err = p.err;
-  cudaError_t e = t.bn == 256 ? run_layout<256>(p, q, s) : run_layout<128>(p, q, s);
+  cudaError_t e = t.bn == 0 ? run_rows(p, q, s) : (t.bn == 256 ? run_sum<256>(p, q, s) : run_sum<128>(p, q, s));
   if (e == cudaSuccess && t.splits > 1) {
     const int64_t n = (p.N + 7) / 8 * p.M;
-    k_linear_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q);
+    k_linear_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q, (int)p.M, (int)p.N);
     e = cudaGetLastError();
   }
   return e;

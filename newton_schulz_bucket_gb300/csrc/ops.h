@@ -58,8 +58,8 @@ struct GradPrep {
 
 // How the tensor-core form runs a product (chosen on the host from sizes).
 struct TilePlan {
-  int bn;                      // columns of a pair's tile: 256 or 128
-  int splits;                  // parts of the sum (GROUP_NONE), joined by a second kernel
+  int bn;                      // sum form (dw): columns of a pair's tile, 256 or 128; 0: rows form
+  int splits;                  // parts of the sum, joined by a second kernel
   int64_t part_bytes;          // scratch of the parts
 };
 TilePlan tile_plan(const Product& p);
