@@ -1,11 +1,12 @@
 // What the two products of a layer's gradient start from: dz = dy * act'(z),
 // and the bias gradient, the column sums of dz over each expert's rows.
 //
-// One pass over dy and z.  A block takes kGradChunk rows and 256 columns; the
-// part of the sum that its chunk c adds to range e goes to row c + e of
-// `part` (along the rows c and e only grow, so no two pairs share a row), and
-// a second kernel adds each range's parts in row order: the same bits every
-// time, and no atomics.
+// One pass over dy and z, bound by HBM.  A block takes kGradChunk rows and 32
+// pieces of columns (16 bytes each where rows allow it), eight threads to a
+// column piece that take every eighth row.  The part of the sum that chunk c
+// adds to range e goes to row c + e of `part` (along the rows c and e only
+// grow, so no two pairs share a row), and a second kernel adds each range's
+// parts in row order: the same bits every time, and no atomics.
 #include "act.cuh"
 #include "common.cuh"
 
@@ -13,64 +14,140 @@ namespace muon {
 
 namespace {
 
+constexpr int kLanes = 32, kRowLanes = 8;
+
 __device__ __forceinline__ int64_t off_at(const GradPrep& g, int e) {
   if (g.experts == 0) return e ? g.rows : 0;
   const int64_t v = g.offsets[e];
   return v < 0 ? 0 : (v > g.rows ? g.rows : v);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_grad_prep(GradPrep g) {
+template <typename T, int VEC>
+__device__ __forceinline__ void load(const T* p, float* f) {
+  if constexpr (VEC == 1) {
+    f[0] = to_f32(*p);
+  } else {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));  // read once
+    const T* h = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = to_f32(h[i]);
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store(T* p, const float* f) {
+  if constexpr (VEC == 1) {
+    *p = from_f32<T>(f[0]);
+  } else {
+    uint4 u;
+    T* h = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<uint4*>(p) = u;
+  }
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int col_blocks) {
   constexpr bool kFast = sizeof(T) == 2;
-  const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.x * kGradChunk;
-  const int64_t r1 = r0 + kGradChunk < g.rows ? r0 + kGradChunk : g.rows;
-  if (col >= g.cols) return;
-  const T* dy = static_cast<const T*>(g.dy);
-  const T* z = static_cast<const T*>(g.z);
+  __shared__ float red[kRowLanes][kLanes * VEC];
+  const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int64_t chunk = blockIdx.x / col_blocks;
+  const int64_t col = ((int64_t)(blockIdx.x % col_blocks) * kLanes + lane) * VEC;
+  const bool live = col < g.cols;
+  const int64_t r0 = chunk * kGradChunk, r1 = min(r0 + kGradChunk, g.rows);
+  const T* dy = static_cast<const T*>(g.dy) + col;
+  const T* z = static_cast<const T*>(g.z) + col;
   T* dz = static_cast<T*>(g.dz);
   const int ranges = g.experts ? g.experts : 1;
   int e = 0;
-  while (e < ranges && off_at(g, e + 1) <= r0) ++e;  // the range of row r0
-  int64_t end = e < ranges ? off_at(g, e + 1) : g.rows;
-  float sum = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    while (r >= end && e < ranges) {
-      if (g.part) g.part[((int64_t)blockIdx.x + e) * g.cols + col] = sum;
-      sum = 0.f;
-      ++e;
-      end = e < ranges ? off_at(g, e + 1) : g.rows;
+  if (g.experts) {  // the first range that ends behind r0
+    int hi = ranges;
+    while (e < hi) {
+      const int m = (e + hi) / 2;
+      if (off_at(g, m + 1) > r0) hi = m;
+      else e = m + 1;
     }
-    float v = to_f32(dy[r * g.dy_stride + col]);
-    if (g.act != ACT_NONE) {
-      v *= act_slope<kFast>(to_f32(z[r * g.cols + col]), g.act);
-      if (dz) dz[r * g.dz_stride + col] = from_f32<T>(v);
-    }
-    sum += v;
   }
-  if (g.part && e < ranges) g.part[((int64_t)blockIdx.x + e) * g.cols + col] = sum;
+  // the chunk's rows range by range; rows of no expert are left out
+  for (int64_t a = r0; e < ranges && a < r1; ++e) {
+    const int64_t b = min(off_at(g, e + 1), r1);
+    float sum[VEC] = {};
+    if (live) {
+#pragma unroll 4
+      for (int64_t r = a + rl; r < b; r += kRowLanes) {
+        float v[VEC];
+        load<T, VEC>(dy + r * g.dy_stride, v);
+        if constexpr (ACT != ACT_NONE) {
+          float zz[VEC];
+          load<T, VEC>(z + r * g.cols, zz);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[i] *= act_slope<kFast>(zz[i], ACT);
+          if (dz) store<T, VEC>(dz + r * g.dz_stride + col, v);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum[i] += v[i];
+      }
+    }
+    if (g.part && b > a) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) red[rl][i * kLanes + lane] = sum[i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < kLanes * VEC; i += kLanes * kRowLanes) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowLanes; ++k) s += red[k][i];
+        const int64_t c = ((int64_t)(blockIdx.x % col_blocks) * kLanes + i % kLanes) * VEC + i / kLanes;
+        if (c < g.cols) g.part[(chunk + e) * g.cols + c] = s;
+      }
+      __syncthreads();
+    }
+    if (b > a) a = b;
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_grad_bias(GradPrep g) {
-  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int e = blockIdx.y;
+__global__ void __launch_bounds__(256) k_grad_bias(GradPrep g, int col_blocks) {
+  const int64_t col = (int64_t)(blockIdx.x % col_blocks) * 256 + threadIdx.x;
+  const int e = blockIdx.x / col_blocks;
   if (col >= g.cols) return;
   const int64_t lo = off_at(g, e), hi = off_at(g, e + 1);
   float sum = 0.f;
-  if (hi > lo)
-    for (int64_t c = lo / kGradChunk; c <= (hi - 1) / kGradChunk; ++c) sum += g.part[(c + e) * g.cols + col];
+  if (hi > lo) {
+    const float* part = g.part + e * g.cols + col;
+    const int64_t last = (hi - 1) / kGradChunk;
+#pragma unroll 8
+    for (int64_t c = lo / kGradChunk; c <= last; ++c) sum += part[c * g.cols];
+  }
   static_cast<T*>(g.db)[(int64_t)e * g.cols + col] = from_f32<T>(sum);
+}
+
+template <typename T, int VEC>
+void prep(const GradPrep& g, cudaStream_t s) {
+  const int cb = (int)((g.cols + kLanes * VEC - 1) / (kLanes * VEC));
+  const unsigned grid = (unsigned)((g.rows + kGradChunk - 1) / kGradChunk * cb);
+  const int threads = kLanes * kRowLanes;
+  switch (g.act) {
+    case ACT_RELU: k_grad_prep<T, VEC, ACT_RELU><<<grid, threads, 0, s>>>(g, cb); break;
+    case ACT_SILU: k_grad_prep<T, VEC, ACT_SILU><<<grid, threads, 0, s>>>(g, cb); break;
+    case ACT_GELU: k_grad_prep<T, VEC, ACT_GELU><<<grid, threads, 0, s>>>(g, cb); break;
+    case ACT_GELU_TANH: k_grad_prep<T, VEC, ACT_GELU_TANH><<<grid, threads, 0, s>>>(g, cb); break;
+    default: k_grad_prep<T, VEC, ACT_NONE><<<grid, threads, 0, s>>>(g, cb);
+  }
 }
 
 template <typename T>
 cudaError_t run(const GradPrep& g, cudaStream_t s) {
-  const unsigned cols = (unsigned)((g.cols + 255) / 256);
-  const unsigned chunks = (unsigned)((g.rows + kGradChunk - 1) / kGradChunk);
-  k_grad_prep<T><<<dim3(chunks, cols), 256, 0, s>>>(g);
+  constexpr int V = 16 / (int)sizeof(T);
+  const auto ok = [](const void* p, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % V == 0;
+  };
+  // 16-byte pieces where every row of every tensor starts on 16 bytes
+  if (g.cols % V == 0 && ok(g.dy, g.dy_stride) && ok(g.z, g.cols) && ok(g.dz, g.dz_stride)) prep<T, V>(g, s);
+  else prep<T, 1>(g, s);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && g.db) {
-    k_grad_bias<T><<<dim3(cols, g.experts ? g.experts : 1), 256, 0, s>>>(g);
+    const int cb = (int)((g.cols + 255) / 256);
+    k_grad_bias<T><<<(unsigned)cb * (g.experts ? g.experts : 1), 256, 0, s>>>(g, cb);
     e = cudaGetLastError();
   }
   return e;

@@ -18,8 +18,10 @@
 // alignment.
 //
 // Sum form (dw = x^T dz).  Both operands are stored across the sum (tokens);
-// tiles are 256 x 256 or 256 x 128.  Output blocks go through a swizzled
-// staging block so that stores are 16 bytes a lane along rows.
+// tiles are 256 x 256 or 256 x 128.  With few tokens to an expert the epilogue
+// sets the pace: 32 x 64 blocks of rounded outputs are staged swizzled and
+// leave by TMA stores (where output rows start on 16 bytes), so that the
+// load/store pipe carries each output once, not three times.
 //
 // Experts.  Row ranges come from a device array, so every role walks the
 // ranges itself.  GROUP_ROWS: an expert's rows are tiled from its first row;
@@ -56,7 +58,7 @@ struct TcProduct {
   int M, N;                 // rows form: features (M); sum form: the output
   int tiles_m, tiles_n;     // sum form; rows form: feature tiles (tiles_m)
   int box_rows;             // rows form: token rows of one TMA copy
-  int bf16, act, vec;       // vec (sum form): output rows start on 16 bytes
+  int bf16, act, vec;       // vec: output rows (and the epilogue's tensors) start on 16 bytes
   void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert
   const void* bias;
   const void* residual;
@@ -74,9 +76,10 @@ struct Smem {
   static constexpr uint32_t kA = 128 * BK * 2;
   static constexpr uint32_t kB = (BN == 0 ? 128 : BN / 2) * BK * 2;
   static constexpr uint32_t kStage = kA + kB;
-  static constexpr uint32_t kBars = kStages * kStage;  // full, empty, fix, tfull, tempty, done; TMEM slot, abort
-  static constexpr uint32_t kEpi = kBars + 256;
-  static constexpr uint32_t kTotal = kEpi + (BN == 0 ? 0 : kEpiWarps * 4096) + 1024;  // + alignment slack
+  static constexpr uint32_t kEpi = kStages * kStage;  // sum form: 4 KB a warp, 1024-byte aligned for TMA's swizzle
+  static constexpr uint32_t kBars = kEpi + (BN == 0 ? 0 : kEpiWarps * 4096);  // full, empty, fix, tfull, tempty,
+                                                                               // done; TMEM slot, abort flag
+  static constexpr uint32_t kTotal = kBars + 256 + 1024;  // + alignment slack
   static_assert((3 * kStages + 5) * 8 + 8 <= 256 && kTotal <= 227 * 1024, "shared memory layout");
 };
 
@@ -247,9 +250,9 @@ __device__ __forceinline__ void write_tokens(const TcProduct& p, float* v, int e
     if (i < n) y[(int64_t)i * p.M] = from_f32<T>(v[i]);
 }
 
-// A warp's 32 x 32 block from TMEM into its staging block, row = lane, the
-// 16-byte pieces of row r at piece index ^ (r & 7): both this write and the
-// reads along rows below are free of bank conflicts.
+// Sum form, a warp's 32 x 32 block from TMEM into its staging block, row =
+// lane, the 16-byte pieces of row r at piece index ^ (r & 7): both this write
+// and the reads along rows below are free of bank conflicts.
 __device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane, bool zero) {
   uint32_t r[32];
   tmem_ld32(taddr, r);
@@ -261,28 +264,32 @@ __device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane,
   __syncwarp();
 }
 
-// Sum form: rows row0 .. row0 + 31 (those < M) and columns col0 .. col0 + 31
-// (those < N) of the output from the staging block.
+// Rows row0 .. row0 + 31 (those < M) and columns col0 .. col0 + 31 (those < N)
+// of the output from the staging block, one column a lane, for rows that TMA
+// cannot store.
 __device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int row0, int col0,
                                             int64_t d_base) {
   const int64_t N = p.N;
-  if (p.vec && col0 + 32 <= p.N) {
-    const int q = lane & 3, c = col0 + q * 8;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int rr = it * 8 + (lane >> 2), row = row0 + rr;
-      const uint4* src = reinterpret_cast<const uint4*>(sw + rr * 32);
-      float v[8];
-      u4_to_f4x2(src[(2 * q) ^ (rr & 7)], src[(2 * q + 1) ^ (rr & 7)], v);
-      if (row < p.M)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + d_base + row * N + c) = pack8(v, p.bf16);
-    }
-  } else if (col0 + lane < p.N) {
+  if (col0 + lane < p.N) {
     const int c = col0 + lane;
     for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
       st16(p.D, d_base + (row0 + rr) * N + c, sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)], p.bf16);
   }
   __syncwarp();  // the block is overwritten next
+}
+
+// 32 rows x 64 columns (two TMEM loads of 32) rounded into the staging block in
+// the layout of a 128-byte-swizzled TMA box.
+__device__ __forceinline__ void stage_rounded(const float* v, uint8_t* sw, int lane, bool zero, int bf16) {
+  uint4* row = reinterpret_cast<uint4*>(sw + lane * 128);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) row[q ^ (lane & 7)] = zero ? make_uint4(0, 0, 0, 0) : pack8(v + 8 * q, bf16);
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // The same block of one part of a split sum, in fp32 (pitch a multiple of 32).
@@ -314,7 +321,7 @@ __device__ void zero_span(void* base, int64_t from, int64_t to, int64_t tid, int
 template <bool AMN, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                const __grid_constant__ TcProduct p) {
+                const __grid_constant__ CUtensorMap mapD, const __grid_constant__ TcProduct p) {
   using L = Smem<BN>;
   constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -475,15 +482,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        float* sw = reinterpret_cast<float*>(smem + L::kEpi) + (warp - 2) * 1024;
-        const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
+        uint8_t* sw = smem + L::kEpi + (warp - 2) * 4096;
+        const bool zero = it.k0 >= it.k1;
+        const int c0 = half * (BN / 2);  // this warp's columns of the tile
+        if (p.splits == 1 && p.vec) {
 #pragma unroll 1
-        for (int ch = half * (BN / 64); ch < (half + 1) * (BN / 64); ++ch) {
-          const int col0 = it.n0 + ch * 32;
-          if (col0 >= p.N || row0 >= p.M) break;  // the same for the whole warp
-          stage_block(tacc + (uint32_t)(ch * 32), sw, lane, it.k0 >= it.k1);
-          if (p.splits > 1) write_part(p, sw, lane, row0, col0, it.split);
-          else write_block(p, sw, lane, row0, col0, d_base);
+          for (int c = c0; c < c0 + BN / 2; c += 64) {
+            if (it.n0 + c >= p.N || row0 >= p.M) break;  // the same for the whole warp
+            float v[64];
+            tmem_ld32_async(tacc + (uint32_t)c, reinterpret_cast<uint32_t*>(v));
+            tmem_ld32_async(tacc + (uint32_t)c + 32, reinterpret_cast<uint32_t*>(v) + 32);
+            // the last store has read the block
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            tmem_wait_ld();
+            stage_rounded(v, sw, lane, zero, p.bf16);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&mapD, saddr(sw), it.n0 + c, row0, it.e);
+          }
+        } else {
+          const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
+#pragma unroll 1
+          for (int c = c0; c < c0 + BN / 2; c += 32) {
+            if (it.n0 + c >= p.N || row0 >= p.M) break;
+            stage_block(tacc + (uint32_t)c, reinterpret_cast<float*>(sw), lane, zero);
+            if (p.splits > 1) write_part(p, reinterpret_cast<float*>(sw), lane, row0, it.n0 + c, it.split);
+            else write_block(p, reinterpret_cast<float*>(sw), lane, row0, it.n0 + c, d_base);
+          }
         }
       }
       tc_fence_before();
@@ -491,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_cluster(map_to(tempty(acc), 0));
       if (++acc == 2) { acc = 0; aph ^= 1; }
     }
+    if (!kRows && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (p.mode == GROUP_ROWS) {  // rows of no expert
       const int64_t from = (int64_t)range_at(p, p.experts, p.rows) * p.M, to = (int64_t)p.rows * p.M;
       const int64_t tid = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 64;
@@ -611,7 +638,8 @@ bool aligned_rows(const void* p, int64_t stride) {
 
 // The kernel with its function attributes set (once per device).
 template <bool AMN, int BN>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcProduct& q, int64_t items, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const TcProduct& q,
+                   int64_t items, cudaStream_t s) {
   auto fn = k_linear_tc<AMN, BN>;
   static bool ready[64] = {};
   static std::mutex mu;
@@ -639,7 +667,7 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcProduct
   at[0].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, fn, ma, mb, q);
+  return cudaLaunchKernelEx(&lc, fn, ma, mb, md, q);
 }
 
 // Rows form of D[p.M rows][p.N features]: M operand p.B (the weights).
@@ -657,18 +685,21 @@ cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
   int64_t tt = (p.M + 255) / 256;
   if (p.mode == GROUP_ROWS) tt = p.M / 256 + (p.M < p.experts ? p.M : p.experts);  // at most
   const int64_t items = tt * q.tiles_m * q.splits;
-  return across ? launch<true, 0>(mw, mx, q, items, s) : launch<false, 0>(mw, mx, q, items, s);
+  return across ? launch<true, 0>(mw, mx, mx, q, items, s) : launch<false, 0>(mw, mx, mx, q, items, s);
 }
 
 template <int BN>
 cudaError_t run_sum(const Product& p, const TcProduct& q, cudaStream_t s) {
   const int type = q.bf16 ? NS_BF16 : NS_F16;
-  CUtensorMap ma, mb;
+  const int64_t mats = p.mode == GROUP_SUM ? p.experts : 1;
+  CUtensorMap ma, mb, md;
   cudaError_t e = tc_encode_map(&ma, p.A, type, p.M, p.K, 1, p.a_k, p.K * p.a_k, 64, 64);
   if (e == cudaSuccess) e = tc_encode_map(&mb, p.B, type, p.N, p.K, 1, p.b_k, p.K * p.b_k, 64, 64);
+  md = mb;
+  if (e == cudaSuccess && q.vec) e = tc_encode_map(&md, p.D, type, p.N, p.M, mats, p.N, p.M * p.N, 64, 32);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)q.tiles_m * q.tiles_n * (p.mode == GROUP_SUM ? p.experts : q.splits);
-  return launch<true, BN>(ma, mb, q, items, s);
+  return launch<true, BN>(ma, mb, md, q, items, s);
 }
 
 // y and dx sum along the rows of A; dw sums across them.

@@ -8,13 +8,16 @@ return are what ``MuonPlan.step`` takes.  All arithmetic is in the library's
 CUDA kernels (include/muon_ops.h holds the contract of each); this module checks
 tensors, allocates outputs and scratch, and marshals pointers.
 
-Every call takes ``stream`` (a ``torch.cuda.Stream`` or a handle; default: the
+Every call takes ``stream=`` (a ``torch.cuda.Stream`` or a handle; default: the
 current stream).  Outputs and scratch belong to that stream in PyTorch's
-allocator; a caller who made the inputs on another stream orders the two.
+allocator; a caller who made the inputs on another stream orders the two.  The
+tensors live on the current device.
 """
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import struct
 
 import torch
 
@@ -27,26 +30,69 @@ ACTIVATIONS = {"none": _c.MUON_ACT_NONE, "relu": _c.MUON_ACT_RELU, "silu": _c.MU
                "gelu": _c.MUON_ACT_GELU, "gelu_tanh": _c.MUON_ACT_GELU_TANH}
 _DTYPES = {torch.float32: _c.MUON_DTYPE_F32, torch.float16: _c.MUON_DTYPE_F16,
            torch.bfloat16: _c.MUON_DTYPE_BF16}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_empty = torch.empty
+
+# A call on small tensors is bound by this module's own time, so the checks
+# read each property once, the argument structure is packed in one step
+# (muon_linear_args: 4 int32, 8 int64, 13 pointers, a size), and scratch sizes
+# are remembered per problem.
+_PACK = struct.Struct("=4i8q14Q").pack
+assert struct.calcsize("=4i8q14Q") == C.sizeof(_c.muon_linear_args)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 
 
-def _dtype(t, what):
+def _on_stream(op):
+    """Adds ``stream`` to an operator that runs on the current stream."""
+
+    @functools.wraps(op)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return op(*args, **kw)
+        like = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if like is None or not like.is_cuda:
+            raise ValueError("the tensors must live on a CUDA device")
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), like.device)
+        if s.device != like.device:
+            raise ValueError(f"stream is on {s.device}, the tensors are on {like.device}")
+        if s != torch.cuda.current_stream(like.device):
+            for t in (*args, *kw.values()):  # not handed out again before this call is done with it
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(s)
+        with torch.cuda.stream(s):
+            return op(*args, **kw)
+
+    return call
+
+
+def _start(t, what, dims):
+    """(device index, current stream, dtype code) of an operator's first tensor."""
+    if t.dim() != dims:
+        raise ValueError(f"{what} must be {dims}-D, got {list(t.shape)}")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{what} has dtype {t.dtype}, expected float32, float16 or bfloat16")
-    return code
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must live on a CUDA device")
+    if dev != _current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev, _raw_stream(dev), code
 
 
-def _check(t, what, like, shape, dtype=None):
-    if t.shape != torch.Size(shape):
+def _check(t, what, dev, dtype, shape):
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {list(t.shape)}, expected {list(shape)}")
-    if t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{what} has dtype {t.dtype}, expected {dtype or like.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{what} must live on {like.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must live on cuda:{dev}")
 
 
-def _contiguous(t, what, like, shape, dtype=None):
-    _check(t, what, like, shape, dtype)
+def _contiguous(t, what, dev, dtype, shape):
+    """Address of a contiguous tensor of this type and shape."""
+    _check(t, what, dev, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
@@ -65,182 +111,148 @@ def _rows(t, what):
     return s0
 
 
-def _weight(w, what):
+def _weight(w, n_in, n_out):
     """(layout, row stride as stored) of the last two dims of w."""
-    n_in, n_out = w.shape[-2:]
-    s0, s1 = w.stride()[-2:]
+    *_, s0, s1 = w.stride()
     if (s1 == 1 or n_out == 1) and (s0 >= n_out or n_in == 1):
         return _c.MUON_W_IN_OUT, s0 if n_in > 1 else n_out
     if (s0 == 1 or n_in == 1) and (s1 >= n_in or n_out == 1):
         return _c.MUON_W_OUT_IN, s1 if n_out > 1 else n_in
-    raise ValueError(f"{what} must be contiguous along in or out, got strides {list(w.stride())}")
-
-
-def _need_cuda(t, what):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must live on a CUDA device")
-
-
-class _On:
-    """The stream and device of one call: its handle, and a context in which
-    they are current where they are not already."""
-
-    def __init__(self, like, stream, tensors):
-        dev = like.device
-        self.other = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), dev)
-            if s.device != dev:
-                raise ValueError(f"stream is on {s.device}, the tensors are on {dev}")
-            self.handle = s.cuda_stream
-            if s != torch.cuda.current_stream(dev):
-                self.other = torch.cuda.stream(s)
-                for t in tensors:  # their memory is not handed out again before this call is done with it
-                    if t is not None:
-                        t.record_stream(s)
-        if self.other is None and torch.cuda.current_device() != dev.index:
-            self.other = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-        return C.c_void_p(self.handle)
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    raise ValueError(f"w must be contiguous along in or out, got strides {list(w.stride())}")
 
 
 # ---- linear ----
 
+_scratch_sizes = {}
 
-def _linear_args(x, w, activation, offsets):
-    """The arguments both directions share, checked."""
-    _need_cuda(x, "x")
-    a = _c.muon_linear_args()
-    a.dtype = _dtype(x, "x")
-    try:
-        a.activation = ACTIVATIONS[activation]
-    except KeyError:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}") from None
-    if x.dim() != 2:
-        raise ValueError(f"x must be [rows, in], got {list(x.shape)}")
+
+@functools.lru_cache(maxsize=None)
+def _linear_call(backward):
+    """muon_linear(_backward) taking the packed structure."""
+    return C.CFUNCTYPE(C.c_int, C.c_char_p, C.c_void_p)(
+        ("muon_linear_backward" if backward else "muon_linear", _c.load()))
+
+
+def _run(backward, dev, stream, head, strides, ptrs):
+    """One call: head = dtype .. out, then strides, then pointers x .. db."""
+    # what the size depends on: the problem, which tensors there are, and 16-byte alignment
+    key = (backward, head, strides, tuple([p & 15 if p else -1 for p in ptrs]))
+    size = _scratch_sizes.get(key)
+    if size is None:
+        n = C.c_size_t()
+        a = _c.muon_linear_args.from_buffer_copy(_PACK(*head, *strides, *ptrs, 0, 0))
+        _c.check(_c.load().muon_linear_workspace(C.byref(a), int(backward), C.byref(n)), "muon_linear_workspace")
+        if len(_scratch_sizes) >= 4096:
+            _scratch_sizes.clear()
+        size = _scratch_sizes[key] = n.value
+    ws = _empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = _linear_call(backward)(_PACK(*head, *strides, *ptrs, ws.data_ptr() if size else 0, size), stream)
+    if st:
+        _c.check(st, "muon_linear_backward" if backward else "muon_linear")
+
+
+def _problem(x, w, offsets, activation):
+    """What both directions share, checked."""
+    dev, stream, code = _start(x, "x", 2)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    rows, n_in = x.shape
+    shape = w.shape
     lead = 0 if offsets is None else 1
-    if w.dim() != 2 + lead or w.shape[-2] != x.shape[1]:
-        raise ValueError(f"w must be [{'experts, ' if lead else ''}in, out] with in = {x.shape[1]}, got {list(w.shape)}")
-    if w.dtype != x.dtype:
-        raise ValueError(f"w has dtype {w.dtype}, expected {x.dtype}")
-    if w.device != x.device:
-        raise ValueError(f"w must live on {x.device}")
-    a.rows, a.out = x.shape[0], w.shape[-1]
-    setattr(a, "in", x.shape[1])
-    a.x, a.x_stride = x.data_ptr(), _rows(x, "x")
-    a.w = w.data_ptr()
-    a.w_layout, a.w_stride = _weight(w, "w")
+    if len(shape) != 2 + lead or shape[-2] != n_in:
+        raise ValueError(f"w must be [{'experts, ' if lead else ''}in, out] with in = {n_in}, got {list(shape)}")
+    if w.dtype != x.dtype or w.get_device() != dev:
+        raise ValueError(f"w must be {x.dtype} on cuda:{dev}, got {w.dtype} on {w.device}")
+    n_out = shape[-1]
+    layout, w_stride = _weight(w, n_in, n_out)
+    experts = off = e_stride = 0
     if lead:
-        a.experts = w.shape[0]
-        a.w_expert_stride = w.stride(0) if w.shape[0] > 1 else 0
-        a.offsets = _contiguous(offsets, "offsets", x, (w.shape[0] + 1,), torch.int32)
-    return a
+        experts = shape[0]
+        e_stride = w.stride(0) if experts > 1 else 0
+        off = _contiguous(offsets, "offsets", dev, _I32, (experts + 1,))
+    return dev, stream, (code, act, experts, layout, rows, n_in, n_out), w_stride, e_stride, off
 
 
-def _scratch(L, a, backward, like):
-    n = C.c_size_t()
-    _c.check(L.muon_linear_workspace(C.byref(a), backward, C.byref(n)), "muon_linear_workspace")
-    if n.value == 0:
-        return None
-    ws = torch.empty(n.value, dtype=torch.uint8, device=like.device)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), n.value
-    return ws
-
-
-def _forward(x, w, offsets, bias, activation, residual, keep_preact, stream):
-    a = _linear_args(x, w, activation, offsets)
-    rows, out = x.shape[0], w.shape[-1]
+def _forward(x, w, offsets, bias, activation, residual, keep_preact):
+    dev, stream, head, w_stride, e_stride, off = _problem(x, w, offsets, activation)
+    dtype, rows, out = x.dtype, head[4], head[6]
+    bp = rp = r_stride = 0
     if bias is not None:
-        a.bias = _contiguous(bias, "bias", x, (*w.shape[:-2], out))
+        bp = _contiguous(bias, "bias", dev, dtype, (out,) if offsets is None else (head[2], out))
     if residual is not None:
-        _check(residual, "residual", x, (rows, out))
-        a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, "residual")
-    L = _c.load()
-    with _On(x, stream, (x, w, offsets, bias, residual)) as st:
-        y = torch.empty((rows, out), dtype=x.dtype, device=x.device)
-        a.y = y.data_ptr()
-        z = None
-        if keep_preact:
-            z = torch.empty_like(y)
-            a.preact_out = z.data_ptr()
-        ws = _scratch(L, a, 0, x)  # noqa: F841  (held until the launch)
-        _c.check(L.muon_linear(C.byref(a), st), "muon_linear")
+        _check(residual, "residual", dev, dtype, (rows, out))
+        rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
+    y = _empty((rows, out), dtype=dtype, device=dev)
+    z = _empty((rows, out), dtype=dtype, device=dev) if keep_preact else None
+    _run(False, dev, stream, head, (_rows(x, "x"), w_stride, e_stride, r_stride, 0),
+         (x.data_ptr(), w.data_ptr(), bp, rp, off, 0, 0, y.data_ptr(), z.data_ptr() if keep_preact else 0, 0, 0, 0))
     return (y, z) if keep_preact else y
 
 
-def _backward(dy, x, w, offsets, preact, activation, dx, dw, bias, stream):
-    a = _linear_args(x, w, activation, offsets)
-    rows, out = x.shape[0], w.shape[-1]
-    _check(dy, "dy", x, (rows, out))
-    a.dy, a.dy_stride = dy.data_ptr(), _rows(dy, "dy")
-    if a.activation != _c.MUON_ACT_NONE:
+def _backward(dy, x, w, offsets, preact, activation, dx, dw, bias):
+    dev, stream, head, w_stride, e_stride, off = _problem(x, w, offsets, activation)
+    dtype, experts, rows, n_in, out = x.dtype, head[2], head[4], head[5], head[6]
+    _check(dy, "dy", dev, dtype, (rows, out))
+    zp = 0
+    if head[1] != _c.MUON_ACT_NONE:
         if preact is None:
             raise ValueError(f"preact is needed for activation {activation!r}")
-        a.preact = _contiguous(preact, "preact", x, (rows, out))
+        zp = _contiguous(preact, "preact", dev, dtype, (rows, out))
     if not (dx or dw or bias):
         raise ValueError("nothing to compute: dx, dw and bias are all False")
-    L = _c.load()
+    lead = () if offsets is None else (experts,)
     gx = gw = gb = None
-    with _On(x, stream, (dy, x, w, offsets, preact)) as st:
-        if dx:
-            gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.dx = gx.data_ptr()
-        if dw:  # in w's memory order
-            if a.w_layout == _c.MUON_W_IN_OUT:
-                gw = torch.empty(w.shape, dtype=w.dtype, device=w.device)
-            else:
-                gw = torch.empty((*w.shape[:-2], out, w.shape[-2]), dtype=w.dtype, device=w.device).transpose(-1, -2)
-            a.dw = gw.data_ptr()
-        if bias:
-            gb = torch.empty((*w.shape[:-2], out), dtype=x.dtype, device=x.device)
-            a.db = gb.data_ptr()
-        ws = _scratch(L, a, 1, x)  # noqa: F841  (held until the launch)
-        _c.check(L.muon_linear_backward(C.byref(a), st), "muon_linear_backward")
+    xp = wp = bp = 0
+    if dx:
+        gx = _empty((rows, n_in), dtype=dtype, device=dev)
+        xp = gx.data_ptr()
+    if dw:  # in w's memory order
+        if head[3] == _c.MUON_W_IN_OUT:
+            gw = _empty((*lead, n_in, out), dtype=dtype, device=dev)
+        else:
+            gw = _empty((*lead, out, n_in), dtype=dtype, device=dev).transpose(-1, -2)
+        wp = gw.data_ptr()
+    if bias:
+        gb = _empty((*lead, out), dtype=dtype, device=dev)
+        bp = gb.data_ptr()
+    _run(True, dev, stream, head, (_rows(x, "x"), w_stride, e_stride, 0, _rows(dy, "dy")),
+         (x.data_ptr(), w.data_ptr(), 0, 0, off, zp, dy.data_ptr(), 0, 0, xp, wp, bp))
     return gx, gw, gb
 
 
-def linear(x, w, bias=None, activation="none", residual=None, keep_preact=False, stream=None):
+@_on_stream
+def linear(x, w, bias=None, activation="none", residual=None, keep_preact=False):
     """y = act(x @ w + bias) + residual for x [rows, in] and w [in, out]; with
     keep_preact (y, z), z = x @ w + bias for the way back.
 
     w may be stored [out, in] and passed as its transposed view; x and residual
     may have any row stride.  float32, float16 or bfloat16, all tensors of one
     type (16-bit types sum in fp32, fp32 stays fp32)."""
-    return _forward(x, w, None, bias, activation, residual, keep_preact, stream)
+    return _forward(x, w, None, bias, activation, residual, keep_preact)
 
 
-def linear_backward(dy, x, w, preact=None, activation="none", dx=True, dw=True, bias=False, stream=None):
+@_on_stream
+def linear_backward(dy, x, w, preact=None, activation="none", dx=True, dw=True, bias=False):
     """(dx, dw, db) of linear for the gradient dy of its result; those not asked
     for are None.  dw has w's shape and memory order.  The residual's gradient
     is dy itself."""
-    return _backward(dy, x, w, None, preact, activation, dx, dw, bias, stream)
+    return _backward(dy, x, w, None, preact, activation, dx, dw, bias)
 
 
-def expert_linear(x, offsets, w, bias=None, activation="none", residual=None, keep_preact=False, stream=None):
+@_on_stream
+def expert_linear(x, offsets, w, bias=None, activation="none", residual=None, keep_preact=False):
     """linear over an expert tensor w [experts, in, out]: rows
     offsets[e] .. offsets[e + 1] - 1 of x (int32, on the device, as ``dispatch``
     gives them) go through w[e] and bias[e].  Rows from offsets[-1] on come out
     zero."""
-    return _forward(x, w, _given(offsets), bias, activation, residual, keep_preact, stream)
+    return _forward(x, w, _given(offsets), bias, activation, residual, keep_preact)
 
 
-def expert_linear_backward(dy, x, offsets, w, preact=None, activation="none", dx=True, dw=True, bias=False,
-                           stream=None):
+@_on_stream
+def expert_linear_backward(dy, x, offsets, w, preact=None, activation="none", dx=True, dw=True, bias=False):
     """(dx, dw, db) of expert_linear; an expert without rows gets zero dw and db."""
-    return _backward(dy, x, w, _given(offsets), preact, activation, dx, dw, bias, stream)
+    return _backward(dy, x, w, _given(offsets), preact, activation, dx, dw, bias)
 
 
 def _given(offsets):
@@ -252,151 +264,143 @@ def _given(offsets):
 # ---- gate ----
 
 
-def _gate_check(logits, top_k):
-    _need_cuda(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [tokens, experts], got {list(logits.shape)}")
-    return _dtype(logits, "logits"), _rows(logits, "logits")
-
-
-def gate(logits, top_k, renormalize=True, stream=None):
+@_on_stream
+def gate(logits, top_k, renormalize=True):
     """(indices int32, weights float32), [tokens, top_k] each: the experts with
     the largest logits in falling order (ties: the lower index) and their
     softmax weights, over the chosen experts (renormalize) or over all.  A
     logit of -inf masks an expert; places that no open expert is left for get
     index -1 and weight 0."""
-    code, stride = _gate_check(logits, top_k)
+    dev, stream, code = _start(logits, "logits", 2)
     tokens, experts = logits.shape
-    L = _c.load()
-    with _On(logits, stream, (logits,)) as st:
-        idx = torch.empty((tokens, int(top_k)), dtype=torch.int32, device=logits.device)
-        wts = torch.empty((tokens, int(top_k)), dtype=torch.float32, device=logits.device)
-        _c.check(L.muon_gate(code, tokens, experts, int(top_k), int(renormalize), logits.data_ptr(), stride,
-                             idx.data_ptr(), wts.data_ptr(), st), "muon_gate")
+    idx = _empty((tokens, top_k), dtype=_I32, device=dev)
+    wts = _empty((tokens, top_k), dtype=_F32, device=dev)
+    st = _c.load().muon_gate(code, tokens, experts, top_k, renormalize, logits.data_ptr(), _rows(logits, "logits"),
+                             idx.data_ptr(), wts.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_gate")
     return idx, wts
 
 
-def gate_backward(dweights, logits, indices, renormalize=True, stream=None):
+@_on_stream
+def gate_backward(dweights, logits, indices, renormalize=True):
     """The gradient of gate's logits for that of its weights, the choice held
     fixed (indices as gate gave them)."""
+    dev, stream, code = _start(logits, "logits", 2)
+    tokens, experts = logits.shape
     if indices.dim() != 2:
         raise ValueError(f"indices must be [tokens, top_k], got {list(indices.shape)}")
     top_k = indices.shape[1]
-    code, stride = _gate_check(logits, top_k)
-    tokens, experts = logits.shape
-    ip = _contiguous(indices, "indices", logits, (tokens, top_k), torch.int32)
-    dp = _contiguous(dweights, "dweights", logits, (tokens, top_k), torch.float32)
-    L = _c.load()
-    with _On(logits, stream, (dweights, logits, indices)) as st:
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-        _c.check(L.muon_gate_backward(code, tokens, experts, top_k, int(renormalize), dp, logits.data_ptr(),
-                                      stride, ip, out.data_ptr(), st), "muon_gate_backward")
+    ip = _contiguous(indices, "indices", dev, _I32, (tokens, top_k))
+    dp = _contiguous(dweights, "dweights", dev, _F32, (tokens, top_k))
+    out = _empty((tokens, experts), dtype=logits.dtype, device=dev)
+    st = _c.load().muon_gate_backward(code, tokens, experts, top_k, renormalize, dp, logits.data_ptr(),
+                                      _rows(logits, "logits"), ip, out.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_gate_backward")
     return out
 
 
 # ---- tokens into expert order and back ----
 
 
-def _matrix(t, what):
-    _need_cuda(t, what)
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be 2-D, got {list(t.shape)}")
-    return _dtype(t, what), _rows(t, what)
-
-
-def _slots(slot, like):
+def _slots(slot, rows, what, dev):
+    """(address, tokens, top_k) of the slots of `rows` rows in expert order."""
     if slot.dim() != 2:
         raise ValueError(f"slot must be [tokens, top_k], got {list(slot.shape)}")
-    return _contiguous(slot, "slot", like, slot.shape, torch.int32)
+    tokens, top_k = slot.shape
+    if rows != tokens * top_k:
+        raise ValueError(f"{what} must have tokens * top_k = {tokens * top_k} rows, got {rows}")
+    return _contiguous(slot, "slot", dev, _I32, (tokens, top_k)), tokens, top_k
 
 
-def dispatch(x, indices, n_experts, stream=None):
+@_on_stream
+def dispatch(x, indices, n_experts):
     """(xs, slot, offsets): the rows of x [tokens, hidden] in expert order.
 
     Assignment (t, j) of indices [tokens, top_k] (int32 or int64) goes to row
     slot[t, j] of xs [tokens * top_k, hidden]: by expert, then t, then j.  An
     index outside [0, n_experts) drops its assignment (slot -1).  Expert e owns
     rows offsets[e] .. offsets[e + 1] - 1; rows that no expert owns are zero."""
-    code, stride = _matrix(x, "x")
+    dev, stream, code = _start(x, "x", 2)
     tokens, hidden = x.shape
     if indices.dim() != 2 or indices.shape[0] != tokens:
         raise ValueError(f"indices must be [tokens, top_k] with tokens = {tokens}, got {list(indices.shape)}")
-    if indices.dtype not in (torch.int32, torch.int64):
+    if indices.dtype != _I32 and indices.dtype != _I64:
         raise ValueError(f"indices has dtype {indices.dtype}, expected int32 or int64")
     top_k = indices.shape[1]
-    ip = _contiguous(indices, "indices", x, indices.shape, indices.dtype)
+    ip = _contiguous(indices, "indices", dev, indices.dtype, indices.shape)
     L = _c.load()
     n = C.c_size_t()
-    _c.check(L.muon_dispatch_workspace(tokens, top_k, int(n_experts), C.byref(n)), "muon_dispatch_workspace")
-    dev = x.device
-    with _On(x, stream, (x, indices)) as st:
-        xs = torch.empty((tokens * top_k, hidden), dtype=x.dtype, device=dev)
-        slot = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-        offsets = torch.empty(int(n_experts) + 1, dtype=torch.int32, device=dev)
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-        _c.check(L.muon_dispatch(code, tokens, hidden, top_k, int(n_experts), x.data_ptr(), stride, ip,
-                                 8 * indices.element_size(), xs.data_ptr(), slot.data_ptr(), offsets.data_ptr(),
-                                 _ptr(ws), n.value, st), "muon_dispatch")
+    st = L.muon_dispatch_workspace(tokens, top_k, n_experts, C.byref(n))
+    if st:
+        _c.check(st, "muon_dispatch_workspace")
+    size = n.value
+    xs = _empty((tokens * top_k, hidden), dtype=x.dtype, device=dev)
+    slot = _empty((tokens, top_k), dtype=_I32, device=dev)
+    offsets = _empty(n_experts + 1, dtype=_I32, device=dev)
+    ws = _empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = L.muon_dispatch(code, tokens, hidden, top_k, n_experts, x.data_ptr(), _rows(x, "x"), ip,
+                         32 if indices.dtype == _I32 else 64, xs.data_ptr(), slot.data_ptr(), offsets.data_ptr(),
+                         ws.data_ptr() if size else None, size, stream)
+    if st:
+        _c.check(st, "muon_dispatch")
     return xs, slot, offsets
 
 
-def dispatch_backward(dxs, slot, stream=None):
+@_on_stream
+def dispatch_backward(dxs, slot):
     """dx[t] = sum over j of dxs[slot[t, j]]."""
-    code, stride = _matrix(dxs, "dxs")
-    sp = _slots(slot, dxs)
-    tokens, top_k = slot.shape
-    if dxs.shape[0] != tokens * top_k:
-        raise ValueError(f"dxs must have tokens * top_k = {tokens * top_k} rows, got {dxs.shape[0]}")
-    L = _c.load()
-    with _On(dxs, stream, (dxs, slot)) as st:
-        dx = torch.empty((tokens, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
-        _c.check(L.muon_dispatch_backward(code, tokens, dxs.shape[1], top_k, dxs.data_ptr(), stride, sp,
-                                          dx.data_ptr(), st), "muon_dispatch_backward")
+    dev, stream, code = _start(dxs, "dxs", 2)
+    rows, hidden = dxs.shape
+    sp, tokens, top_k = _slots(slot, rows, "dxs", dev)
+    dx = _empty((tokens, hidden), dtype=dxs.dtype, device=dev)
+    st = _c.load().muon_dispatch_backward(code, tokens, hidden, top_k, dxs.data_ptr(), _rows(dxs, "dxs"), sp,
+                                          dx.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_dispatch_backward")
     return dx
 
 
-def combine(ys, slot, weights, residual=None, stream=None):
+@_on_stream
+def combine(ys, slot, weights, residual=None):
     """y[t] = sum over j of weights[t, j] * ys[slot[t, j]], + residual[t]."""
-    code, stride = _matrix(ys, "ys")
-    sp = _slots(slot, ys)
-    tokens, top_k = slot.shape
-    if ys.shape[0] != tokens * top_k:
-        raise ValueError(f"ys must have tokens * top_k = {tokens * top_k} rows, got {ys.shape[0]}")
-    wp = _contiguous(weights, "weights", ys, slot.shape, torch.float32)
-    hidden, r_stride = ys.shape[1], 0
+    dev, stream, code = _start(ys, "ys", 2)
+    rows, hidden = ys.shape
+    sp, tokens, top_k = _slots(slot, rows, "ys", dev)
+    wp = _contiguous(weights, "weights", dev, _F32, (tokens, top_k))
+    rp, r_stride = None, 0
     if residual is not None:
-        _check(residual, "residual", ys, (tokens, hidden))
-        r_stride = _rows(residual, "residual")
-    L = _c.load()
-    with _On(ys, stream, (ys, slot, weights, residual)) as st:
-        y = torch.empty((tokens, hidden), dtype=ys.dtype, device=ys.device)
-        _c.check(L.muon_combine(code, tokens, hidden, top_k, ys.data_ptr(), stride, sp, wp, _ptr(residual),
-                                r_stride, y.data_ptr(), st), "muon_combine")
+        _check(residual, "residual", dev, ys.dtype, (tokens, hidden))
+        rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
+    y = _empty((tokens, hidden), dtype=ys.dtype, device=dev)
+    st = _c.load().muon_combine(code, tokens, hidden, top_k, ys.data_ptr(), _rows(ys, "ys"), sp, wp, rp, r_stride,
+                                y.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_combine")
     return y
 
 
-def combine_backward(dy, ys, slot, offsets, weights, stream=None):
+@_on_stream
+def combine_backward(dy, ys, slot, offsets, weights):
     """(dys, dweights): dys[slot[t, j]] = weights[t, j] * dy[t], zero in the rows
     that no expert owns, and dweights[t, j] = <ys[slot[t, j]], dy[t]> in fp32
     (offsets as ``dispatch`` gave them)."""
-    code, stride = _matrix(ys, "ys")
-    sp = _slots(slot, ys)
-    tokens, top_k = slot.shape
-    if ys.shape[0] != tokens * top_k:
-        raise ValueError(f"ys must have tokens * top_k = {tokens * top_k} rows, got {ys.shape[0]}")
-    _check(dy, "dy", ys, (tokens, ys.shape[1]))
-    d_stride = _rows(dy, "dy")
-    wp = _contiguous(weights, "weights", ys, slot.shape, torch.float32)
+    dev, stream, code = _start(ys, "ys", 2)
+    rows, hidden = ys.shape
+    sp, tokens, top_k = _slots(slot, rows, "ys", dev)
+    _check(dy, "dy", dev, ys.dtype, (tokens, hidden))
+    wp = _contiguous(weights, "weights", dev, _F32, (tokens, top_k))
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"offsets must be [experts + 1], got {list(offsets.shape)}")
-    op = _contiguous(offsets, "offsets", ys, offsets.shape, torch.int32)
-    L = _c.load()
-    with _On(ys, stream, (dy, ys, slot, offsets, weights)) as st:
-        dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device)
-        dwts = torch.empty(slot.shape, dtype=torch.float32, device=ys.device)
-        _c.check(L.muon_combine_backward(code, tokens, ys.shape[1], top_k, offsets.shape[0] - 1, dy.data_ptr(),
-                                         d_stride, ys.data_ptr(), stride, sp, op, wp, dys.data_ptr(),
-                                         dwts.data_ptr(), st), "muon_combine_backward")
+    op = _contiguous(offsets, "offsets", dev, _I32, offsets.shape)
+    dys = _empty((rows, hidden), dtype=ys.dtype, device=dev)
+    dwts = _empty((tokens, top_k), dtype=_F32, device=dev)
+    st = _c.load().muon_combine_backward(code, tokens, hidden, top_k, offsets.shape[0] - 1, dy.data_ptr(),
+                                         _rows(dy, "dy"), ys.data_ptr(), _rows(ys, "ys"), sp, op, wp,
+                                         dys.data_ptr(), dwts.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_combine_backward")
     return dys, dwts
 
 
