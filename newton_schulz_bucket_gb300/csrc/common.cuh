@@ -34,6 +34,28 @@ __device__ __forceinline__ bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+// Programmatic launches: a kernel launched by launch_early may start while the
+// one before it drains (once all of that one's blocks have called
+// grid_launch_next or left), and touches no memory before grid_wait returns, by
+// which time the one before it is done.  Every such kernel waits in every
+// block, so that completion carries over from launch to launch.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, fn, P(args)...);
+}
+
 // Sum over a warp with a fixed butterfly: the result depends only on the 32
 // inputs, never on timing.
 __device__ __forceinline__ float warp_sum(float v) {

@@ -57,7 +57,9 @@ struct TcProduct {
   int rows, K;              // rows form: token rows; the sum's length (GROUP_SUM: all rows)
   int M, N;                 // rows form: features (M); sum form: the output
   int tiles_m, tiles_n;     // sum form; rows form: feature tiles (tiles_m)
+  int tile_rows;            // rows form: most token rows of a tile (64, 128 or 256)
   int box_rows;             // rows form: token rows of one TMA copy
+  int stages;               // rows form: ring depth, more for smaller tiles
   int bf16, act, vec;       // vec: output rows (and the epilogue's tensors) start on 16 bytes
   void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert
   const void* bias;
@@ -69,7 +71,10 @@ struct TcProduct {
   int* err;
 };
 
-// Ring and staging of one CTA.  Rows form: BN = 0.
+// Ring and staging of one CTA.  Rows form (BN = 0): the same bytes hold 7, 9 or
+// 11 stages for tiles of up to 256, 128 or 64 tokens, so that a stream of
+// weights past few tokens has more of them in flight.
+constexpr int kMaxStages = 11;
 template <int BN>
 struct Smem {
   static constexpr int kStages = BN == 0 ? 7 : (BN == 256 ? 6 : 8);
@@ -79,12 +84,22 @@ struct Smem {
   static constexpr uint32_t kEpi = kStages * kStage;  // sum form: 4 KB a warp, 1024-byte aligned for TMA's swizzle
   static constexpr uint32_t kBars = kEpi + (BN == 0 ? 0 : kEpiWarps * 4096);  // full, empty, fix, tfull, tempty,
                                                                                // done; TMEM slot, abort flag
-  static constexpr uint32_t kTotal = kBars + 256 + 1024;  // + alignment slack
-  static_assert((3 * kStages + 5) * 8 + 8 <= 256 && kTotal <= 227 * 1024, "shared memory layout");
+  static constexpr uint32_t kTotal = kBars + 512 + 1024;  // + alignment slack
+  static_assert((3 * kMaxStages + 5) * 8 + 8 <= 512 && kTotal <= 227 * 1024, "shared memory layout");
 };
+__host__ __device__ constexpr uint32_t rows_stage_bytes(int tile_rows) { return (128 + tile_rows / 2) * BK * 2; }
+__host__ __device__ constexpr int rows_stages(int tile_rows) { return (int)(Smem<0>::kEpi / rows_stage_bytes(tile_rows)); }
+static_assert(rows_stages(256) == 7 && rows_stages(128) == 9 && rows_stages(64) == kMaxStages, "ring depths");
 
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
@@ -98,8 +113,8 @@ struct Item {
   int e, m0, n0, n_end, k0, k1, split;
 };
 
-// Token tiles of a range of n rows: as few as 256 allows, of even size in
-// steps of 32 (n > 256 (tiles - 1) >= size (tiles - 1), so none is empty).
+// Token tiles of a range of n rows: as few as tile_rows allows, of even size in
+// steps of 32 (n > tile_rows (tiles - 1) >= size (tiles - 1): none is empty).
 __device__ __forceinline__ int token_tile(int n, int tiles) { return ((n + tiles - 1) / tiles + 31) / 32 * 32; }
 // Columns of a tile's MMA.
 __device__ __forceinline__ int mma_cols(const Item& it) { return (it.n_end - it.n0 + 31) / 32 * 32; }
@@ -118,53 +133,81 @@ __device__ __forceinline__ void raster(int r, int tiles_m, int tiles_n, int& tm,
 // Walks this pair's tiles: every role of both CTAs sees the same sequence.
 template <int BN>
 struct Walk {
-  int t, step;
-  int e, lo, hi, base, cnt, tt;  // current range, its first item, item and token tile counts
+  int r, step;                // item within the current range / part, stride
+  int e, lo, hi, after;       // range, its rows, the end of the one behind it
+  int cnt, tt, size;          // its items, token tiles and their size
   __device__ __forceinline__ Walk(const TcProduct& p)
-      : t(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), base(0), cnt(0), tt(0) {}
+      : r(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), after(0), cnt(0), tt(0), size(0) {
+    if (p.mode == GROUP_NONE) {
+      after = BN == 0 ? p.rows : p.K;
+    } else {
+      hi = range_at(p, 0, BN == 0 ? p.rows : p.K);
+      after = range_at(p, 1, BN == 0 ? p.rows : p.K);
+    }
+  }
+  __device__ __forceinline__ void advance(const TcProduct& p, int most) {
+    ++e;
+    lo = hi;
+    hi = max(lo, after);
+    if (p.mode != GROUP_NONE && e + 2 <= p.experts) after = range_at(p, e + 2, most);
+  }
   __device__ __forceinline__ void part_of_sum(const TcProduct& p, int split, Item& it) {
-    const int kb = (p.K + BK - 1) / BK;
     it.split = split;
-    it.k0 = (int)((int64_t)kb * split / p.splits) * BK;
-    it.k1 = split + 1 == p.splits ? p.K : (int)((int64_t)kb * (split + 1) / p.splits) * BK;
+    it.k0 = 0;
+    it.k1 = p.K;
+    if (p.splits > 1) {  // splits * blocks of the sum stays below 2^31
+      const int kb = (p.K + BK - 1) / BK;
+      it.k0 = kb * split / p.splits * BK;
+      if (split + 1 < p.splits) it.k1 = kb * (split + 1) / p.splits * BK;
+    }
   }
   __device__ __forceinline__ bool next(const TcProduct& p, Item& it) {
     int tm, tn;
     if constexpr (BN == 0) {
-      while (t >= base + cnt) {
-        base += cnt;
-        if (++e >= (p.mode == GROUP_ROWS ? p.experts : 1)) return false;
-        lo = p.mode == GROUP_ROWS ? range_at(p, e, p.rows) : 0;
-        hi = p.mode == GROUP_ROWS ? range_at(p, e + 1, p.rows) : p.rows;
-        tt = hi > lo ? (hi - lo + 255) / 256 : 0;
+      while (r >= cnt) {
+        r -= cnt;
+        if (e + 1 >= (p.mode == GROUP_ROWS ? p.experts : 1)) { cnt = 0; e = 1 << 28; return false; }
+        advance(p, p.rows);
+        tt = (hi - lo + p.tile_rows - 1) / p.tile_rows;
         cnt = tt * p.tiles_m * p.splits;
+        size = tt ? token_tile(hi - lo, tt) : 0;
       }
-      const int per = tt * p.tiles_m, g = (t - base) / per;
-      raster(t - base - g * per, p.tiles_m, tt, tm, tn);
-      const int size = token_tile(hi - lo, tt);
+      int q = r, split = 0;
+      if (p.splits > 1) {
+        const int per = tt * p.tiles_m;
+        split = q / per;
+        q -= split * per;
+      }
+      raster(q, p.tiles_m, tt, tm, tn);
       it.e = e;
       it.m0 = tm * BM;
       it.n0 = lo + tn * size;
       it.n_end = min(hi, it.n0 + size);
-      part_of_sum(p, g, it);
+      part_of_sum(p, split, it);
     } else {
-      const int per = p.tiles_m * p.tiles_n, g = t / per;
-      if (g >= (p.mode == GROUP_SUM ? p.experts : p.splits)) return false;
-      raster(t - g * per, p.tiles_m, p.tiles_n, tm, tn);
+      const int per = p.tiles_m * p.tiles_n;
+      while (r >= cnt) {  // range or part e + 1
+        r -= cnt;
+        if (e + 1 >= (p.mode == GROUP_SUM ? p.experts : p.splits)) { cnt = 0; e = 1 << 28; return false; }
+        if (p.mode == GROUP_SUM) advance(p, p.K);
+        else ++e;
+        cnt = per;
+      }
+      raster(r, p.tiles_m, p.tiles_n, tm, tn);
       it.m0 = tm * BM;
       it.n0 = tn * BN;
       it.n_end = p.N;
       if (p.mode == GROUP_SUM) {
-        it.e = g;
+        it.e = e;
         it.split = 0;
-        it.k0 = range_at(p, g, p.K);
-        it.k1 = max(it.k0, range_at(p, g + 1, p.K));
+        it.k0 = lo;
+        it.k1 = hi;
       } else {
         it.e = 0;
-        part_of_sum(p, g, it);
+        part_of_sum(p, e, it);
       }
     }
-    t += step;
+    r += step;
     return true;
   }
 };
@@ -323,21 +366,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                 const __grid_constant__ CUtensorMap mapD, const __grid_constant__ TcProduct p) {
   using L = Smem<BN>;
-  constexpr int S = L::kStages;
+  const int S = BN == 0 ? p.stages : L::kStages;
+  const uint32_t stage_bytes = BN == 0 ? rows_stage_bytes(p.tile_rows) : L::kStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   const uint32_t bar0 = saddr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-  auto fix = [&](int s) { return bar0 + 8u * (2 * S + s); };
-  auto tfull = [&](int a) { return bar0 + 8u * (3 * S + a); };
-  auto tempty = [&](int a) { return bar0 + 8u * (3 * S + 2 + a); };
-  const uint32_t done = bar0 + 8u * (3 * S + 4);
+  auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto fix = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (3 * kMaxStages + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };
+  const uint32_t done = bar0 + 8u * (3 * kMaxStages + 4);
   constexpr bool kRows = BN == 0;
   constexpr int kAccCols = kRows ? 256 : BN;
   constexpr uint32_t kCols = 2 * kAccCols;  // two accumulators
@@ -367,87 +411,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier();  // both CTAs' barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_launch_next();
+  grid_wait();  // all that runs before this launch is done: its results may be read, its inputs overwritten
   Walk<BN> walk(p);
   Item it;
+  bool more = walk.next(p, it);
 
-  if (warp == 0) {
-    if (lane == 0) {  // ---- TMA producer (both CTAs) ----
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      while (ok && walk.next(p, it)) {
-        const int arow = it.m0 + (int)rank * 128;
-        // rows form: this CTA's half of the tile's tokens, in boxes of box_rows
-        const int half = kRows ? mma_cols(it) / 2 : BN / 2;
-        const int brow = it.n0 + (int)rank * half;
-        const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
-        const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
-        for (int k = it.k0; k < it.k1; k += BK) {
-          if (!(ok = mbar_wait(empty(s), ph ^ 1, abort_flag, p.err, 1))) break;
-          const uint32_t sa = saddr(smem + s * L::kStage), sb = sa + L::kA;
-          const bool tail = group_sum && it.k1 - k < BK;
-          uint32_t bar;  // where this CTA's copies are counted: the leader's ring, or its own helper
-          if (tail) {
+  // The producer's and the issuer's loops have to stay ahead of the MMAs (about
+  // 500 cycles a block).  Whole warps run them, so that their addresses and
+  // descriptors stay in uniform registers, and one elected lane issues.
+  if (warp == 0) {  // ---- TMA producer (both CTAs) ----
+    const uint32_t ring = saddr(smem), full_leader = map_to(full(0), 0);
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (; ok && more; more = walk.next(p, it)) {
+      const int arow = it.m0 + (int)rank * 128;
+      // rows form: this CTA's half of the tile's tokens, in boxes of box_rows
+      const int half = kRows ? mma_cols(it) / 2 : BN / 2;
+      const int brow = it.n0 + (int)rank * half;
+      const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
+      const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
+      const int ae = kRows ? it.e : 0;
+      for (int k = it.k0; k < it.k1; k += BK) {
+        if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 1))) break;
+        const uint32_t sa = ring + s * stage_bytes, sb = sa + L::kA;
+        if (elect_lane()) {
+          uint32_t bar = full_leader + 8u * s;  // where this CTA's copies are counted: the leader's ring
+          if (group_sum && it.k1 - k < BK) {    // or, for a range's last rows, its own helper
             bar = fix(s);
             mbar_expect_tx(bar, bytes);
-          } else {
-            bar = map_to(full(s), 0);
-            if (rank == 0) mbar_expect_tx(full(s), 2 * bytes);
-            else if (group_sum) mbar_arrive_cluster(bar);
+          } else if (rank == 0) {
+            mbar_expect_tx(full(s), 2 * bytes);
+          } else if (group_sum) {
+            mbar_arrive_cluster(bar);
           }
           if (AMN) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              tma_load_3d_pair(sa + c * (64 * BK * 2), &mapA, bar, arow + c * 64, k, kRows ? it.e : 0);
+            tma_load_3d_pair(sa, &mapA, bar, arow, k, ae);
+            tma_load_3d_pair(sa + 64 * BK * 2, &mapA, bar, arow + 64, k, ae);
           } else {
-            tma_load_3d_pair(sa, &mapA, bar, k, arow, it.e);
+            tma_load_3d_pair(sa, &mapA, bar, k, arow, ae);
           }
           if constexpr (kRows) {
-            for (int c = 0; c < boxes; ++c)
+            tma_load_3d_pair(sb, &mapB, bar, k, brow, 0);
+            for (int c = 1; c < boxes; ++c)
               tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, 0);
           } else {
 #pragma unroll
             for (int c = 0; c < BN / 128; ++c)
               tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, 0);
           }
-          if (++s == S) { s = 0; ph ^= 1; }
         }
-      }
-      if (!ok) {  // gave up: let the copies in flight land before the block leaves
-        const long long t0 = clock64();
-        while (clock64() - t0 < (1ll << 21)) {}
+        __syncwarp();
+        if (++s == S) { s = 0; ph ^= 1; }
       }
     }
+    if (!ok) {  // gave up: let the copies in flight land before the block leaves
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1ll << 21)) {}
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {  // ---- MMA issuer (leader only) ----
+    if (rank == 0) {  // ---- MMA issuer (leader only) ----
+      // descriptors of stage 0; a stage further is stage_bytes / 16 more in the
+      // low word, 16 steps of the sum further kStepA / kStepB more
+      const uint64_t da = AMN ? smem_desc(saddr(smem), 64 * BK * 2, 1024) : smem_desc(saddr(smem), 16, 1024);
+      const uint64_t db = kRows ? smem_desc(saddr(smem) + L::kA, 16, 1024)
+                                : smem_desc(saddr(smem) + L::kA, 64 * BK * 2, 1024);
+      constexpr uint64_t kStepA = AMN ? 2048 / 16 : 32 / 16, kStepB = kRows ? 32 / 16 : 2048 / 16;
       int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
+      uint32_t ph = 0, aph = 1;
       bool ok = true;
-      while (ok && walk.next(p, it)) {
-        if (!(ok = mbar_wait(tempty(acc), aph ^ 1, abort_flag, p.err, 2))) break;
+      for (; more; more = walk.next(p, it)) {
+        if (!(ok = mbar_wait(tempty(acc), aph, abort_flag, p.err, 2))) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
         const uint32_t idesc = instr_desc(p.bf16 ? 1u : 0u, BM, kRows ? mma_cols(it) : BN, !kRows, AMN);
+        uint32_t add = 0;  // the tile's first MMA overwrites
         for (int k = it.k0; k < it.k1; k += BK) {
           if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
           tc_fence_after();
-          const uint32_t sa = saddr(smem + s * L::kStage), sb = sa + L::kA;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = AMN ? smem_desc(sa + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sa + kk * 32, 16, 1024);
-            const uint64_t bd = !kRows ? smem_desc(sb + kk * 2048, 64 * BK * 2, 1024) : smem_desc(sb + kk * 32, 16, 1024);
-            umma_pair(d_tmem, ad, bd, idesc, k != it.k0 || kk != 0);
+          const uint64_t a = da + s * (stage_bytes >> 4), b = db + s * (stage_bytes >> 4);
+          if (elect_lane()) {
+            umma_pair(d_tmem, a, b, idesc, add);
+            if (it.k1 - k >= BK) {
+              umma_pair(d_tmem, a + kStepA, b + kStepB, idesc, 1);
+              umma_pair(d_tmem, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
+              umma_pair(d_tmem, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
+            } else {  // behind the sum's end there are only zeros: skipped
+              for (int kk = 1; kk * 16 < it.k1 - k; ++kk)
+                umma_pair(d_tmem, a + kk * kStepA, b + kk * kStepB, idesc, 1);
+            }
+            umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
           }
-          umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
+          __syncwarp();
+          add = 1;
           if (++s == S) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
-        umma_commit_pair(tfull(acc), 3);
+        if (elect_lane()) umma_commit_pair(tfull(acc), 3);
+        __syncwarp();
         if (++acc == 2) { acc = 0; aph ^= 1; }
       }
       // every MMA issued has completed before TMEM and shared memory go away
       // (waited for even after an abort, so the wait ignores the abort flag)
-      umma_commit_pair(done, 1);
+      if (elect_lane()) umma_commit_pair(done, 1);
+      __syncwarp();
       volatile int keep_waiting = 0;
       mbar_wait(done, 0, &keep_waiting, p.err, 16);
     }
@@ -456,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2; // which half of the tile's columns
     int acc = 0;
     uint32_t aph = 0;
-    while (walk.next(p, it)) {
+    for (; more; more = walk.next(p, it)) {
       if (!mbar_wait(tfull(acc), aph, abort_flag, p.err, 8)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(quarter * 32) << 16);
@@ -529,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t fph = 0;  // parity of each stage's fix barrier
     bool ok = true;
-    while (ok && walk.next(p, it)) {
+    for (; ok && more; more = walk.next(p, it)) {
       const int blocks = (it.k1 - it.k0 + BK - 1) / BK, rem = (it.k1 - it.k0) % BK;
       if (rem) {
         const int st = (s + blocks - 1) % S;
@@ -558,6 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of a split sum, in order, and runs the epilogue: output
 // [rows][cols], 8 columns a thread.  Row ranges: a row's expert by bisection.
 __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p, int rows, int cols) {
+  grid_launch_next();
+  grid_wait();
   const int64_t per_row = (cols + 7) / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= per_row * rows) return;
@@ -660,13 +730,15 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = Smem<BN>::kTotal;
   lc.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
+  lc.numAttrs = 2;
   return cudaLaunchKernelEx(&lc, fn, ma, mb, md, q);
 }
 
@@ -682,8 +754,8 @@ cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
   if (e == cudaSuccess)
     e = tc_encode_map(&mx, p.A, type, p.K, p.M, 1, p.a_m, p.M * p.a_m, 64, (uint32_t)q.box_rows);
   if (e != cudaSuccess) return e;
-  int64_t tt = (p.M + 255) / 256;
-  if (p.mode == GROUP_ROWS) tt = p.M / 256 + (p.M < p.experts ? p.M : p.experts);  // at most
+  int64_t tt = (p.M + q.tile_rows - 1) / q.tile_rows;
+  if (p.mode == GROUP_ROWS) tt = p.M / q.tile_rows + (p.M < p.experts ? p.M : p.experts);  // at most
   const int64_t items = tt * q.tiles_m * q.splits;
   return across ? launch<true, 0>(mw, mx, mx, q, items, s) : launch<false, 0>(mw, mx, mx, q, items, s);
 }
@@ -725,41 +797,49 @@ cudaError_t ops_error_word(int** err) {
   return cudaSuccess;
 }
 
-// Tile width (sum form) and parts of the sum with the least estimated time: a
-// block of 64 steps of the sum takes a pair about 0.27 us on a 256 x 256 tile
-// (0.15 us on 256 x 128, in proportion for fewer tokens, at least the 0.1 us in
-// which its weights arrive), a tile's start and end about 1 us; parts cost a
-// launch and their traffic at about 5 TB/s.
+// The tile and the parts of the sum with the least estimated time, in us on one
+// GB300.  A pair takes 0.28 us for 64 steps of the sum on 256 columns, in
+// proportion for fewer, but no less than 0.2 us (an operand of 256 rows has to
+// reach the tensor cores all the same), and about 1 us to start and end a tile.
+// All pairs together read weights at 6.2 TB/s.  Parts of the sum cost a launch
+// and their traffic.
 TilePlan tile_plan(const Product& p) {
-  const int64_t pairs = 76;
+  const int64_t pairs = num_sms() / 2;
   const int64_t kb = (p.K + BK - 1) / BK;
-  TilePlan best{0, 1, 0};
-  double best_t = 1e30;
   const bool rows = rows_form(p);
-  for (int bn : {256, 128}) {
-    if (rows && bn == 128) break;
-    int64_t tiles;
-    double per_kb = bn == 256 ? 0.27 : 0.15, blocks = (double)kb;
-    if (rows) {
-      const int64_t tm = (p.N + BM - 1) / BM;
-      int64_t tt = (p.M + 255) / 256, ranges = 1;
-      if (p.mode == GROUP_ROWS) {
-        ranges = p.M < p.experts ? p.M : p.experts;
-        tt = ranges * ((p.M / ranges + 255) / 256);
-      }
-      tiles = tm * tt;
-      const double cols = (double)p.M / tt;
-      per_kb = 0.27 * cols / 256 > 0.1 ? 0.27 * cols / 256 : 0.1;
-    } else {
-      tiles = (p.M + BM - 1) / BM * ((p.N + bn - 1) / bn);
-      if (p.mode == GROUP_SUM) { tiles *= p.experts; blocks = (double)kb / p.experts + 0.5; }
-    }
+  TilePlan best{};
+  double best_t = 1e30;
+  const auto offer = [&](int bn, int tile_rows, int64_t tiles, double cols, double blocks, double bytes) {
+    const double per_kb = 0.28 * cols / 256 > 0.2 ? 0.28 * cols / 256 : 0.2;
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && (p.mode != GROUP_NONE || kb / s < 4)) break;
-      const double waves = (double)((tiles * s + pairs - 1) / pairs);
+      const double waves = (double)((tiles * s + pairs - 1) / pairs), uneven = waves * pairs / (double)(tiles * s);
       double t = waves * (blocks / s * per_kb + 1.0);
-      if (s > 1) t += 3.0 + (double)p.M * p.N * 8.0 * s / 5e6;
-      if (t < best_t) { best_t = t; best.bn = rows ? 0 : bn; best.splits = s; }
+      const double stream = bytes / 6.2e6 * uneven;
+      if (t < stream) t = stream;
+      if (s > 1) t += 2.5 + (double)p.M * p.N * 8.0 * s / 5e6;
+      if (t < best_t * 0.98) { best_t = t; best = {bn, tile_rows, s, 0}; }
+    }
+  };
+  if (rows) {
+    const int64_t tm = (p.N + BM - 1) / BM;
+    const int64_t ranges = p.mode == GROUP_ROWS ? (p.M < p.experts ? p.M : p.experts) : 1;
+    const int64_t each = (p.M + ranges - 1) / ranges;
+    const double bytes = 2.0 * ranges * p.N * p.K;
+    for (int tr : {256, 128, 64}) {
+      const int64_t tt = (each + tr - 1) / tr;
+      const int64_t cols = ((each + tt - 1) / tt + 31) / 32 * 32;
+      // a range often has more rows than the average: not where that would
+      // need another tile
+      if (p.mode == GROUP_ROWS && tr < 256 && 2 * each > tr) continue;
+      offer(0, tr, tm * tt * ranges, (double)cols, (double)kb, bytes);
+    }
+  } else {
+    for (int bn : {256, 128}) {
+      int64_t tiles = (p.M + BM - 1) / BM * ((p.N + bn - 1) / bn);
+      double blocks = (double)kb;
+      if (p.mode == GROUP_SUM) { tiles *= p.experts; blocks = (double)kb / p.experts + 0.5; }
+      offer(bn, 0, tiles, bn, blocks, 0.0);
     }
   }
   if (best.splits > 1) best.part_bytes = (int64_t)best.splits * p.M * ((p.N + 31) / 32 * 32) * 4;
@@ -774,10 +854,11 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
     q.rows = (int)p.M;
     q.M = (int)p.N;
     q.tiles_m = (int)((p.N + BM - 1) / BM);
-    // token rows of one copy: a tile's half of them (16 to 128), so that few
-    // rows do not drag others in
-    const int64_t typical = p.mode == GROUP_ROWS ? 2 * p.M / p.experts + 1 : p.M;
-    q.box_rows = typical <= 32 ? 16 : (typical <= 64 ? 32 : (typical <= 128 ? 64 : 128));
+    q.tile_rows = t.tile_rows;
+    q.stages = rows_stages(t.tile_rows);
+    // token rows of one copy: one copy a block where it can be (copies cost more
+    // than the rows they drag along), 16 for the least tiles
+    q.box_rows = p.mode == GROUP_NONE && p.M <= 32 ? 16 : t.tile_rows / 2;
   } else {
     q.M = (int)p.M;
     q.N = (int)p.N;
@@ -795,8 +876,7 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
   cudaError_t e = t.bn == 0 ? run_rows(p, q, s) : (t.bn == 256 ? run_sum<256>(p, q, s) : run_sum<128>(p, q, s));
   if (e == cudaSuccess && t.splits > 1) {
     const int64_t n = (p.N + 7) / 8 * p.M;
-    k_linear_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(q, (int)p.M, (int)p.N);
-    e = cudaGetLastError();
+    e = launch_early(k_linear_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, q, (int)p.M, (int)p.N);
   }
   return e;
 }

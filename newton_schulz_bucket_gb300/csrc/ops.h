@@ -59,6 +59,7 @@ struct GradPrep {
 // How the tensor-core form runs a product (chosen on the host from sizes).
 struct TilePlan {
   int bn;                      // sum form (dw): columns of a pair's tile, 256 or 128; 0: rows form
+  int tile_rows;               // rows form: most token rows of a tile, 256, 128 or 64
   int splits;                  // parts of the sum, joined by a second kernel
   int64_t part_bytes;          // scratch of the parts
 };
