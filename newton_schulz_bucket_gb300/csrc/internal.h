@@ -145,9 +145,9 @@ struct TcMaps {
   CUtensorMap a_k128, a_ksq, q_k128;
   int bn_sq, bn_up;
 };
-// A 3-D tensor map over 16-bit elements [B][rows][inner] (logical extents; row
-// pitch and matrix distance in elements, multiples of 8), 128-byte swizzle,
-// zero fill outside the extents.
+// A 3-D tensor map over [B][rows][inner] elements of an NsType (logical extents;
+// row pitch and matrix distance in elements, multiples of 16 bytes), 128-byte
+// swizzle, zero fill outside the extents.
 cudaError_t tc_encode_map(CUtensorMap* m, const void* base, int ns_type, int64_t inner, int64_t rows,
                           int64_t B, int64_t pitch, int64_t batch, uint32_t box0, uint32_t box1);
 cudaError_t tc_make_maps(const KArgs& a, TcMaps* t);

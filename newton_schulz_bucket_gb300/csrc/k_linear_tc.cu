@@ -1,6 +1,12 @@
 // A layer's product on the tensor cores: D(m, n) = act(sum_k A(m, k) B(k, n) +
 // bias) + residual in fp16 / bf16 operands with fp32 sums.
 //
+// fp32 tensors.  Each operand is cut into three bf16 numbers, x = h + m + l with
+// 8 significant bits each (truncated, so the three hold all 24 bits), and the
+// product is the sum of the six partial products down to h l, m m and l h; what
+// is left out is below 2^-23 of the whole.  Six bf16 products are 4 to 5 times
+// as fast as one in fp32 FMA.
+//
 // A cluster of two CTAs computes one 256 x N tile (N <= 256) with tcgen05.mma
 // cta_group::2, as the Newton-Schulz products do: each CTA stages its 128 rows
 // of the M operand and its half of the N operand's rows in a ring of TMA tiles,
@@ -60,12 +66,13 @@ struct TcProduct {
   int tile_rows;            // rows form: most token rows of a tile (64, 128 or 256)
   int box_rows;             // rows form: token rows of one TMA copy
   int stages;               // rows form: ring depth, more for smaller tiles
-  int bf16, act, vec;       // vec: output rows (and the epilogue's tensors) start on 16 bytes
+  int type, act, vec;       // DType; vec: output rows (and the epilogue's tensors) start on 16 bytes
   void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert
   const void* bias;
   const void* residual;
   int64_t r_m;
   void* preact;
+  int first;                // first of the partial products (0 for fp32, 5 for the 16-bit types: one product)
   float* part;              // splits > 1: [splits][output rows][part_pitch] sums
   int64_t part_pitch;
   int* err;
@@ -212,16 +219,25 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ float ld16(const void* p, int64_t i, int bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-              : __half2float(static_cast<const __half*>(p)[i]);
+// Planes (0 high, 1 middle, 2 low) of the two operands in partial product i,
+// smallest products first.
+constexpr int kProducts = 6;
+__device__ __forceinline__ int plane_m(int i) { return (0x010120 >> (4 * i)) & 3; }
+__device__ __forceinline__ int plane_n(int i) { return (0x001102 >> (4 * i)) & 3; }
+
+__device__ __forceinline__ float ld_el(const void* p, int64_t i, int type) {
+  if (type == DT_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  if (type == DT_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return static_cast<const float*>(p)[i];
 }
-__device__ __forceinline__ void st16(void* p, int64_t i, float v, int bf16) {
-  if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+__device__ __forceinline__ void st_el(void* p, int64_t i, float v, int type) {
+  if (type == DT_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else if (type == DT_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else static_cast<float*>(p)[i] = v;
 }
-__device__ __forceinline__ void unpack8(const uint4& u, float* f, int bf16) {
-  if (bf16) {
+// 8 values of a 16-bit type.
+__device__ __forceinline__ void unpack8(const uint4& u, float* f, int type) {
+  if (type == DT_BF16) {
     bf16x8_to_f32(u, f);
   } else {
     const __half2* h = reinterpret_cast<const __half2*>(&u);
@@ -233,33 +249,33 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f, int bf16) {
     }
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* f, int bf16) {
-  if (bf16) return f32_to_bf16x8(f);
+__device__ __forceinline__ uint4 pack8(const float* f, int type) {
+  if (type == DT_BF16) return f32_to_bf16x8(f);
   uint4 u;
   __half2* h = reinterpret_cast<__half2*>(&u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
   return u;
 }
-template <int N>
+template <int N, bool kFast>
 __device__ __forceinline__ void activate_n(float* v, int act) {
   switch (act) {  // outside the loop over values
     case ACT_NONE: break;
     case ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_RELU);
+      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_RELU);
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_SILU);
+      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_SILU);
       break;
     case ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_GELU);
+      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_GELU);
       break;
     default:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<true>(v[i], ACT_GELU_TANH);
+      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_GELU_TANH);
   }
 }
 
@@ -280,7 +296,7 @@ __device__ __forceinline__ void write_tokens(const TcProduct& p, float* v, int e
     for (int i = 0; i < 32; ++i)
       if (i < n) z[(int64_t)i * p.M] = from_f32<T>(v[i]);
   }
-  activate_n<32>(v, p.act);
+  activate_n<32, sizeof(T) == 2>(v, p.act);
   if (p.residual) {
     const T* r = static_cast<const T*>(p.residual) + t0 * p.r_m + f;
 #pragma unroll
@@ -316,17 +332,17 @@ __device__ __forceinline__ void write_block(const TcProduct& p, const float* sw,
   if (col0 + lane < p.N) {
     const int c = col0 + lane;
     for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
-      st16(p.D, d_base + (row0 + rr) * N + c, sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)], p.bf16);
+      st_el(p.D, d_base + (row0 + rr) * N + c, sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)], p.type);
   }
   __syncwarp();  // the block is overwritten next
 }
 
 // 32 rows x 64 columns (two TMEM loads of 32) rounded into the staging block in
 // the layout of a 128-byte-swizzled TMA box.
-__device__ __forceinline__ void stage_rounded(const float* v, uint8_t* sw, int lane, bool zero, int bf16) {
+__device__ __forceinline__ void stage_rounded(const float* v, uint8_t* sw, int lane, bool zero, int type) {
   uint4* row = reinterpret_cast<uint4*>(sw + lane * 128);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) row[q ^ (lane & 7)] = zero ? make_uint4(0, 0, 0, 0) : pack8(v + 8 * q, bf16);
+  for (int q = 0; q < 8; ++q) row[q ^ (lane & 7)] = zero ? make_uint4(0, 0, 0, 0) : pack8(v + 8 * q, type);
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
@@ -348,7 +364,7 @@ __device__ __forceinline__ void write_part(const TcProduct& p, const float* sw, 
   __syncwarp();
 }
 
-// n elements of 16 bits to zero, by all epilogue threads of the grid.
+// 16-bit units from .. to - 1 to zero, by all epilogue threads of the grid.
 __device__ void zero_span(void* base, int64_t from, int64_t to, int64_t tid, int64_t n_threads) {
   uint16_t* p = static_cast<uint16_t*>(base);
   while (from < to && (reinterpret_cast<uintptr_t>(p + from) & 15)) {
@@ -432,7 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int brow = it.n0 + (int)rank * half;
       const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
       const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
-      const int ae = kRows ? it.e : 0;
+      for (int i = p.first; ok && i < kProducts; ++i) {
+      const int planes = p.first == 0 ? 3 : 1;
+      const int ae = (kRows ? it.e * planes : 0) + plane_m(i), be = plane_n(i);
       for (int k = it.k0; k < it.k1; k += BK) {
         if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 1))) break;
         const uint32_t sa = ring + s * stage_bytes, sb = sa + L::kA;
@@ -453,17 +471,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(sa, &mapA, bar, k, arow, ae);
           }
           if constexpr (kRows) {
-            tma_load_3d_pair(sb, &mapB, bar, k, brow, 0);
+            tma_load_3d_pair(sb, &mapB, bar, k, brow, be);
             for (int c = 1; c < boxes; ++c)
-              tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, 0);
+              tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, be);
           } else {
 #pragma unroll
             for (int c = 0; c < BN / 128; ++c)
-              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, 0);
+              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, be);
           }
         }
         __syncwarp();
         if (++s == S) { s = 0; ph ^= 1; }
+      }
       }
     }
     if (!ok) {  // gave up: let the copies in flight land before the block leaves
@@ -485,8 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait(tempty(acc), aph, abort_flag, p.err, 2))) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
-        const uint32_t idesc = instr_desc(p.bf16 ? 1u : 0u, BM, kRows ? mma_cols(it) : BN, !kRows, AMN);
+        const uint32_t idesc = instr_desc(p.type == DT_F16 ? 0u : 1u, BM, kRows ? mma_cols(it) : BN, !kRows, AMN);
         uint32_t add = 0;  // the tile's first MMA overwrites
+        for (int i = p.first; ok && i < kProducts; ++i)
         for (int k = it.k0; k < it.k1; k += BK) {
           if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
           tc_fence_after();
@@ -543,17 +563,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (i < n) dst[i * p.part_pitch] = v[i];
-          } else if (p.bf16) {
+          } else if (p.type == DT_BF16) {
             write_tokens<__nv_bfloat16>(p, v, it.e, f, t0, n);
-          } else {
+          } else if (p.type == DT_F16) {
             write_tokens<__half>(p, v, it.e, f, t0, n);
+          } else {
+            write_tokens<float>(p, v, it.e, f, t0, n);
           }
         }
       } else {
         uint8_t* sw = smem + L::kEpi + (warp - 2) * 4096;
         const bool zero = it.k0 >= it.k1;
         const int c0 = half * (BN / 2);  // this warp's columns of the tile
-        if (p.splits == 1 && p.vec) {
+        if (p.splits == 1 && p.vec && p.type != DT_F32) {
 #pragma unroll 1
           for (int c = c0; c < c0 + BN / 2; c += 64) {
             if (it.n0 + c >= p.N || row0 >= p.M) break;  // the same for the whole warp
@@ -564,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
             tmem_wait_ld();
-            stage_rounded(v, sw, lane, zero, p.bf16);
+            stage_rounded(v, sw, lane, zero, p.type);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tma_store_3d(&mapD, saddr(sw), it.n0 + c, row0, it.e);
@@ -574,6 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = c0; c < c0 + BN / 2; c += 32) {
             if (it.n0 + c >= p.N || row0 >= p.M) break;
+            if (p.splits == 1 && p.vec) {  // fp32: a staged block is a TMA box of 32 x 32
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+              stage_block(tacc + (uint32_t)c, reinterpret_cast<float*>(sw), lane, zero);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) tma_store_3d(&mapD, saddr(sw), it.n0 + c, row0, it.e);
+              continue;
+            }
             stage_block(tacc + (uint32_t)c, reinterpret_cast<float*>(sw), lane, zero);
             if (p.splits > 1) write_part(p, reinterpret_cast<float*>(sw), lane, row0, it.n0 + c, it.split);
             else write_block(p, reinterpret_cast<float*>(sw), lane, row0, it.n0 + c, d_base);
@@ -587,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!kRows && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (p.mode == GROUP_ROWS) {  // rows of no expert
-      const int64_t from = (int64_t)range_at(p, p.experts, p.rows) * p.M, to = (int64_t)p.rows * p.M;
+      const int64_t halves = p.type == DT_F32 ? 2 : 1;  // 16-bit units of an element
+      const int64_t from = halves * range_at(p, p.experts, p.rows) * p.M, to = halves * p.rows * p.M;
       const int64_t tid = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 64;
       const int64_t n_threads = (int64_t)gridDim.x * (32 * kEpiWarps);
       zero_span(p.D, from, to, tid, n_threads);
@@ -599,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (; ok && more; more = walk.next(p, it)) {
       const int blocks = (it.k1 - it.k0 + BK - 1) / BK, rem = (it.k1 - it.k0) % BK;
+      for (int i = p.first; ok && i < kProducts; ++i) {
       if (rem) {
         const int st = (s + blocks - 1) % S;
         if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32))) break;
@@ -612,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_release_cluster(map_to(full(st), 0));
       }
       s = (s + blocks) % S;
+      }
     }
   }
   tc_fence_before();
@@ -653,35 +687,73 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
   }
   const int n = (int)min((int64_t)8, cols - c);
   const int64_t bi = (int64_t)e * cols + c;
-  if (p.vec && n == 8) {
+  if (p.vec && n == 8 && p.type != DT_F32) {
     float b[8];
     if (p.bias) {
-      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + bi), b, p.bf16);
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + bi), b, p.type);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    if (p.preact) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * cols + c) = pack8(v, p.bf16);
-    activate_n<8>(v, p.act);
+    if (p.preact) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.preact) + row * cols + c) = pack8(v, p.type);
+    activate_n<8, true>(v, p.act);
     if (p.residual) {
-      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c), b, p.bf16);
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) + row * p.r_m + c), b, p.type);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * cols + c) = pack8(v, p.bf16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * cols + c) = pack8(v, p.type);
     return;
   }
   for (int k = 0; k < n; ++k) {
     float z = v[k];
-    if (p.bias) z += ld16(p.bias, bi + k, p.bf16);
-    if (p.preact) st16(p.preact, row * cols + c + k, z, p.bf16);
-    z = activate<true>(z, p.act);
-    if (p.residual) z += ld16(p.residual, row * p.r_m + c + k, p.bf16);
-    st16(p.D, row * cols + c + k, z, p.bf16);
+    if (p.bias) z += ld_el(p.bias, bi + k, p.type);
+    if (p.preact) st_el(p.preact, row * cols + c + k, z, p.type);
+    z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
+    if (p.residual) z += ld_el(p.residual, row * p.r_m + c + k, p.type);
+    st_el(p.D, row * cols + c + k, z, p.type);
   }
+}
+
+// fp32 rows into three bf16 planes: dst [batch][3][rows][pitch], zeros in the
+// padding.  Truncation leaves remainders that are exact in fp32; a non-finite
+// value goes whole into the high plane.
+__global__ void __launch_bounds__(256) k_split_rows(const float* src, int64_t stride, int64_t batch_stride,
+                                                    uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols) {
+  grid_launch_next();
+  grid_wait();
+  const int64_t r = blockIdx.x, b = blockIdx.z;
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= pitch) return;
+  const float* s = src + b * batch_stride + r * stride + c;
+  float f[8];
+  if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
+    u4_to_f4x2(reinterpret_cast<const uint4*>(s)[0], reinterpret_cast<const uint4*>(s)[1], f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? s[i] : 0.f;
+  }
+  uint16_t h[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v = f[i];
+    const bool finite = fabsf(v) < __int_as_float(0x7f800000);
+    if (v != v) v = __int_as_float(0x7fc00000);  // a NaN whose high half is one too
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+      h[k][i] = (uint16_t)(top >> 16);
+      v = finite ? v - __uint_as_float(top) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<uint4*>(dst + ((b * 3 + k) * rows + r) * pitch + c) = *reinterpret_cast<const uint4*>(h[k]);
 }
 
 __global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t stride, int64_t batch_stride,
                                                   uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols) {
+  grid_launch_next();
+  grid_wait();
   const int64_t r = blockIdx.x, b = blockIdx.z;
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
   if (c >= pitch) return;
@@ -702,9 +774,12 @@ int num_sms() {
   return n;
 }
 
-bool aligned_rows(const void* p, int64_t stride) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+bool aligned_rows(const void* p, int64_t stride, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % (type == DT_F32 ? 4 : 8) == 0;
 }
+// Operands are bf16 planes for fp32.
+int operand_type(const TcProduct& q) { return q.type == DT_F16 ? NS_F16 : NS_BF16; }
+int planes(const TcProduct& q) { return q.type == DT_F32 ? 3 : 1; }
 
 // The kernel with its function attributes set (once per device).
 template <bool AMN, int BN>
@@ -744,15 +819,15 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
 
 // Rows form of D[p.M rows][p.N features]: M operand p.B (the weights).
 cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
-  const int type = q.bf16 ? NS_BF16 : NS_F16;
-  const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
+  const int type = operand_type(q), np = planes(q);
+  const int64_t mats = np * (p.mode == GROUP_ROWS ? p.experts : 1);
   const bool across = p.b_k != 1;  // weights stored across the sum
   const int64_t between = mats > 1 ? p.b_e : (across ? p.K * p.b_k : p.N * p.b_n);
   CUtensorMap mw, mx;
   cudaError_t e = across ? tc_encode_map(&mw, p.B, type, p.N, p.K, mats, p.b_k, between, 64, 64)
                          : tc_encode_map(&mw, p.B, type, p.K, p.N, mats, p.b_n, between, 64, 128);
   if (e == cudaSuccess)
-    e = tc_encode_map(&mx, p.A, type, p.K, p.M, 1, p.a_m, p.M * p.a_m, 64, (uint32_t)q.box_rows);
+    e = tc_encode_map(&mx, p.A, type, p.K, p.M, np, p.a_m, p.M * p.a_m, 64, (uint32_t)q.box_rows);
   if (e != cudaSuccess) return e;
   int64_t tt = (p.M + q.tile_rows - 1) / q.tile_rows;
   if (p.mode == GROUP_ROWS) tt = p.M / q.tile_rows + (p.M < p.experts ? p.M : p.experts);  // at most
@@ -762,13 +837,15 @@ cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
 
 template <int BN>
 cudaError_t run_sum(const Product& p, const TcProduct& q, cudaStream_t s) {
-  const int type = q.bf16 ? NS_BF16 : NS_F16;
+  const int type = operand_type(q), np = planes(q);
   const int64_t mats = p.mode == GROUP_SUM ? p.experts : 1;
   CUtensorMap ma, mb, md;
-  cudaError_t e = tc_encode_map(&ma, p.A, type, p.M, p.K, 1, p.a_k, p.K * p.a_k, 64, 64);
-  if (e == cudaSuccess) e = tc_encode_map(&mb, p.B, type, p.N, p.K, 1, p.b_k, p.K * p.b_k, 64, 64);
+  cudaError_t e = tc_encode_map(&ma, p.A, type, p.M, p.K, np, p.a_k, p.K * p.a_k, 64, 64);
+  if (e == cudaSuccess) e = tc_encode_map(&mb, p.B, type, p.N, p.K, np, p.b_k, p.K * p.b_k, 64, 64);
   md = mb;
-  if (e == cudaSuccess && q.vec) e = tc_encode_map(&md, p.D, type, p.N, p.M, mats, p.N, p.M * p.N, 64, 32);
+  if (e == cudaSuccess && q.vec)
+    e = tc_encode_map(&md, p.D, q.type == DT_F32 ? NS_F32 : type, p.N, p.M, mats, p.N, p.M * p.N,
+                      q.type == DT_F32 ? 32 : 64, 32);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)q.tiles_m * q.tiles_n * (p.mode == GROUP_SUM ? p.experts : q.splits);
   return launch<true, BN>(ma, mb, md, q, items, s);
@@ -810,7 +887,7 @@ TilePlan tile_plan(const Product& p) {
   TilePlan best{};
   double best_t = 1e30;
   const auto offer = [&](int bn, int tile_rows, int64_t tiles, double cols, double blocks, double bytes) {
-    const double per_kb = 0.28 * cols / 256 > 0.2 ? 0.28 * cols / 256 : 0.2;
+    const double per_kb = (p.dtype == DT_F32 ? 6 : 1) * (0.28 * cols / 256 > 0.2 ? 0.28 * cols / 256 : 0.2);
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && (p.mode != GROUP_NONE || kb / s < 4)) break;
       const double waves = (double)((tiles * s + pairs - 1) / pairs), uneven = waves * pairs / (double)(tiles * s);
@@ -825,7 +902,7 @@ TilePlan tile_plan(const Product& p) {
     const int64_t tm = (p.N + BM - 1) / BM;
     const int64_t ranges = p.mode == GROUP_ROWS ? (p.M < p.experts ? p.M : p.experts) : 1;
     const int64_t each = (p.M + ranges - 1) / ranges;
-    const double bytes = 2.0 * ranges * p.N * p.K;
+    const double bytes = (p.dtype == DT_F32 ? 12.0 : 2.0) * ranges * p.N * p.K;
     for (int tr : {256, 128, 64}) {
       const int64_t tt = (each + tr - 1) / tr;
       const int64_t cols = ((each + tt - 1) / tt + 31) / 32 * 32;
@@ -865,11 +942,12 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
     q.tiles_m = (int)((p.M + BM - 1) / BM);
     q.tiles_n = (int)((p.N + t.bn - 1) / t.bn);
   }
-  q.bf16 = p.dtype == DT_BF16;
+  q.type = p.dtype;
+  q.first = p.dtype == DT_F32 ? 0 : kProducts - 1;
   q.act = p.act;
   q.D = p.D; q.bias = p.bias; q.residual = p.residual; q.r_m = p.r_m; q.preact = p.preact;
-  q.vec = aligned_rows(p.D, p.N) && (!p.bias || aligned_rows(p.bias, p.N)) &&
-          (!p.residual || aligned_rows(p.residual, p.r_m)) && (!p.preact || aligned_rows(p.preact, p.N));
+  q.vec = aligned_rows(p.D, p.N, q.type) && (!p.bias || aligned_rows(p.bias, p.N, q.type)) &&
+          (!p.residual || aligned_rows(p.residual, p.r_m, q.type)) && (!p.preact || aligned_rows(p.preact, p.N, q.type));
   q.part = part;
   q.part_pitch = (p.N + 31) / 32 * 32;
   q.err = p.err;
@@ -884,9 +962,15 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
 cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
                             int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
   const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)batch);
-  k_pad_rows<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(src), stride, batch_stride,
-                                  static_cast<uint16_t*>(dst), pitch, rows, cols);
-  return cudaGetLastError();
+  return launch_early(k_pad_rows, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src), stride, batch_stride,
+                      static_cast<uint16_t*>(dst), pitch, rows, cols);
+}
+
+cudaError_t launch_split_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
+                              int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
+  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)batch);
+  return launch_early(k_split_rows, grid, dim3(256), 0, s, static_cast<const float*>(src), stride, batch_stride,
+                      static_cast<uint16_t*>(dst), pitch, rows, cols);
 }
 
 }  // namespace muon

@@ -164,15 +164,23 @@ Product dw_product(const muon_linear_args* a, const void* x, int64_t x_stride, c
   return p;
 }
 
-// An operand of the tensor-core form: as it is where TMA can read it (base and
-// row pitch multiples of 16 bytes), else a copy with padded rows in scratch.
-// (r, c) strides of the operand are (stride, 1) over rows x cols, batch apart.
+// An operand of the tensor-core form.  16-bit types: as it is where TMA can read
+// it (base and row pitch multiples of 16 bytes), else a copy with padded rows in
+// scratch.  fp32: its three bf16 planes in scratch.  (r, c) strides of the
+// operand are (stride, 1) over rows x cols, batch apart.
 struct Operand {
   const void* p;
   int64_t stride, batch_stride;
 };
-Operand tma_operand(Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch, cudaStream_t s,
-                    cudaError_t* e) {
+Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch,
+                    cudaStream_t s, cudaError_t* e) {
+  if (dtype == DT_F32) {
+    const int64_t pitch = (cols + 7) / 8 * 8;
+    void* dst = c.take((size_t)(batch * 3 * rows * pitch * 2));
+    if (launch && *e == cudaSuccess)
+      *e = launch_split_rows(o.p, o.stride, o.batch_stride, dst, pitch, rows, cols, batch, s);
+    return {dst, pitch, rows * pitch};
+  }
   const bool ok = (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
                   (batch == 1 || o.batch_stride % 8 == 0);
   if (ok) return o;
@@ -182,21 +190,24 @@ Operand tma_operand(Operand o, int64_t rows, int64_t cols, int64_t batch, Carve&
   return {dst, pitch, rows * pitch};
 }
 
-// One product: fp32 in FMA, 16-bit types on the tensor cores.
-cudaError_t run_product(Product p, Carve& c, bool launch, cudaStream_t s) {
-  if (p.dtype == DT_F32) return launch ? launch_linear_simt(p, s) : cudaSuccess;
+// One product.  `ready` operands went through tma_operand already.
+cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool launch, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const bool a_along = p.a_k == 1, b_along = p.b_k == 1;
   const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
-  const Operand a = tma_operand({p.A, a_along ? p.a_m : p.a_k, 0}, a_along ? p.M : p.K, a_along ? p.K : p.M, 1, c,
-                                launch, s, &e);
-  const Operand b = tma_operand({p.B, b_along ? p.b_n : p.b_k, p.b_e}, b_along ? p.N : p.K, b_along ? p.K : p.N, mats,
-                                c, launch, s, &e);
-  p.A = a.p;
-  (a_along ? p.a_m : p.a_k) = a.stride;
-  p.B = b.p;
-  (b_along ? p.b_n : p.b_k) = b.stride;
-  p.b_e = b.batch_stride;
+  if (!a_ready) {
+    const Operand a = tma_operand(p.dtype, {p.A, a_along ? p.a_m : p.a_k, 0}, a_along ? p.M : p.K,
+                                  a_along ? p.K : p.M, 1, c, launch, s, &e);
+    p.A = a.p;
+    (a_along ? p.a_m : p.a_k) = a.stride;
+  }
+  if (!b_ready) {
+    const Operand b = tma_operand(p.dtype, {p.B, b_along ? p.b_n : p.b_k, p.b_e}, b_along ? p.N : p.K,
+                                  b_along ? p.K : p.N, mats, c, launch, s, &e);
+    p.B = b.p;
+    (b_along ? p.b_n : p.b_k) = b.stride;
+    p.b_e = b.batch_stride;
+  }
   const TilePlan t = tile_plan(p);
   float* part = t.part_bytes ? static_cast<float*>(c.take((size_t)t.part_bytes)) : nullptr;
   if (!launch || e != cudaSuccess) return e;
@@ -207,7 +218,7 @@ cudaError_t run_product(Product p, Carve& c, bool launch, cudaStream_t s) {
 muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, bool launch, cudaStream_t s) {
   if (!backward) {
     if (a->rows == 0) return MUON_OK;
-    return cuda_status("muon_linear", run_product(forward_product(a), c, launch, s));
+    return cuda_status("muon_linear", run_product(forward_product(a), false, false, c, launch, s));
   }
   const char* what = "muon_linear_backward";
   const int64_t b = dtype_size(a->dtype);
@@ -232,12 +243,11 @@ muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, boo
   if (launch && (act || a->db)) e = launch_grad_prep(g, s);
   Operand dz{act ? g.dz : a->dy, act ? g.dz_stride : a->dy_stride, 0};
   Operand x{a->x, a->x_stride, 0};
-  if (a->dtype != DT_F32) {  // padded once for both products
-    if (products) dz = tma_operand(dz, a->rows, a->out, 1, c, launch, s, &e);
-    if (a->dw) x = tma_operand(x, a->rows, a->in, 1, c, launch, s, &e);
-  }
-  if (a->dx && e == cudaSuccess) e = run_product(dx_product(a, dz.p, dz.stride), c, launch, s);
-  if (a->dw && e == cudaSuccess) e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), c, launch, s);
+  if (products) dz = tma_operand(a->dtype, dz, a->rows, a->out, 1, c, launch, s, &e);  // once for both products
+  if (a->dw) x = tma_operand(a->dtype, x, a->rows, a->in, 1, c, launch, s, &e);
+  if (a->dx && e == cudaSuccess) e = run_product(dx_product(a, dz.p, dz.stride), true, false, c, launch, s);
+  if (a->dw && e == cudaSuccess)
+    e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), true, true, c, launch, s);
   return cuda_status(what, e);
 }
 

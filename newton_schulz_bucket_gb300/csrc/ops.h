@@ -68,11 +68,13 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
 // 16-bit rows copied to a pitch that TMA can read: rows of every matrix.
 cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
                             int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
+// fp32 rows as three bf16 planes: dst [batch][3][rows][pitch].
+cudaError_t launch_split_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
+                              int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
 cudaError_t ops_error_word(int** err);  // device address of the error word of the current device
 
 constexpr int kGradChunk = 128;  // rows of one partial column sum
 
-cudaError_t launch_linear_simt(const Product& p, cudaStream_t s);
 cudaError_t launch_grad_prep(const GradPrep& g, cudaStream_t s);
 
 struct GateArgs {
