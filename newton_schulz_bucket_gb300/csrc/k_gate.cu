@@ -24,6 +24,8 @@ template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kWarps) k_gate(GateArgs g) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  grid_launch_next();
+  grid_wait();
   if (t >= g.tokens) return;
   const T* row = static_cast<const T*>(g.logits) + t * g.stride;
   float v[NV], w[NV];  // logits; logits still to choose from
@@ -73,6 +75,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate_backward(GateArgs g) {
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  grid_launch_next();
+  grid_wait();
   if (t >= g.tokens) return;
   float* grad = smem + warp * 2 * g.experts;      // g per expert
   float* chosen = grad + g.experts;               // 1 where chosen
@@ -122,9 +126,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate_backward(GateArgs g) {
 template <typename T, int NV>
 cudaError_t run_nv(const GateArgs& g, bool backward, cudaStream_t s) {
   const unsigned blocks = (unsigned)((g.tokens + kWarps - 1) / kWarps);
-  if (backward) k_gate_backward<T, NV><<<blocks, 32 * kWarps, sizeof(float) * 2 * kWarps * g.experts, s>>>(g);
-  else k_gate<T, NV><<<blocks, 32 * kWarps, 0, s>>>(g);
-  return cudaGetLastError();
+  const dim3 grid(blocks), block(32 * kWarps);
+  if (backward)
+    return launch_early(k_gate_backward<T, NV>, grid, block, sizeof(float) * 2 * kWarps * g.experts, s, g);
+  return launch_early(k_gate<T, NV>, grid, block, 0, s, g);
 }
 
 template <typename T>

@@ -50,6 +50,8 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int col_blocks) {
   constexpr bool kFast = sizeof(T) == 2;
   __shared__ float red[kRowLanes][kLanes * VEC];
+  grid_launch_next();
+  grid_wait();
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int64_t chunk = blockIdx.x / col_blocks;
   const int64_t col = ((int64_t)(blockIdx.x % col_blocks) * kLanes + lane) * VEC;
@@ -109,6 +111,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_grad_bias(GradPrep g, int col_blocks) {
   const int64_t col = (int64_t)(blockIdx.x % col_blocks) * 256 + threadIdx.x;
   const int e = blockIdx.x / col_blocks;
+  grid_launch_next();
+  grid_wait();
   if (col >= g.cols) return;
   const int64_t lo = off_at(g, e), hi = off_at(g, e + 1);
   float sum = 0.f;
@@ -122,16 +126,15 @@ __global__ void __launch_bounds__(256) k_grad_bias(GradPrep g, int col_blocks) {
 }
 
 template <typename T, int VEC>
-void prep(const GradPrep& g, cudaStream_t s) {
+cudaError_t prep(const GradPrep& g, cudaStream_t s) {
   const int cb = (int)((g.cols + kLanes * VEC - 1) / (kLanes * VEC));
-  const unsigned grid = (unsigned)((g.rows + kGradChunk - 1) / kGradChunk * cb);
-  const int threads = kLanes * kRowLanes;
+  const dim3 grid((unsigned)((g.rows + kGradChunk - 1) / kGradChunk * cb)), block(kLanes * kRowLanes);
   switch (g.act) {
-    case ACT_RELU: k_grad_prep<T, VEC, ACT_RELU><<<grid, threads, 0, s>>>(g, cb); break;
-    case ACT_SILU: k_grad_prep<T, VEC, ACT_SILU><<<grid, threads, 0, s>>>(g, cb); break;
-    case ACT_GELU: k_grad_prep<T, VEC, ACT_GELU><<<grid, threads, 0, s>>>(g, cb); break;
-    case ACT_GELU_TANH: k_grad_prep<T, VEC, ACT_GELU_TANH><<<grid, threads, 0, s>>>(g, cb); break;
-    default: k_grad_prep<T, VEC, ACT_NONE><<<grid, threads, 0, s>>>(g, cb);
+    case ACT_RELU: return launch_early(k_grad_prep<T, VEC, ACT_RELU>, grid, block, 0, s, g, cb);
+    case ACT_SILU: return launch_early(k_grad_prep<T, VEC, ACT_SILU>, grid, block, 0, s, g, cb);
+    case ACT_GELU: return launch_early(k_grad_prep<T, VEC, ACT_GELU>, grid, block, 0, s, g, cb);
+    case ACT_GELU_TANH: return launch_early(k_grad_prep<T, VEC, ACT_GELU_TANH>, grid, block, 0, s, g, cb);
+    default: return launch_early(k_grad_prep<T, VEC, ACT_NONE>, grid, block, 0, s, g, cb);
   }
 }
 
@@ -142,13 +145,11 @@ cudaError_t run(const GradPrep& g, cudaStream_t s) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % V == 0;
   };
   // 16-byte pieces where every row of every tensor starts on 16 bytes
-  if (g.cols % V == 0 && ok(g.dy, g.dy_stride) && ok(g.z, g.cols) && ok(g.dz, g.dz_stride)) prep<T, V>(g, s);
-  else prep<T, 1>(g, s);
-  cudaError_t e = cudaGetLastError();
+  const bool vec = g.cols % V == 0 && ok(g.dy, g.dy_stride) && ok(g.z, g.cols) && ok(g.dz, g.dz_stride);
+  cudaError_t e = vec ? prep<T, V>(g, s) : prep<T, 1>(g, s);
   if (e == cudaSuccess && g.db) {
     const int cb = (int)((g.cols + 255) / 256);
-    k_grad_bias<T><<<(unsigned)cb * (g.experts ? g.experts : 1), 256, 0, s>>>(g, cb);
-    e = cudaGetLastError();
+    e = launch_early(k_grad_bias<T>, dim3((unsigned)cb * (g.experts ? g.experts : 1)), dim3(256), 0, s, g, cb);
   }
   return e;
 }

@@ -1,13 +1,16 @@
 // Token rows into expert order and back, and the gradients of both.
 //
 // dispatch: a stable counting sort of the assignments by expert.  Blocks of
-// kSortChunk assignments count their experts, one block turns the counts into
-// first rows (offsets, and per chunk), and the blocks place their assignments
-// in order; then each token's row is read once and written to its top_k rows.
+// kSortChunk assignments count their experts, a scan turns the counts into
+// first rows, and the blocks place their assignments in order; then each token's
+// row is read once and written to its top_k rows.  Up to kSortChunk assignments
+// take one launch.
 // combine and the gradients go token by token the other way: a token's row is
 // held in registers while its top_k expert rows stream by, so every byte
 // crosses HBM once.  No atomics on results: slots, sums and dot products are
 // the same bits every time.
+#include <type_traits>
+
 #include "common.cuh"
 #include "ops.h"
 
@@ -25,6 +28,8 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i) {
 
 __global__ void __launch_bounds__(1024) k_sort_count(SortArgs a, int64_t n) {
   extern __shared__ int hist[];
+  grid_launch_next();
+  grid_wait();
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int64_t i = (int64_t)blockIdx.x * kSortChunk + threadIdx.x;
@@ -35,54 +40,70 @@ __global__ void __launch_bounds__(1024) k_sort_count(SortArgs a, int64_t n) {
     a.counts[(int64_t)blockIdx.x * a.experts + k] = hist[k];
 }
 
-// counts[c][e] becomes the row of the first assignment of chunk c to e.
+// counts[c][e] becomes the number of e's assignments before chunk c, total[e]
+// that of all.  A block takes 32 experts (one a lane, so that loads run along
+// the table's rows) and each of its 32 warps a run of chunks.
 __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs a, int chunks) {
-  __shared__ int total[1024 + 1];
+  grid_launch_next();
+  grid_wait();
+  __shared__ int sum[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = warp; e < a.experts; e += 32) {
-    int sum = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-      const int c = c0 + lane;
-      int v = c < chunks ? a.counts[(int64_t)c * a.experts + e] : 0;
-      const int own = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (c < chunks) a.counts[(int64_t)c * a.experts + e] = sum + v - own;
-      sum += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) total[e] = sum;
+  const int e = blockIdx.x * 32 + lane;
+  const bool live = e < a.experts;
+  const int c0 = (int)((int64_t)chunks * warp / 32), c1 = (int)((int64_t)chunks * (warp + 1) / 32);
+  int* col = a.counts + e;
+  int s = 0;
+  if (live) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) s += col[(int64_t)c * a.experts];
   }
+  sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-    int base = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int v = e < a.experts ? total[e] : 0;
-      const int own = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (e < a.experts) a.offsets[e] = total[e] = base + v - own;
-      base += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) a.offsets[a.experts] = base;
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += sum[w][lane];
+  if (!live) return;
+  for (int c = c0; c < c1; ++c) {
+    const int n = col[(int64_t)c * a.experts];
+    col[(int64_t)c * a.experts] = before;
+    before += n;
   }
+  if (warp == 31) a.total[e] = before;
+}
+
+// Exclusive prefix of v over a block of 1024 threads (warp totals in w).
+__device__ __forceinline__ int block_prefix(int v, int* w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) w[warp] = incl;
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < (int64_t)chunks * a.experts; i += blockDim.x)
-    a.counts[i] += total[i % a.experts];
+  int before = 0;
+  for (int k = 0; k < warp; ++k) before += w[k];
+  return before + incl - v;
 }
 
 __global__ void __launch_bounds__(1024) k_sort_place(SortArgs a, int64_t n) {
   extern __shared__ int next[];
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-    next[e] = a.counts[(int64_t)blockIdx.x * a.experts + e];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * kSortChunk + threadIdx.x;
+  __shared__ int warps[32];
+  grid_launch_next();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  grid_wait();
+  {
+    const int count = tid < a.experts ? a.total[tid] : 0;
+    const int first = block_prefix(count, warps);  // the expert's first row
+    if (tid < a.experts) {
+      next[tid] = first + (n ? a.counts[(int64_t)blockIdx.x * a.experts + tid] : 0);
+      if (blockIdx.x == 0) {
+        a.offsets[tid] = first;
+        if (tid == a.experts - 1) a.offsets[a.experts] = first + count;
+      }
+    }
+  }
+  const int64_t i = (int64_t)blockIdx.x * kSortChunk + tid;
   const int e = i < n ? expert_of(a, i) : -1;
   const unsigned same = __match_any_sync(0xffffffffu, e);
   const int before = __popc(same & ((1u << lane) - 1));
@@ -100,124 +121,225 @@ __global__ void __launch_bounds__(1024) k_sort_place(SortArgs a, int64_t n) {
 
 // ---- rows ----
 
-// 16 bytes of T as floats, or one element.
+// 16 bytes of T, or one element, as floats.
 template <typename T, bool VEC>
 struct Piece {
   static constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
   float f[N];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const T* h = reinterpret_cast<const T*>(&u);
+  static __device__ __forceinline__ Raw fetch(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void open(const Raw& u) {
+    const T* h = reinterpret_cast<const T*>(&u);
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = to_f32(h[i]);
-    } else {
-      f[0] = to_f32(*p);
-    }
+    for (int i = 0; i < N; ++i) f[i] = to_f32(h[i]);
   }
+  __device__ __forceinline__ void load(const T* p) { open(fetch(p)); }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (VEC) {
-      uint4 u;
-      T* h = reinterpret_cast<T*>(&u);
+    Raw u;
+    T* h = reinterpret_cast<T*>(&u);
 #pragma unroll
-      for (int i = 0; i < N; ++i) h[i] = from_f32<T>(f[i]);
-      *reinterpret_cast<uint4*>(p) = u;
-    } else {
-      *p = from_f32<T>(f[0]);
-    }
+    for (int i = 0; i < N; ++i) h[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<Raw*>(p) = u;
   }
 };
 
-constexpr int kRowThreads = 256;
 constexpr int kMaxTopK = 32;
+constexpr int kTogether = 8;  // expert rows a thread has in flight
+
+// A block works on one token's rows, or on one of gridDim.y shares of their
+// pieces where the tokens are too few to fill the GPU.
+struct Span {
+  int64_t h, end, step;
+};
+template <int N>
+__device__ __forceinline__ Span my_span(int64_t hidden) {
+  const int64_t pieces = hidden / N, per = (pieces + gridDim.y - 1) / gridDim.y;
+  const int64_t p0 = per * blockIdx.y, p1 = min(p0 + per, pieces);
+  return {(p0 + threadIdx.x) * N, p1 * N, (int64_t)blockDim.x * N};
+}
+
+// x[t] to its rows; the block's share of the rows that no expert owns to zero.
+template <typename T, bool VEC>
+__device__ __forceinline__ void spread_row(const SortArgs& a, int64_t t, const int* slot, int64_t owned) {
+  constexpr int N = Piece<T, VEC>::N;
+  const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
+  T* xs = static_cast<T*>(a.xs);
+  const int64_t r0 = t * a.top_k;
+  for (Span s = my_span<N>(a.hidden); s.h < s.end; s.h += s.step) {
+    Piece<T, VEC> v, zero{};
+    v.load(x + s.h);
+    for (int j = 0; j < a.top_k; ++j)
+      if (slot[j] >= 0) v.store(xs + (int64_t)slot[j] * a.hidden + s.h);
+    for (int j = a.top_k - 1; j >= 0 && r0 + j >= owned; --j) zero.store(xs + (r0 + j) * a.hidden + s.h);
+  }
+}
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_gather(SortArgs a) {
-  constexpr int N = Piece<T, VEC>::N;
+__global__ void __launch_bounds__(256) k_gather(SortArgs a) {
   __shared__ int slot[kMaxTopK];
+  grid_launch_next();
+  grid_wait();
   const int64_t t = blockIdx.x;
   if (threadIdx.x < a.top_k) slot[threadIdx.x] = a.slot[t * a.top_k + threadIdx.x];
   const int64_t owned = a.offsets[a.experts];
   __syncthreads();
-  const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
-  T* xs = static_cast<T*>(a.xs);
-  for (int64_t h = (int64_t)threadIdx.x * N; h < a.hidden; h += kRowThreads * N) {
-    Piece<T, VEC> v, zero{};
-    v.load(x + h);
-    for (int j = 0; j < a.top_k; ++j) {
-      if (slot[j] >= 0) v.store(xs + (int64_t)slot[j] * a.hidden + h);
-      const int64_t r = t * a.top_k + j;  // this block clears its share of the rows that no expert owns
-      if (r >= owned) zero.store(xs + r * a.hidden + h);
+  spread_row<T, VEC>(a, t, slot, owned);
+}
+
+// dispatch in one launch, for at most kSortChunk assignments: every block looks
+// at all of them and counts its token's slots (assignments to lower experts, or
+// to the same one earlier) instead of sorting.  Block row `tokens` does the
+// offsets.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_dispatch_small(SortArgs a) {
+  __shared__ int ex[kSortChunk], hist[1024], slot[kMaxTopK], valid;
+  const int n = (int)(a.tokens * a.top_k), tid = threadIdx.x;
+  grid_launch_next();
+  grid_wait();
+  if (tid < kMaxTopK) slot[tid] = 0;
+  if (tid == 0) valid = 0;
+  for (int i = tid; i < n; i += blockDim.x) ex[i] = expert_of(a, i);
+  __syncthreads();
+  const int64_t t = blockIdx.x;
+  if (t == a.tokens) {
+    if (blockIdx.y) return;
+    for (int e = tid; e < a.experts; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += blockDim.x)
+      if (ex[i] >= 0) atomicAdd(&hist[ex[i]], 1);
+    __syncthreads();
+    if (tid >= 32) return;
+    int base = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      const int own = e0 + tid < a.experts ? hist[e0 + tid] : 0;
+      int incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (tid >= o) incl += u;
+      }
+      if (e0 + tid < a.experts) a.offsets[e0 + tid] = base + incl - own;
+      base += __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (tid == 0) a.offsets[a.experts] = base;
+    return;
   }
+  const int i0 = (int)t * a.top_k;
+  int live = 0;
+  for (int i = tid; i < n; i += blockDim.x) live += ex[i] >= 0;
+  if (live) atomicAdd(&valid, live);  // whole numbers
+  for (int j = 0; j < a.top_k; ++j) {
+    const int e = ex[i0 + j];
+    int c = 0;
+    for (int i = tid; i < n; i += blockDim.x) c += ex[i] >= 0 && (ex[i] < e || (ex[i] == e && i < i0 + j));
+    if (c) atomicAdd(&slot[j], c);
+  }
+  __syncthreads();
+  if (tid < a.top_k) {
+    if (ex[i0 + tid] < 0) slot[tid] = -1;
+    if (blockIdx.y == 0) a.slot[i0 + tid] = slot[tid];
+  }
+  __syncthreads();
+  if (a.xs) spread_row<T, VEC>(a, t, slot, valid);
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_combine(SortArgs a) {
+__global__ void __launch_bounds__(256) k_combine(SortArgs a) {
   constexpr int N = Piece<T, VEC>::N;
   __shared__ int slot[kMaxTopK];
   __shared__ float wt[kMaxTopK];
+  grid_launch_next();
+  grid_wait();
   const int64_t t = blockIdx.x, rows = a.tokens * a.top_k;
-  if (threadIdx.x < a.top_k) {
-    const int s = a.slot[t * a.top_k + threadIdx.x];
+  if (threadIdx.x < kMaxTopK) {
+    const bool in = threadIdx.x < a.top_k;
+    const int s = in ? a.slot[t * a.top_k + threadIdx.x] : -1;
     slot[threadIdx.x] = s < rows ? s : -1;
-    wt[threadIdx.x] = a.weights ? a.weights[t * a.top_k + threadIdx.x] : 1.f;
+    wt[threadIdx.x] = in ? (a.weights ? a.weights[t * a.top_k + threadIdx.x] : 1.f) : 0.f;
   }
   __syncthreads();
   const T* ys = static_cast<const T*>(a.ys);
-  for (int64_t h = (int64_t)threadIdx.x * N; h < a.hidden; h += kRowThreads * N) {
-    Piece<T, VEC> sum{}, v;
-    for (int j = 0; j < a.top_k; ++j) {
-      if (slot[j] < 0) continue;
-      v.load(ys + (int64_t)slot[j] * a.ys_stride + h);
+  for (Span s = my_span<N>(a.hidden); s.h < s.end; s.h += s.step) {
+    Piece<T, VEC> sum{}, r{};
+    if (a.residual) r.load(static_cast<const T*>(a.residual) + t * a.r_stride + s.h);
+    for (int j0 = 0; j0 < a.top_k; j0 += kTogether) {
+      typename Piece<T, VEC>::Raw u[kTogether];
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum.f[i] = fmaf(wt[j], v.f[i], sum.f[i]);
-    }
-    if (a.residual) {
-      v.load(static_cast<const T*>(a.residual) + t * a.r_stride + h);
+      for (int j = 0; j < kTogether; ++j)
+        if (slot[j0 + j] >= 0) u[j] = Piece<T, VEC>::fetch(ys + (int64_t)slot[j0 + j] * a.ys_stride + s.h);
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum.f[i] += v.f[i];
+      for (int j = 0; j < kTogether; ++j) {
+        if (slot[j0 + j] < 0) continue;
+        Piece<T, VEC> v;
+        v.open(u[j]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum.f[i] = fmaf(wt[j0 + j], v.f[i], sum.f[i]);
+      }
     }
-    sum.store(static_cast<T*>(a.y) + t * a.hidden + h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum.f[i] += r.f[i];
+    sum.store(static_cast<T*>(a.y) + t * a.hidden + s.h);
   }
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) k_combine_backward(SortArgs a) {
+__global__ void __launch_bounds__(256) k_combine_backward(SortArgs a) {
   constexpr int N = Piece<T, VEC>::N;
   __shared__ int slot[kMaxTopK];
-  __shared__ float wt[kMaxTopK], scratch[33];
-  const int64_t t = blockIdx.x, rows = a.tokens * a.top_k;
-  if (threadIdx.x < a.top_k) {
-    const int s = a.slot[t * a.top_k + threadIdx.x];
+  __shared__ float wt[kMaxTopK], part[8][kTogether];
+  grid_launch_next();
+  grid_wait();
+  const int64_t t = blockIdx.x, rows = a.tokens * a.top_k, r0 = t * a.top_k;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < kMaxTopK) {
+    const bool in = threadIdx.x < a.top_k;
+    const int s = in ? a.slot[r0 + threadIdx.x] : -1;
     slot[threadIdx.x] = s < rows ? s : -1;
-    wt[threadIdx.x] = a.weights[t * a.top_k + threadIdx.x];
+    wt[threadIdx.x] = in ? a.weights[r0 + threadIdx.x] : 0.f;
   }
-  int64_t owned = a.offsets[a.experts];
-  if (owned < 0) owned = 0;
+  const int64_t owned = max(a.offsets[a.experts], 0);
   __syncthreads();
   const T* dy = static_cast<const T*>(a.dy) + t * a.dy_stride;
   const T* ys = static_cast<const T*>(a.ys);
   T* dys = static_cast<T*>(a.dys);
-  for (int j = 0; j < a.top_k; ++j) {
-    float dot = 0.f;
-    const int64_t r = t * a.top_k + j;
-    for (int64_t h = (int64_t)threadIdx.x * N; h < a.hidden; h += kRowThreads * N) {
-      Piece<T, VEC> d, v, zero{};
+  for (int j0 = 0; j0 < a.top_k; j0 += kTogether) {
+    float dot[kTogether] = {};
+    for (int64_t h = (int64_t)threadIdx.x * N; h < a.hidden; h += (int64_t)blockDim.x * N) {
+      Piece<T, VEC> d;
+      typename Piece<T, VEC>::Raw u[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j)
+        if (slot[j0 + j] >= 0) u[j] = Piece<T, VEC>::fetch(ys + (int64_t)slot[j0 + j] * a.ys_stride + h);
       d.load(dy + h);
-      if (slot[j] >= 0) {
-        v.load(ys + (int64_t)slot[j] * a.ys_stride + h);
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        if (slot[j0 + j] < 0) continue;
+        Piece<T, VEC> v;
+        v.open(u[j]);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          dot = fmaf(v.f[i], d.f[i], dot);
-          d.f[i] *= wt[j];
+          dot[j] = fmaf(v.f[i], d.f[i], dot[j]);
+          v.f[i] = wt[j0 + j] * d.f[i];
         }
-        d.store(dys + (int64_t)slot[j] * a.hidden + h);
+        v.store(dys + (int64_t)slot[j0 + j] * a.hidden + h);
       }
-      if (r >= owned) zero.store(dys + r * a.hidden + h);
+      for (int64_t r = r0 + a.top_k - 1; j0 == 0 && r >= r0 && r >= owned; --r) {
+        Piece<T, VEC> zero{};
+        zero.store(dys + r * a.hidden + h);
+      }
     }
-    dot = block_sum(dot, scratch);
-    if (threadIdx.x == 0) a.dweights[r] = dot;
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const float w = warp_sum(dot[j]);
+      if (lane == 0) part[warp][j] = w;
+    }
+    __syncthreads();
+    if (threadIdx.x < kTogether && j0 + threadIdx.x < a.top_k) {
+      float s = 0.f;
+      for (int w = 0; w < (int)blockDim.x / 32; ++w) s += part[w][threadIdx.x];
+      a.dweights[r0 + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -225,14 +347,25 @@ bool vec_ok(const void* p, int64_t stride, int64_t size) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride * size) % 16 == 0;
 }
 
-enum RowOp { OP_GATHER, OP_COMBINE, OP_COMBINE_BACKWARD };
+enum RowOp { OP_GATHER, OP_DISPATCH_SMALL, OP_COMBINE, OP_COMBINE_BACKWARD };
 
 template <typename T, bool VEC>
-void launch_rows(RowOp op, const SortArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)a.tokens;
-  if (op == OP_GATHER) k_gather<T, VEC><<<grid, kRowThreads, 0, s>>>(a);
-  else if (op == OP_COMBINE) k_combine<T, VEC><<<grid, kRowThreads, 0, s>>>(a);
-  else k_combine_backward<T, VEC><<<grid, kRowThreads, 0, s>>>(a);
+cudaError_t launch_rows(RowOp op, const SortArgs& a, cudaStream_t s) {
+  constexpr int N = Piece<T, VEC>::N;
+  const int64_t pieces = (a.hidden + N - 1) / N;
+  // enough blocks to fill the GPU (a token's dot products stay in one block)
+  int64_t y = 1;
+  if (op != OP_COMBINE_BACKWARD) {
+    while (a.tokens * y < 304 && pieces / (2 * y) >= 32) y *= 2;
+  }
+  // whole warps that divide a block's pieces into even rounds
+  const int64_t per = (pieces + y - 1) / y, rounds = (per + 255) / 256;
+  const unsigned threads = (unsigned)(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  const dim3 grid((unsigned)(a.tokens + (op == OP_DISPATCH_SMALL)), (unsigned)y), block(threads);
+  if (op == OP_GATHER) return launch_early(k_gather<T, VEC>, grid, block, 0, s, a);
+  if (op == OP_DISPATCH_SMALL) return launch_early(k_dispatch_small<T, VEC>, grid, block, 0, s, a);
+  if (op == OP_COMBINE) return launch_early(k_combine<T, VEC>, grid, block, 0, s, a);
+  return launch_early(k_combine_backward<T, VEC>, grid, block, 0, s, a);
 }
 
 // 16-byte accesses where every row of every tensor starts on 16 bytes and has
@@ -243,9 +376,7 @@ cudaError_t rows_t(RowOp op, const SortArgs& a, cudaStream_t s) {
   const bool vec = (a.hidden * b) % 16 == 0 && vec_ok(a.x, a.x_stride, b) && vec_ok(a.xs, a.hidden, b) &&
                    vec_ok(a.ys, a.ys_stride, b) && vec_ok(a.residual, a.r_stride, b) &&
                    vec_ok(a.y, a.hidden, b) && vec_ok(a.dy, a.dy_stride, b) && vec_ok(a.dys, a.hidden, b);
-  if (vec) launch_rows<T, true>(op, a, s);
-  else launch_rows<T, false>(op, a, s);
-  return cudaGetLastError();
+  return vec ? launch_rows<T, true>(op, a, s) : launch_rows<T, false>(op, a, s);
 }
 
 cudaError_t rows(RowOp op, const SortArgs& a, cudaStream_t s) {
@@ -260,13 +391,16 @@ cudaError_t rows(RowOp op, const SortArgs& a, cudaStream_t s) {
 
 cudaError_t launch_dispatch(const SortArgs& a, cudaStream_t s) {
   const int64_t n = a.tokens * a.top_k;
+  if (n <= kSortChunk) return rows(OP_DISPATCH_SMALL, a, s);
   const unsigned chunks = (unsigned)((n + kSortChunk - 1) / kSortChunk);
   const size_t smem = sizeof(int) * a.experts;
-  if (chunks) k_sort_count<<<chunks, kSortChunk, smem, s>>>(a, n);
-  k_sort_scan<<<1, 1024, 0, s>>>(a, (int)chunks);
-  if (chunks) k_sort_place<<<chunks, kSortChunk, smem, s>>>(a, n);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.xs && a.tokens) e = rows(OP_GATHER, a, s);
+  SortArgs b = a;
+  b.total = a.counts + (int64_t)chunks * a.experts;
+  cudaError_t e = launch_early(k_sort_count, dim3(chunks), dim3(kSortChunk), smem, s, b, n);
+  if (e == cudaSuccess)
+    e = launch_early(k_sort_scan, dim3((a.experts + 31) / 32), dim3(1024), 0, s, b, (int)chunks);
+  if (e == cudaSuccess) e = launch_early(k_sort_place, dim3(chunks), dim3(kSortChunk), smem, s, b, n);
+  if (e == cudaSuccess && a.xs) e = rows(OP_GATHER, b, s);
   return e;
 }
 

@@ -98,7 +98,8 @@ struct SortArgs {
   void* xs;
   int32_t* slot;
   int32_t* offsets;
-  int32_t* counts;             // workspace [chunks][experts]
+  int32_t* counts;             // workspace [chunks][experts], then
+  int32_t* total;              // [experts]
   const void* ys;              // rows in expert order
   int64_t ys_stride;
   const float* weights;        // nullable: every weight is 1
@@ -110,7 +111,7 @@ struct SortArgs {
   void* dys;
   float* dweights;
 };
-constexpr int kSortChunk = 1024;  // assignments one block counts and places
+constexpr int kSortChunk = 1024;  // assignments one block counts and places; up to these need no workspace
 cudaError_t launch_dispatch(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine_backward(const SortArgs& a, cudaStream_t s);
