@@ -41,17 +41,13 @@
 
 #include <mutex>
 
-#include "act.cuh"
-#include "common.cuh"
-#include "mbarrier.cuh"
-#include "tcgen05.cuh"
+#include "linear.cuh"
 
 namespace muon {
 
 namespace {
 
-constexpr int BM = 256;     // features (rows form) or output rows (sum form) of a pair's tile
-constexpr int BK = 64;      // one 128-byte swizzle row of k
+constexpr int BM = 256;  // features (rows form) or output rows (sum form) of a pair's tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (3 + kEpiWarps);  // producer, MMA issuer, epilogue, range-tail helper
 
@@ -100,13 +96,6 @@ static_assert(rows_stages(256) == 7 && rows_stages(128) == 9 && rows_stages(64) 
 
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
 }
 
 __device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
@@ -218,66 +207,6 @@ struct Walk {
     return true;
   }
 };
-
-// Planes (0 high, 1 middle, 2 low) of the two operands in partial product i,
-// smallest products first.
-constexpr int kProducts = 6;
-__device__ __forceinline__ int plane_m(int i) { return (0x010120 >> (4 * i)) & 3; }
-__device__ __forceinline__ int plane_n(int i) { return (0x001102 >> (4 * i)) & 3; }
-
-__device__ __forceinline__ float ld_el(const void* p, int64_t i, int type) {
-  if (type == DT_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  if (type == DT_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return static_cast<const float*>(p)[i];
-}
-__device__ __forceinline__ void st_el(void* p, int64_t i, float v, int type) {
-  if (type == DT_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else if (type == DT_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else static_cast<float*>(p)[i] = v;
-}
-// 8 values of a 16-bit type.
-__device__ __forceinline__ void unpack8(const uint4& u, float* f, int type) {
-  if (type == DT_BF16) {
-    bf16x8_to_f32(u, f);
-  } else {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(h[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* f, int type) {
-  if (type == DT_BF16) return f32_to_bf16x8(f);
-  uint4 u;
-  __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-  return u;
-}
-template <int N, bool kFast>
-__device__ __forceinline__ void activate_n(float* v, int act) {
-  switch (act) {  // outside the loop over values
-    case ACT_NONE: break;
-    case ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_RELU);
-      break;
-    case ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_SILU);
-      break;
-    case ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_GELU);
-      break;
-    default:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_GELU_TANH);
-  }
-}
 
 // Rows form, one warp: feature f (this lane's) of tokens t0 .. t0 + n - 1 (n
 // <= 32) from 32 accumulator columns.  Each store covers 32 features of one
@@ -449,40 +378,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
       const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
       for (int i = p.first; ok && i < kProducts; ++i) {
-      const int planes = p.first == 0 ? 3 : 1;
-      const int ae = (kRows ? it.e * planes : 0) + plane_m(i), be = plane_n(i);
-      for (int k = it.k0; k < it.k1; k += BK) {
-        if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 1))) break;
-        const uint32_t sa = ring + s * stage_bytes, sb = sa + L::kA;
-        if (elect_lane()) {
-          uint32_t bar = full_leader + 8u * s;  // where this CTA's copies are counted: the leader's ring
-          if (group_sum && it.k1 - k < BK) {    // or, for a range's last rows, its own helper
-            bar = fix(s);
-            mbar_expect_tx(bar, bytes);
-          } else if (rank == 0) {
-            mbar_expect_tx(full(s), 2 * bytes);
-          } else if (group_sum) {
-            mbar_arrive_cluster(bar);
-          }
-          if (AMN) {
-            tma_load_3d_pair(sa, &mapA, bar, arow, k, ae);
-            tma_load_3d_pair(sa + 64 * BK * 2, &mapA, bar, arow + 64, k, ae);
-          } else {
-            tma_load_3d_pair(sa, &mapA, bar, k, arow, ae);
-          }
-          if constexpr (kRows) {
-            tma_load_3d_pair(sb, &mapB, bar, k, brow, be);
-            for (int c = 1; c < boxes; ++c)
-              tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, be);
-          } else {
+        const int planes = p.first == 0 ? 3 : 1;
+        const int ae = (kRows ? it.e * planes : 0) + plane_m(i), be = plane_n(i);
+        for (int k = it.k0; k < it.k1; k += BK) {
+          if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 1))) break;
+          const uint32_t sa = ring + s * stage_bytes, sb = sa + L::kA;
+          if (elect_lane()) {
+            uint32_t bar = full_leader + 8u * s;  // where this CTA's copies are counted: the leader's ring
+            if (group_sum && it.k1 - k < BK) {    // or, for a range's last rows, its own helper
+              bar = fix(s);
+              mbar_expect_tx(bar, bytes);
+            } else if (rank == 0) {
+              mbar_expect_tx(full(s), 2 * bytes);
+            } else if (group_sum) {
+              mbar_arrive_cluster(bar);
+            }
+            if (AMN) {
+              tma_load_3d_pair(sa, &mapA, bar, arow, k, ae);
+              tma_load_3d_pair(sa + 64 * BK * 2, &mapA, bar, arow + 64, k, ae);
+            } else {
+              tma_load_3d_pair(sa, &mapA, bar, k, arow, ae);
+            }
+            if constexpr (kRows) {
+              tma_load_3d_pair(sb, &mapB, bar, k, brow, be);
+              for (int c = 1; c < boxes; ++c)
+                tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, be);
+            } else {
 #pragma unroll
-            for (int c = 0; c < BN / 128; ++c)
-              tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, be);
+              for (int c = 0; c < BN / 128; ++c)
+                tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, be);
+            }
           }
+          __syncwarp();
+          if (++s == S) { s = 0; ph ^= 1; }
         }
-        __syncwarp();
-        if (++s == S) { s = 0; ph ^= 1; }
-      }
       }
     }
     if (!ok) {  // gave up: let the copies in flight land before the block leaves
@@ -506,26 +435,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
         const uint32_t idesc = instr_desc(p.type == DT_F16 ? 0u : 1u, BM, kRows ? mma_cols(it) : BN, !kRows, AMN);
         uint32_t add = 0;  // the tile's first MMA overwrites
-        for (int i = p.first; ok && i < kProducts; ++i)
-        for (int k = it.k0; k < it.k1; k += BK) {
-          if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
-          tc_fence_after();
-          const uint64_t a = da + s * (stage_bytes >> 4), b = db + s * (stage_bytes >> 4);
-          if (elect_lane()) {
-            umma_pair(d_tmem, a, b, idesc, add);
-            if (it.k1 - k >= BK) {
-              umma_pair(d_tmem, a + kStepA, b + kStepB, idesc, 1);
-              umma_pair(d_tmem, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
-              umma_pair(d_tmem, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
-            } else {  // behind the sum's end there are only zeros: skipped
-              for (int kk = 1; kk * 16 < it.k1 - k; ++kk)
-                umma_pair(d_tmem, a + kk * kStepA, b + kk * kStepB, idesc, 1);
+        for (int i = p.first; ok && i < kProducts; ++i) {
+          for (int k = it.k0; k < it.k1; k += BK) {
+            if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
+            tc_fence_after();
+            const uint64_t a = da + s * (stage_bytes >> 4), b = db + s * (stage_bytes >> 4);
+            if (elect_lane()) {
+              umma_pair(d_tmem, a, b, idesc, add);
+              if (it.k1 - k >= BK) {
+                umma_pair(d_tmem, a + kStepA, b + kStepB, idesc, 1);
+                umma_pair(d_tmem, a + 2 * kStepA, b + 2 * kStepB, idesc, 1);
+                umma_pair(d_tmem, a + 3 * kStepA, b + 3 * kStepB, idesc, 1);
+              } else {  // behind the sum's end there are only zeros: skipped
+                for (int kk = 1; kk * 16 < it.k1 - k; ++kk)
+                  umma_pair(d_tmem, a + kk * kStepA, b + kk * kStepB, idesc, 1);
+              }
+              umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
             }
-            umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
+            __syncwarp();
+            add = 1;
+            if (++s == S) { s = 0; ph ^= 1; }
           }
-          __syncwarp();
-          add = 1;
-          if (++s == S) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
         if (elect_lane()) umma_commit_pair(tfull(acc), 3);
@@ -632,19 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && more; more = walk.next(p, it)) {
       const int blocks = (it.k1 - it.k0 + BK - 1) / BK, rem = (it.k1 - it.k0) % BK;
       for (int i = p.first; ok && i < kProducts; ++i) {
-      if (rem) {
-        const int st = (s + blocks - 1) % S;
-        if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32))) break;
-        fph ^= 1u << st;
-        uint8_t* stage = smem + st * L::kStage;
-        for (int box = 0; box < (int)(L::kStage / (64 * BK * 2)); ++box)  // 64 rows of k, 128 bytes each
-          for (int i = rem * 8 + lane; i < BK * 8; i += 32)
-            reinterpret_cast<uint4*>(stage + box * (64 * BK * 2))[i] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(map_to(full(st), 0));
-      }
-      s = (s + blocks) % S;
+        if (rem) {
+          const int st = (s + blocks - 1) % S;
+          if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32))) break;
+          fph ^= 1u << st;
+          uint8_t* stage = smem + st * L::kStage;
+          for (int box = 0; box < (int)(L::kStage / (64 * BK * 2)); ++box)  // 64 rows of k, 128 bytes each
+            for (int i = rem * 8 + lane; i < BK * 8; i += 32)
+              reinterpret_cast<uint4*>(stage + box * (64 * BK * 2))[i] = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_release_cluster(map_to(full(st), 0));
+        }
+        s = (s + blocks) % S;
       }
     }
   }
@@ -764,16 +694,6 @@ __global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t s
   *reinterpret_cast<uint4*>(dst + (b * rows + r) * pitch + c) = *reinterpret_cast<const uint4*>(h);
 }
 
-int num_sms() {
-  static int n = [] {
-    int dev = 0, v = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    return v > 0 ? v : 152;
-  }();
-  return n;
-}
-
 bool aligned_rows(const void* p, int64_t stride, int type) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % (type == DT_F32 ? 4 : 8) == 0;
 }
@@ -855,6 +775,16 @@ cudaError_t run_sum(const Product& p, const TcProduct& q, cudaStream_t s) {
 bool rows_form(const Product& p) { return p.a_k == 1; }
 
 }  // namespace
+
+int num_sms() {
+  static int n = [] {
+    int dev = 0, v = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    return v > 0 ? v : 152;
+  }();
+  return n;
+}
 
 cudaError_t ops_error_word(int** err) {
   static int* addr[64] = {};

@@ -208,6 +208,11 @@ cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool la
     (b_along ? p.b_n : p.b_k) = b.stride;
     p.b_e = b.batch_stride;
   }
+  if (linear_few_fits(p)) {
+    if (!launch || e != cudaSuccess) return e;
+    e = ops_error_word(&p.err);
+    return e == cudaSuccess ? launch_linear_few(p, s) : e;
+  }
   const TilePlan t = tile_plan(p);
   float* part = t.part_bytes ? static_cast<float*>(c.take((size_t)t.part_bytes)) : nullptr;
   if (!launch || e != cudaSuccess) return e;

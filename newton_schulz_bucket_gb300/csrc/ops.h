@@ -65,6 +65,10 @@ struct TilePlan {
 };
 TilePlan tile_plan(const Product& p);
 cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, cudaStream_t s);
+// Few token rows: one launch, no scratch (operands as launch_linear_tc's).
+bool linear_few_fits(const Product& p);
+cudaError_t launch_linear_few(const Product& p, cudaStream_t s);
+int num_sms();
 // 16-bit rows copied to a pitch that TMA can read: rows of every matrix.
 cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
                             int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
