@@ -39,6 +39,7 @@
 // the MMAs.
 #include <cuda.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "linear.cuh"
@@ -130,22 +131,25 @@ __device__ __forceinline__ void raster(int r, int tiles_m, int tiles_n, int& tm,
 template <int BN>
 struct Walk {
   int r, step;                // item within the current range / part, stride
-  int e, lo, hi, after;       // range, its rows, the end of the one behind it
-  int cnt, tt, size;          // its items, token tiles and their size
+  int e, lo, hi, after;       // the current range, its rows, the end of the one behind it
+  int cnt, tt, size;          // the range's items, token tiles and their size
   __device__ __forceinline__ Walk(const TcProduct& p)
       : r(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), after(0), cnt(0), tt(0), size(0) {
+    const int most = BN == 0 ? p.rows : p.K;
     if (p.mode == GROUP_NONE) {
-      after = BN == 0 ? p.rows : p.K;
+      after = most;
     } else {
-      hi = range_at(p, 0, BN == 0 ? p.rows : p.K);
-      after = range_at(p, 1, BN == 0 ? p.rows : p.K);
+      hi = range_at(p, 0, most);
+      after = range_at(p, 1, most);
     }
   }
-  __device__ __forceinline__ void advance(const TcProduct& p, int most) {
+  // The next range; the end of its successor is on its way by the time it is
+  // needed.
+  __device__ __forceinline__ void advance(const TcProduct& p) {
     ++e;
     lo = hi;
     hi = max(lo, after);
-    if (p.mode != GROUP_NONE && e + 2 <= p.experts) after = range_at(p, e + 2, most);
+    if (p.mode != GROUP_NONE && e + 2 <= p.experts) after = range_at(p, e + 2, BN == 0 ? p.rows : p.K);
   }
   __device__ __forceinline__ void part_of_sum(const TcProduct& p, int split, Item& it) {
     it.split = split;
@@ -162,8 +166,8 @@ struct Walk {
     if constexpr (BN == 0) {
       while (r >= cnt) {
         r -= cnt;
-        if (e + 1 >= (p.mode == GROUP_ROWS ? p.experts : 1)) { cnt = 0; e = 1 << 28; return false; }
-        advance(p, p.rows);
+        if (e + 1 >= (p.mode == GROUP_ROWS ? p.experts : 1)) { cnt = 0; return false; }
+        advance(p);
         tt = (hi - lo + p.tile_rows - 1) / p.tile_rows;
         cnt = tt * p.tiles_m * p.splits;
         size = tt ? token_tile(hi - lo, tt) : 0;
@@ -184,8 +188,8 @@ struct Walk {
       const int per = p.tiles_m * p.tiles_n;
       while (r >= cnt) {  // range or part e + 1
         r -= cnt;
-        if (e + 1 >= (p.mode == GROUP_SUM ? p.experts : p.splits)) { cnt = 0; e = 1 << 28; return false; }
-        if (p.mode == GROUP_SUM) advance(p, p.K);
+        if (e + 1 >= (p.mode == GROUP_SUM ? p.experts : p.splits)) { cnt = 0; return false; }
+        if (p.mode == GROUP_SUM) advance(p);
         else ++e;
         cnt = per;
       }
@@ -646,21 +650,22 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
 
 // fp32 rows into three bf16 planes: dst [batch][3][rows][pitch], zeros in the
 // padding.  Truncation leaves remainders that are exact in fp32; a non-finite
-// value goes whole into the high plane.
-__global__ void __launch_bounds__(256) k_split_rows(const float* src, int64_t stride, int64_t batch_stride,
-                                                    uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols) {
+// value goes whole into the high plane.  Up to two tensors a launch.
+__global__ void __launch_bounds__(256) k_split_rows(SplitRows first, SplitRows second) {
   grid_launch_next();
   grid_wait();
-  const int64_t r = blockIdx.x, b = blockIdx.z;
+  const bool two = blockIdx.z >= first.batch;
+  const SplitRows& q = two ? second : first;
+  const int64_t r = blockIdx.x, b = blockIdx.z - (two ? first.batch : 0);
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-  if (c >= pitch) return;
-  const float* s = src + b * batch_stride + r * stride + c;
+  if (r >= q.rows || c >= q.pitch) return;
+  const float* s = q.src + b * q.batch_stride + r * q.stride + c;
   float f[8];
-  if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
+  if (c + 8 <= q.cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
     u4_to_f4x2(reinterpret_cast<const uint4*>(s)[0], reinterpret_cast<const uint4*>(s)[1], f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? s[i] : 0.f;
+    for (int i = 0; i < 8; ++i) f[i] = c + i < q.cols ? s[i] : 0.f;
   }
   uint16_t h[3][8];
 #pragma unroll
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(256) k_split_rows(const float* src, int64_t st
   }
 #pragma unroll
   for (int k = 0; k < 3; ++k)
-    *reinterpret_cast<uint4*>(dst + ((b * 3 + k) * rows + r) * pitch + c) = *reinterpret_cast<const uint4*>(h[k]);
+    *reinterpret_cast<uint4*>(q.dst + ((b * 3 + k) * q.rows + r) * q.pitch + c) = *reinterpret_cast<const uint4*>(h[k]);
 }
 
 __global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t stride, int64_t batch_stride,
@@ -896,11 +901,10 @@ cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_strid
                       static_cast<uint16_t*>(dst), pitch, rows, cols);
 }
 
-cudaError_t launch_split_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
-                              int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
-  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)batch);
-  return launch_early(k_split_rows, grid, dim3(256), 0, s, static_cast<const float*>(src), stride, batch_stride,
-                      static_cast<uint16_t*>(dst), pitch, rows, cols);
+cudaError_t launch_split_rows(const SplitRows& first, const SplitRows& second, cudaStream_t s) {
+  const int64_t rows = std::max(first.rows, second.rows), pitch = std::max(first.pitch, second.pitch);
+  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)(first.batch + second.batch));
+  return launch_early(k_split_rows, grid, dim3(256), 0, s, first, second);
 }
 
 }  // namespace muon

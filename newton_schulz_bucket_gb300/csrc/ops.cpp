@@ -172,13 +172,20 @@ struct Operand {
   const void* p;
   int64_t stride, batch_stride;
 };
+// `waiting` holds an fp32 split that has not been launched: two go together.
 Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch,
-                    cudaStream_t s, cudaError_t* e) {
+                    SplitRows* waiting, cudaStream_t s, cudaError_t* e) {
   if (dtype == DT_F32) {
     const int64_t pitch = (cols + 7) / 8 * 8;
     void* dst = c.take((size_t)(batch * 3 * rows * pitch * 2));
-    if (launch && *e == cudaSuccess)
-      *e = launch_split_rows(o.p, o.stride, o.batch_stride, dst, pitch, rows, cols, batch, s);
+    const SplitRows mine{static_cast<const float*>(o.p), o.stride, o.batch_stride, static_cast<uint16_t*>(dst), pitch,
+                         rows, cols, batch};
+    if (waiting->batch == 0) {
+      *waiting = mine;
+    } else {
+      if (launch && *e == cudaSuccess) *e = launch_split_rows(*waiting, mine, s);
+      *waiting = SplitRows{};
+    }
     return {dst, pitch, rows * pitch};
   }
   const bool ok = (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
@@ -191,23 +198,25 @@ Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_
 }
 
 // One product.  `ready` operands went through tma_operand already.
-cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool launch, cudaStream_t s) {
+cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool launch, SplitRows waiting,
+                        cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const bool a_along = p.a_k == 1, b_along = p.b_k == 1;
   const int64_t mats = p.mode == GROUP_ROWS ? p.experts : 1;
   if (!a_ready) {
     const Operand a = tma_operand(p.dtype, {p.A, a_along ? p.a_m : p.a_k, 0}, a_along ? p.M : p.K,
-                                  a_along ? p.K : p.M, 1, c, launch, s, &e);
+                                  a_along ? p.K : p.M, 1, c, launch, &waiting, s, &e);
     p.A = a.p;
     (a_along ? p.a_m : p.a_k) = a.stride;
   }
   if (!b_ready) {
     const Operand b = tma_operand(p.dtype, {p.B, b_along ? p.b_n : p.b_k, p.b_e}, b_along ? p.N : p.K,
-                                  b_along ? p.K : p.N, mats, c, launch, s, &e);
+                                  b_along ? p.K : p.N, mats, c, launch, &waiting, s, &e);
     p.B = b.p;
     (b_along ? p.b_n : p.b_k) = b.stride;
     p.b_e = b.batch_stride;
   }
+  if (launch && e == cudaSuccess && waiting.batch) e = launch_split_rows(waiting, SplitRows{}, s);
   if (linear_few_fits(p)) {
     if (!launch || e != cudaSuccess) return e;
     e = ops_error_word(&p.err);
@@ -223,7 +232,7 @@ cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool la
 muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, bool launch, cudaStream_t s) {
   if (!backward) {
     if (a->rows == 0) return MUON_OK;
-    return cuda_status("muon_linear", run_product(forward_product(a), false, false, c, launch, s));
+    return cuda_status("muon_linear", run_product(forward_product(a), false, false, c, launch, SplitRows{}, s));
   }
   const char* what = "muon_linear_backward";
   const int64_t b = dtype_size(a->dtype);
@@ -248,11 +257,15 @@ muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, boo
   if (launch && (act || a->db)) e = launch_grad_prep(g, s);
   Operand dz{act ? g.dz : a->dy, act ? g.dz_stride : a->dy_stride, 0};
   Operand x{a->x, a->x_stride, 0};
-  if (products) dz = tma_operand(a->dtype, dz, a->rows, a->out, 1, c, launch, s, &e);  // once for both products
-  if (a->dw) x = tma_operand(a->dtype, x, a->rows, a->in, 1, c, launch, s, &e);
-  if (a->dx && e == cudaSuccess) e = run_product(dx_product(a, dz.p, dz.stride), true, false, c, launch, s);
+  SplitRows waiting{};
+  if (products) dz = tma_operand(a->dtype, dz, a->rows, a->out, 1, c, launch, &waiting, s, &e);  // once for both
+  if (a->dw) x = tma_operand(a->dtype, x, a->rows, a->in, 1, c, launch, &waiting, s, &e);
+  if (a->dx && e == cudaSuccess) {
+    e = run_product(dx_product(a, dz.p, dz.stride), true, false, c, launch, waiting, s);
+    waiting = SplitRows{};
+  }
   if (a->dw && e == cudaSuccess)
-    e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), true, true, c, launch, s);
+    e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), true, true, c, launch, waiting, s);
   return cuda_status(what, e);
 }
 

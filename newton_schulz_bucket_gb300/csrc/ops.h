@@ -72,9 +72,14 @@ int num_sms();
 // 16-bit rows copied to a pitch that TMA can read: rows of every matrix.
 cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
                             int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
-// fp32 rows as three bf16 planes: dst [batch][3][rows][pitch].
-cudaError_t launch_split_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
-                              int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
+// fp32 rows as three bf16 planes: dst [batch][3][rows][pitch]; batch 0: none.
+struct SplitRows {
+  const float* src;
+  int64_t stride, batch_stride;
+  uint16_t* dst;
+  int64_t pitch, rows, cols, batch;
+};
+cudaError_t launch_split_rows(const SplitRows& first, const SplitRows& second, cudaStream_t s);
 cudaError_t ops_error_word(int** err);  // device address of the error word of the current device
 
 constexpr int kGradChunk = 128;  // rows of one partial column sum
