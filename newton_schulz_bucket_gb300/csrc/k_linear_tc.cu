@@ -61,7 +61,6 @@ struct TcProduct {
   int M, N;                 // rows form: features (M); sum form: the output
   int tiles_m, tiles_n;     // sum form; rows form: feature tiles (tiles_m)
   int tile_rows;            // rows form: most token rows of a tile (64, 128 or 256)
-  int box_rows;             // rows form: token rows of one TMA copy
   int stages;               // rows form: ring depth, more for smaller tiles
   int type, act, vec;       // DType; vec: output rows (and the epilogue's tensors) start on 16 bytes
   void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert
@@ -110,9 +109,13 @@ struct Item {
   int e, m0, n0, n_end, k0, k1, split;
 };
 
-// Token tiles of a range of n rows: as few as tile_rows allows, of even size in
-// steps of 32 (n > tile_rows (tiles - 1) >= size (tiles - 1): none is empty).
-__device__ __forceinline__ int token_tile(int n, int tiles) { return ((n + tiles - 1) / tiles + 31) / 32 * 32; }
+// Token tiles of a range of n rows: as few as tile_rows allows, in steps of 32
+// rows shared out evenly (the first ones take one more).  Tile i of tiles starts
+// at token_start(i); none is empty, as tiles - 1 full ones do not hold n.
+__device__ __forceinline__ int token_start(int n, int tiles, int i) {
+  const int units = (n + 31) / 32, each = units / tiles;
+  return 32 * (i * each + min(i, units - each * tiles));
+}
 // Columns of a tile's MMA.
 __device__ __forceinline__ int mma_cols(const Item& it) { return (it.n_end - it.n0 + 31) / 32 * 32; }
 
@@ -132,9 +135,9 @@ template <int BN>
 struct Walk {
   int r, step;                // item within the current range / part, stride
   int e, lo, hi, after;       // the current range, its rows, the end of the one behind it
-  int cnt, tt, size;          // the range's items, token tiles and their size
+  int cnt, tt;                // the range's items and token tiles
   __device__ __forceinline__ Walk(const TcProduct& p)
-      : r(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), after(0), cnt(0), tt(0), size(0) {
+      : r(blockIdx.x >> 1), step(gridDim.x >> 1), e(-1), lo(0), hi(0), after(0), cnt(0), tt(0) {
     const int most = BN == 0 ? p.rows : p.K;
     if (p.mode == GROUP_NONE) {
       after = most;
@@ -170,7 +173,6 @@ struct Walk {
         advance(p);
         tt = (hi - lo + p.tile_rows - 1) / p.tile_rows;
         cnt = tt * p.tiles_m * p.splits;
-        size = tt ? token_tile(hi - lo, tt) : 0;
       }
       int q = r, split = 0;
       if (p.splits > 1) {
@@ -181,8 +183,8 @@ struct Walk {
       raster(q, p.tiles_m, tt, tm, tn);
       it.e = e;
       it.m0 = tm * BM;
-      it.n0 = lo + tn * size;
-      it.n_end = min(hi, it.n0 + size);
+      it.n0 = lo + token_start(hi - lo, tt, tn);
+      it.n_end = min(hi, lo + token_start(hi - lo, tt, tn + 1));
       part_of_sum(p, split, it);
     } else {
       const int per = p.tiles_m * p.tiles_n;
@@ -309,10 +311,18 @@ __device__ void zero_span(void* base, int64_t from, int64_t to, int64_t tid, int
   for (int64_t i = from + v * 8 + tid; i < to; i += n_threads) p[i] = 0;
 }
 
+// Maps of the N operand.  Rows form: the same rows in boxes of 16, 32, 64, 96 and
+// 128, so that a block's tokens come in one copy and drag few others along.
+constexpr int kBoxes = 5;
+struct NMaps {
+  CUtensorMap box[kBoxes];
+};
+__host__ __device__ constexpr int box_rows(int b) { return b < 2 ? 16 << b : 32 * b; }
+
 // BN = 0: rows form (M operand stored across the sum if AMN); else sum form.
 template <bool AMN, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+    k_linear_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ NMaps mapsB,
                 const __grid_constant__ CUtensorMap mapD, const __grid_constant__ TcProduct p) {
   using L = Smem<BN>;
   const int S = BN == 0 ? p.stages : L::kStages;
@@ -348,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&mapA) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapB) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapsB.box[0]) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
@@ -376,11 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (; ok && more; more = walk.next(p, it)) {
       const int arow = it.m0 + (int)rank * 128;
-      // rows form: this CTA's half of the tile's tokens, in boxes of box_rows
+      // rows form: this CTA's half of the tile's tokens
       const int half = kRows ? mma_cols(it) / 2 : BN / 2;
       const int brow = it.n0 + (int)rank * half;
-      const int boxes = kRows ? (half + p.box_rows - 1) / p.box_rows : 0;
-      const uint32_t bytes = kRows ? L::kA + (uint32_t)(boxes * p.box_rows) * (BK * 2) : L::kStage;
+      int box = 0;
+      if (kRows) while (box_rows(box) < half) ++box;
+      const CUtensorMap* mapB = &mapsB.box[box];
+      const uint32_t bytes = kRows ? L::kA + (uint32_t)box_rows(box) * (BK * 2) : L::kStage;
       for (int i = p.first; ok && i < kProducts; ++i) {
         const int planes = p.first == 0 ? 3 : 1;
         const int ae = (kRows ? it.e * planes : 0) + plane_m(i), be = plane_n(i);
@@ -404,13 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(sa, &mapA, bar, k, arow, ae);
             }
             if constexpr (kRows) {
-              tma_load_3d_pair(sb, &mapB, bar, k, brow, be);
-              for (int c = 1; c < boxes; ++c)
-                tma_load_3d_pair(sb + c * p.box_rows * (BK * 2), &mapB, bar, k, brow + c * p.box_rows, be);
+              tma_load_3d_pair(sb, mapB, bar, k, brow, be);
             } else {
 #pragma unroll
               for (int c = 0; c < BN / 128; ++c)
-                tma_load_3d_pair(sb + c * (64 * BK * 2), &mapB, bar, brow + c * 64, k, be);
+                tma_load_3d_pair(sb + c * (64 * BK * 2), mapB, bar, brow + c * 64, k, be);
             }
           }
           __syncwarp();
@@ -708,7 +718,7 @@ int planes(const TcProduct& q) { return q.type == DT_F32 ? 3 : 1; }
 
 // The kernel with its function attributes set (once per device).
 template <bool AMN, int BN>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const TcProduct& q,
+cudaError_t launch(const CUtensorMap& ma, const NMaps& mb, const CUtensorMap& md, const TcProduct& q,
                    int64_t items, cudaStream_t s) {
   auto fn = k_linear_tc<AMN, BN>;
   static bool ready[64] = {};
@@ -748,26 +758,28 @@ cudaError_t run_rows(const Product& p, TcProduct q, cudaStream_t s) {
   const int64_t mats = np * (p.mode == GROUP_ROWS ? p.experts : 1);
   const bool across = p.b_k != 1;  // weights stored across the sum
   const int64_t between = mats > 1 ? p.b_e : (across ? p.K * p.b_k : p.N * p.b_n);
-  CUtensorMap mw, mx;
+  CUtensorMap mw;
+  NMaps mx;
   cudaError_t e = across ? tc_encode_map(&mw, p.B, type, p.N, p.K, mats, p.b_k, between, 64, 64)
                          : tc_encode_map(&mw, p.B, type, p.K, p.N, mats, p.b_n, between, 64, 128);
-  if (e == cudaSuccess)
-    e = tc_encode_map(&mx, p.A, type, p.K, p.M, np, p.a_m, p.M * p.a_m, 64, (uint32_t)q.box_rows);
+  for (int b = 0; b < kBoxes && e == cudaSuccess; ++b)
+    e = tc_encode_map(&mx.box[b], p.A, type, p.K, p.M, np, p.a_m, p.M * p.a_m, 64, (uint32_t)box_rows(b));
   if (e != cudaSuccess) return e;
   int64_t tt = (p.M + q.tile_rows - 1) / q.tile_rows;
   if (p.mode == GROUP_ROWS) tt = p.M / q.tile_rows + (p.M < p.experts ? p.M : p.experts);  // at most
   const int64_t items = tt * q.tiles_m * q.splits;
-  return across ? launch<true, 0>(mw, mx, mx, q, items, s) : launch<false, 0>(mw, mx, mx, q, items, s);
+  return across ? launch<true, 0>(mw, mx, mw, q, items, s) : launch<false, 0>(mw, mx, mw, q, items, s);
 }
 
 template <int BN>
 cudaError_t run_sum(const Product& p, const TcProduct& q, cudaStream_t s) {
   const int type = operand_type(q), np = planes(q);
   const int64_t mats = p.mode == GROUP_SUM ? p.experts : 1;
-  CUtensorMap ma, mb, md;
+  CUtensorMap ma, md;
+  NMaps mb{};
   cudaError_t e = tc_encode_map(&ma, p.A, type, p.M, p.K, np, p.a_k, p.K * p.a_k, 64, 64);
-  if (e == cudaSuccess) e = tc_encode_map(&mb, p.B, type, p.N, p.K, np, p.b_k, p.K * p.b_k, 64, 64);
-  md = mb;
+  if (e == cudaSuccess) e = tc_encode_map(&mb.box[0], p.B, type, p.N, p.K, np, p.b_k, p.K * p.b_k, 64, 64);
+  md = ma;
   if (e == cudaSuccess && q.vec)
     e = tc_encode_map(&md, p.D, q.type == DT_F32 ? NS_F32 : type, p.N, p.M, mats, p.N, p.M * p.N,
                       q.type == DT_F32 ? 32 : 64, 32);
@@ -868,9 +880,6 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
     q.tiles_m = (int)((p.N + BM - 1) / BM);
     q.tile_rows = t.tile_rows;
     q.stages = rows_stages(t.tile_rows);
-    // token rows of one copy: one copy a block where it can be (copies cost more
-    // than the rows they drag along), 16 for the least tiles
-    q.box_rows = p.mode == GROUP_NONE && p.M <= 32 ? 16 : t.tile_rows / 2;
   } else {
     q.M = (int)p.M;
     q.N = (int)p.N;
