@@ -318,3 +318,65 @@ def test_refusals():
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def _check_dw(dw, x, dz, offsets):
+    """dw of 16-bit x and dz (no activation) against fp64 products on the GPU,
+    expert by expert: sums of fp32 terms, rounded once."""
+    from layers_tol import TINY, U, acc
+    dt = x.dtype
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        a, b = x[lo:hi].double(), dz[lo:hi].double()
+        want, size = a.T @ b, a.abs().T @ b.abs()
+        tol = acc(hi - lo) * size
+        tol += U[dt] * (want.abs() + tol) * 1.01 + TINY[dt]
+        bad = (dw[e].double() - want).abs() > tol
+        assert not bad.any(), f"expert {e} ({hi - lo} rows): {int(bad.sum())} of {bad.numel()} off"
+
+
+@pytest.mark.parametrize("out_in", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_weight_gradients_of_many_tiles(dtype, out_in):
+    """More tiles than the GPU takes at a time: empty experts, sums that end on and
+    beside a block of 64, and rows of NaN that belong to none."""
+    g = np.random.default_rng(8)
+    counts = g.integers(0, 200, 128)
+    counts[[0, 5, 6, 127]] = 0
+    counts[[1, 2, 3, 9, 64, 126]] = [384, 385, 383, 700, 64, 1]
+    off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    rows = off[-1] + 11
+    x, w, b, r, dy, z = _problem(rows, 264, 2000, DT[dtype], 17, 1, out_in)
+    w = w.expand(128, *w.shape[1:]).contiguous() if not out_in else w.transpose(1, 2).expand(128, 2000, 264).contiguous().transpose(1, 2)
+    x[off[-1]:] = math.nan
+    dy[off[-1]:] = math.nan
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        dx, dw, db = muon.expert_linear_backward(dy, x, o, w, dx=False)
+        muon.check_ops_error()
+        _check_dw(dw, x, dy, off)
+
+
+def test_many_experts_keep_apart():
+    """NaN rows of every fourth expert reach no other expert's weight gradient."""
+    counts = np.tile([100, 37, 300, 64], 32)
+    off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    x, w, b, r, dy, z = _problem(off[-1], 256, 2048, torch.bfloat16, 18)
+    w = torch.zeros(128, 256, 2048, dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    want = muon.expert_linear_backward(dy, x, o, w, dx=False)[1]
+    _check_dw(want, x, dy, off)
+    for e in range(1, 128, 4):
+        x[off[e]:off[e + 1]] = math.nan
+        dy[off[e]:off[e + 1]] = math.inf
+    got = muon.expert_linear_backward(dy, x, o, w, dx=False)[1]
+    keep = [e for e in range(128) if e % 4 != 1]
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[1::4]).all()
+
+
+@pytest.mark.parametrize("rows", [70, 300, 384, 385])
+def test_weight_gradient_of_a_large_matrix(rows):
+    """A matrix of more tiles than the GPU takes at a time, odd widths, short sums."""
+    x, w, b, r, dy, z = _problem(rows, 4100, 16000, torch.bfloat16, 19)
+    dw = muon.linear_backward(dy, x, w, dx=False)[1]
+    muon.check_ops_error()
+    _check_dw(dw[None], x, dy, [0, rows])
