@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "linear.cuh"
 
@@ -263,11 +264,21 @@ __device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane,
 // cannot store.
 __device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int row0, int col0,
                                             int64_t d_base) {
-  const int64_t N = p.N;
   if (col0 + lane < p.N) {
-    const int c = col0 + lane;
-    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr)
-      st_el(p.D, d_base + (row0 + rr) * N + c, sw[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)], p.type);
+    const int rows = min(32, p.M - row0);
+    const int64_t at = d_base + (int64_t)row0 * p.N + col0 + lane;
+    const float* col = sw + (lane & 3);
+    const auto value = [&](int rr) { return col[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2)]; };
+    // the type outside the loop, several rows in flight
+    const auto store = [&](auto* d) {
+      using T = std::remove_reference_t<decltype(*d)>;
+      d += at;
+#pragma unroll 8
+      for (int rr = 0; rr < rows; ++rr) d[(int64_t)rr * p.N] = from_f32<T>(value(rr));
+    };
+    if (p.type == DT_BF16) store(static_cast<__nv_bfloat16*>(p.D));
+    else if (p.type == DT_F16) store(static_cast<__half*>(p.D));
+    else store(static_cast<float*>(p.D));
   }
   __syncwarp();  // the block is overwritten next
 }
@@ -695,18 +706,68 @@ __global__ void __launch_bounds__(256) k_split_rows(SplitRows first, SplitRows s
     *reinterpret_cast<uint4*>(q.dst + ((b * 3 + k) * q.rows + r) * q.pitch + c) = *reinterpret_cast<const uint4*>(h[k]);
 }
 
+// Eight 16-bit elements from any address: two aligned 16-byte loads and a shift
+// where both lie in begin .. end, else element by element; nothing outside is
+// read.  The loads (fetch) are apart from the rest (finish) so that a thread has
+// several pieces in flight.
+struct Unaligned {
+  uintptr_t begin, end;
+  struct Piece {
+    uint4 v0, v1;
+  };
+  __device__ __forceinline__ bool inside(const uint16_t* p) const {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+    return lo >= begin && lo + 32 <= end;
+  }
+  __device__ __forceinline__ Piece fetch(const uint16_t* p, bool wanted) const {
+    Piece u{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (wanted && inside(p)) {
+      const uint4* lo = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+      u.v0 = __ldcs(lo);
+      u.v1 = __ldcs(lo + 1);
+    }
+    return u;
+  }
+  // The elements, those from the n-th on as zeros.
+  __device__ __forceinline__ uint4 finish(const Piece& s, const uint16_t* p, int64_t n) const {
+    const uint32_t w[8] = {s.v0.x, s.v0.y, s.v0.z, s.v0.w, s.v1.x, s.v1.y, s.v1.z, s.v1.w};
+    const int word = (int)(reinterpret_cast<uintptr_t>(p) & 15) >> 2;
+    const int bits = (int)(reinterpret_cast<uintptr_t>(p) & 3) * 8;
+    uint32_t o[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)  // w[word + i] without an indexed register
+      o[i] = word == 0 ? w[i] : word == 1 ? w[i + 1] : word == 2 ? w[i + 2] : w[i + 3];
+    const uint4 u = make_uint4(__funnelshift_r(o[0], o[1], bits), __funnelshift_r(o[1], o[2], bits),
+                               __funnelshift_r(o[2], o[3], bits), __funnelshift_r(o[3], o[4], bits));
+    if (n >= 8 && inside(p)) return u;
+    alignas(16) uint16_t h[8];  // a row's end, or the buffer's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = i < n ? p[i] : (uint16_t)0;
+    return *reinterpret_cast<const uint4*>(h);
+  }
+};
+
+// 16-bit rows to an aligned pitch, zeros in the padding: blockDim.x pieces of
+// eight elements of kPadRows rows a block, gridDim.y blocks a row.
+constexpr int kPadRows = 4;
 __global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t stride, int64_t batch_stride,
-                                                  uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols) {
+                                                  uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols,
+                                                  int64_t batch) {
   grid_launch_next();
   grid_wait();
-  const int64_t r = blockIdx.x, b = blockIdx.z;
-  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  const int64_t r0 = (int64_t)blockIdx.x * kPadRows, b = blockIdx.z;
+  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
   if (c >= pitch) return;
-  const uint16_t* s = src + b * batch_stride + r * stride + c;
-  uint16_t h[8];
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(src);
+  const Unaligned d{begin, begin + (uintptr_t)(((batch - 1) * batch_stride + (rows - 1) * stride + cols) * 2)};
+  const uint16_t* s = src + b * batch_stride + r0 * stride + c;
+  Unaligned::Piece u[kPadRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = c + i < cols ? s[i] : (uint16_t)0;
-  *reinterpret_cast<uint4*>(dst + (b * rows + r) * pitch + c) = *reinterpret_cast<const uint4*>(h);
+  for (int k = 0; k < kPadRows; ++k) u[k] = d.fetch(s + k * stride, r0 + k < rows);
+#pragma unroll
+  for (int k = 0; k < kPadRows; ++k)
+    if (r0 + k < rows)
+      *reinterpret_cast<uint4*>(dst + (b * rows + r0 + k) * pitch + c) = d.finish(u[k], s + k * stride, cols - c);
 }
 
 bool aligned_rows(const void* p, int64_t stride, int type) {
@@ -905,9 +966,12 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
 
 cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
                             int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
-  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)batch);
-  return launch_early(k_pad_rows, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src), stride, batch_stride,
-                      static_cast<uint16_t*>(dst), pitch, rows, cols);
+  const int64_t pieces = pitch / 8, blocks = (pieces + 255) / 256;
+  const unsigned threads = (unsigned)(((pieces + blocks - 1) / blocks + 31) / 32 * 32);
+  return launch_early(k_pad_rows, dim3((unsigned)((rows + kPadRows - 1) / kPadRows), (unsigned)blocks, (unsigned)batch),
+                      dim3(threads), 0, s,
+                      static_cast<const uint16_t*>(src), stride, batch_stride, static_cast<uint16_t*>(dst), pitch,
+                      rows, cols, batch);
 }
 
 cudaError_t launch_split_rows(const SplitRows& first, const SplitRows& second, cudaStream_t s) {

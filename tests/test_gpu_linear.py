@@ -74,6 +74,16 @@ def test_dense(size, dtype, out_in):
     _both(*size, DT[dtype], act, out_in, seed=sum(size))
 
 
+@pytest.mark.parametrize("out_in", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("size", [(1, 4097, 515), (5, 2051, 1025), (16, 66, 9000), (40, 515, 130), (63, 777, 2049),
+                                  (64, 9001, 40)], ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_of_odd_widths(size, out_in):
+    """Long sums shared by a cluster, rows that start on no 16 bytes."""
+    _both(*size, torch.bfloat16, "silu", out_in, seed=sum(size))
+    x, w, b, r, dy, z = _problem(*size, torch.float16, 3, out_in=out_in)
+    check_forward(muon.linear(x, w), None, x, w, None, "none", None)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("rows", [5, 384])
