@@ -122,3 +122,24 @@ def test_sort_refuses(lib):
         bad = list(good)
         bad[i] = v
         assert lib.muon_combine_backward(*bad) == INVALID, (i, v)
+
+
+def test_header_compiles_as_c(tmp_path):
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    src = tmp_path / "ops.c"
+    src.write_text('#include "muon_ops.h"\nint main(void) { muon_linear_args a = {0}; return (int)a.rows; }\n')
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-Wno-missing-field-initializers",
+                        "-I", os.path.join(ROOT, "include"), "-fsyntax-only", str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_argument_structure_matches_the_header():
+    hdr = open(os.path.join(ROOT, "include", "muon_ops.h"), encoding="utf-8").read()
+    body = re.search(r"typedef struct \{(.*?)\} muon_linear_args;", hdr, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    names = [n.strip(" *") for decl in body.split(";") if decl.strip()
+             for n in re.sub(r"^\s*(const\s+)?\w+", "", decl.strip()).split(",")]
+    assert names == [f[0] for f in _capi.muon_linear_args._fields_]
