@@ -76,7 +76,10 @@ typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_weight_layout_t;
  * preact, and writes those of dx, dw and db that are not NULL:
  *   dz = dy * act'(z), dx = dz W^T, dw = x^T dz, db = sum over rows of dz
  * (the residual's gradient is dy itself).  All tensors are of `dtype`.  fp32
- * products are fp32 throughout. */
+ * operands are cut into three bf16 numbers that together hold their 24 bits (in
+ * scratch), and six partial products summed in fp32 make a product to within
+ * 2^-22 of its size; below about 2^-100 an operand loses low bits, and where an
+ * infinite operand would make a sum infinite the result may be NaN. */
 typedef struct {
   int32_t dtype;       /* muon_dtype_t                                        */
   int32_t activation;  /* muon_activation_t                                   */

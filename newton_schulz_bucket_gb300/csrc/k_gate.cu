@@ -6,7 +6,8 @@
 // (the exponential is monotone, and this way equal logits stay equal), as
 // integers in the same order: a round of the choice is one warp reduction and
 // one vote, and the first lane that holds the maximum holds the lowest expert.
-// Bound by instruction issue, not by HBM: 16384 tokens of 64 experts are 4 MB.
+// Bound by instruction issue, not by HBM: 131072 tokens of 64 experts, 34 MB, take
+// 44 us (35 back), 32768 of 512 take 48 (40 back); 16384 of 64 take 7.
 #include "common.cuh"
 #include "ops.h"
 

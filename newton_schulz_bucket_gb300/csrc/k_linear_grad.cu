@@ -1,7 +1,8 @@
 // What the two products of a layer's gradient start from: dz = dy * act'(z),
 // and the bias gradient, the column sums of dz over each expert's rows.
 //
-// One pass over dy and z, bound by HBM.  A block takes kGradChunk rows and 32
+// One pass over dy and z, bound by HBM ([4096, 16384] bf16 through gelu: 76 us, 5.3
+// TB/s; element by element it took 212).  A block takes kGradChunk rows and 32
 // pieces of columns (16 bytes each where rows allow it), eight threads to a
 // column piece that take every eighth row.  The part of the sum that chunk c
 // adds to range e goes to row c + e of `part` (along the rows c and e only

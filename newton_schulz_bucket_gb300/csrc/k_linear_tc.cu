@@ -17,17 +17,23 @@
 //
 // Rows form (y = x W, dx = dz W^T).  The weight matrix is the M operand and
 // the token rows are the N operand, i.e. a tile is 256 features x N tokens.  N
-// is chosen per tile from the rows there are, in steps of 32: a single token
-// streams the weights through 32-column MMAs, and an expert with 257 rows costs
-// two tiles of 160 and 128 columns, not two of 256.  An accumulator lane is a
-// feature, so a warp's stores run along a token's row for any width and
-// alignment.
+// is chosen per tile from the rows there are, in steps of 32: few rows stream the
+// weights through 32-column MMAs, and an expert with 257 rows costs two tiles of
+// 160 and 128 columns, not two of 256.  An accumulator lane is a feature, so a
+// warp's stores run along a token's row for any width and alignment.  Measured:
+// [4096 x 4096] x [4096, 16384] with gelu and its pre-activation 346 us back to
+// back (1590 TFLOP/s under the power cap, where cuBLAS alone sustains 1700); 64
+// experts [7168, 2048] with 16 rows each 263 us (7.1 TB/s of weights: HBM), with
+// 256 rows 315 us (1530 TFLOP/s), with 320 rows 410 us: two tiles an expert, bound
+// by neither HBM nor the MMAs alone.
 //
 // Sum form (dw = x^T dz).  Both operands are stored across the sum (tokens);
-// tiles are 256 x 256 or 256 x 128.  With few tokens to an expert the epilogue
-// sets the pace: 32 x 64 blocks of rounded outputs are staged swizzled and
-// leave by TMA stores (where output rows start on 16 bytes), so that the
-// load/store pipe carries each output once, not three times.
+// tiles are 256 x 256 or 256 x 128.  With few tokens to an expert the stores set
+// the pace: 32 x 64 blocks of rounded outputs are staged swizzled and leave by TMA
+// stores (where output rows start on 16 bytes), so that the load/store pipe
+// carries each output once, not three times (654 -> 564 us at its first measure).
+// 64 experts [2048, 7168] from 64 rows each: 356 us (5.3 TB/s of stores), from 256
+// rows 400 us, from 512 rows 618 us, where loads alone would take 474.
 //
 // Experts.  Row ranges come from a device array, so every role walks the
 // ranges itself.  GROUP_ROWS: an expert's rows are tiled from its first row;
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of a split sum, in order, and runs the epilogue: output
-// [rows][cols], 8 columns a thread.  Row ranges: a row's expert by bisection.
+// [rows][cols], 8 columns a thread.
 __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p, int rows, int cols) {
   grid_launch_next();
   grid_wait();
@@ -621,17 +627,6 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= per_row * rows) return;
   const int64_t row = i / per_row, c = (i - row * per_row) * 8;
-  int e = 0;
-  if (p.mode == GROUP_ROWS) {
-    if (row >= range_at(p, p.experts, rows)) return;  // of no expert: cleared by the product's kernel
-    int a = 0, b = p.experts;  // offsets[a] <= row < offsets[b]
-    while (b - a > 1) {
-      const int m = (a + b) / 2;
-      if (range_at(p, m, rows) <= row) a = m;
-      else b = m;
-    }
-    e = a;
-  }
   float v[8] = {};
   for (int s = 0; s < p.splits; ++s) {
     const uint4* src = reinterpret_cast<const uint4*>(p.part + ((int64_t)s * rows + row) * p.part_pitch + c);
@@ -641,11 +636,10 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
     for (int k = 0; k < 8; ++k) v[k] += f[k];
   }
   const int n = (int)min((int64_t)8, cols - c);
-  const int64_t bi = (int64_t)e * cols + c;
   if (p.vec && n == 8 && p.type != DT_F32) {
     float b[8];
     if (p.bias) {
-      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + bi), b, p.type);
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + c), b, p.type);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
@@ -661,7 +655,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
   }
   for (int k = 0; k < n; ++k) {
     float z = v[k];
-    if (p.bias) z += ld_el(p.bias, bi + k, p.type);
+    if (p.bias) z += ld_el(p.bias, c + k, p.type);
     if (p.preact) st_el(p.preact, row * cols + c + k, z, p.type);
     z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
     if (p.residual) z += ld_el(p.residual, row * p.r_m + c + k, p.type);
