@@ -7,7 +7,8 @@
 // column piece that take every eighth row.  The part of the sum that chunk c
 // adds to range e goes to row c + e of `part` (along the rows c and e only
 // grow, so no two pairs share a row), and a second kernel adds each range's
-// parts in row order: the same bits every time, and no atomics.
+// parts in row order: the same bits every time, and no atomics.  Up to
+// kGradSingle rows are one chunk, whose sums are the result.
 #include "act.cuh"
 #include "common.cuh"
 
@@ -57,7 +58,8 @@ __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int
   const int64_t chunk = blockIdx.x / col_blocks;
   const int64_t col = ((int64_t)(blockIdx.x % col_blocks) * kLanes + lane) * VEC;
   const bool live = col < g.cols;
-  const int64_t r0 = chunk * kGradChunk, r1 = min(r0 + kGradChunk, g.rows);
+  const bool single = g.rows <= kGradSingle;
+  const int64_t r0 = single ? 0 : chunk * kGradChunk, r1 = single ? g.rows : min(r0 + kGradChunk, g.rows);
   const T* dy = static_cast<const T*>(g.dy) + col;
   const T* z = static_cast<const T*>(g.z) + col;
   T* dz = static_cast<T*>(g.dz);
@@ -71,8 +73,9 @@ __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int
       else e = m + 1;
     }
   }
+  if (single) e = 0;  // empty ranges too: their sums are stored here
   // the chunk's rows range by range; rows of no expert are left out
-  for (int64_t a = r0; e < ranges && a < r1; ++e) {
+  for (int64_t a = r0; e < ranges && (a < r1 || (single && g.db)); ++e) {
     const int64_t b = min(off_at(g, e + 1), r1);
     float sum[VEC] = {};
     if (live) {
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int
         for (int i = 0; i < VEC; ++i) sum[i] += v[i];
       }
     }
-    if (g.part && b > a) {
+    if (g.db && (b > a || single)) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) red[rl][i * kLanes + lane] = sum[i];
       __syncthreads();
@@ -100,7 +103,9 @@ __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int
 #pragma unroll
         for (int k = 0; k < kRowLanes; ++k) s += red[k][i];
         const int64_t c = ((int64_t)(blockIdx.x % col_blocks) * kLanes + i % kLanes) * VEC + i / kLanes;
-        if (c < g.cols) g.part[(chunk + e) * g.cols + c] = s;
+        if (c >= g.cols) continue;
+        if (single) static_cast<T*>(g.db)[e * g.cols + c] = from_f32<T>(s);
+        else g.part[(chunk + e) * g.cols + c] = s;
       }
       __syncthreads();
     }
@@ -129,7 +134,8 @@ __global__ void __launch_bounds__(256) k_grad_bias(GradPrep g, int col_blocks) {
 template <typename T, int VEC>
 cudaError_t prep(const GradPrep& g, cudaStream_t s) {
   const int cb = (int)((g.cols + kLanes * VEC - 1) / (kLanes * VEC));
-  const dim3 grid((unsigned)((g.rows + kGradChunk - 1) / kGradChunk * cb)), block(kLanes * kRowLanes);
+  const int64_t chunks = g.rows <= kGradSingle ? 1 : (g.rows + kGradChunk - 1) / kGradChunk;
+  const dim3 grid((unsigned)(chunks * cb)), block(kLanes * kRowLanes);
   switch (g.act) {
     case ACT_RELU: return launch_early(k_grad_prep<T, VEC, ACT_RELU>, grid, block, 0, s, g, cb);
     case ACT_SILU: return launch_early(k_grad_prep<T, VEC, ACT_SILU>, grid, block, 0, s, g, cb);
@@ -148,7 +154,7 @@ cudaError_t run(const GradPrep& g, cudaStream_t s) {
   // 16-byte pieces where every row of every tensor starts on 16 bytes
   const bool vec = g.cols % V == 0 && ok(g.dy, g.dy_stride) && ok(g.z, g.cols) && ok(g.dz, g.dz_stride);
   cudaError_t e = vec ? prep<T, V>(g, s) : prep<T, 1>(g, s);
-  if (e == cudaSuccess && g.db) {
+  if (e == cudaSuccess && g.db && g.rows > kGradSingle) {
     const int cb = (int)((g.cols + 255) / 256);
     e = launch_early(k_grad_bias<T>, dim3((unsigned)cb * (g.experts ? g.experts : 1)), dim3(256), 0, s, g, cb);
   }

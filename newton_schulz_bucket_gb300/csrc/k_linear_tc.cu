@@ -663,43 +663,6 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
   }
 }
 
-// fp32 rows into three bf16 planes: dst [batch][3][rows][pitch], zeros in the
-// padding.  Truncation leaves remainders that are exact in fp32; a non-finite
-// value goes whole into the high plane.  Up to two tensors a launch.
-__global__ void __launch_bounds__(256) k_split_rows(SplitRows first, SplitRows second) {
-  grid_launch_next();
-  grid_wait();
-  const bool two = blockIdx.z >= first.batch;
-  const SplitRows& q = two ? second : first;
-  const int64_t r = blockIdx.x, b = blockIdx.z - (two ? first.batch : 0);
-  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
-  if (r >= q.rows || c >= q.pitch) return;
-  const float* s = q.src + b * q.batch_stride + r * q.stride + c;
-  float f[8];
-  if (c + 8 <= q.cols && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
-    u4_to_f4x2(reinterpret_cast<const uint4*>(s)[0], reinterpret_cast<const uint4*>(s)[1], f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < q.cols ? s[i] : 0.f;
-  }
-  uint16_t h[3][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v = f[i];
-    const bool finite = fabsf(v) < __int_as_float(0x7f800000);
-    if (v != v) v = __int_as_float(0x7fc00000);  // a NaN whose high half is one too
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-      h[k][i] = (uint16_t)(top >> 16);
-      v = finite ? v - __uint_as_float(top) : 0.f;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 3; ++k)
-    *reinterpret_cast<uint4*>(q.dst + ((b * 3 + k) * q.rows + r) * q.pitch + c) = *reinterpret_cast<const uint4*>(h[k]);
-}
-
 // Eight 16-bit elements from any address: two aligned 16-byte loads and a shift
 // where both lie in begin .. end, else element by element; nothing outside is
 // read.  The loads (fetch) are apart from the rest (finish) so that a thread has
@@ -741,27 +704,85 @@ struct Unaligned {
   }
 };
 
-// 16-bit rows to an aligned pitch, zeros in the padding: blockDim.x pieces of
-// eight elements of kPadRows rows a block, gridDim.y blocks a row.
-constexpr int kPadRows = 4;
-__global__ void __launch_bounds__(256) k_pad_rows(const uint16_t* src, int64_t stride, int64_t batch_stride,
-                                                  uint16_t* dst, int64_t pitch, int64_t rows, int64_t cols,
-                                                  int64_t batch) {
+// Operands that TMA cannot read as they are, up to two tensors a launch.  fp32
+// rows become three bf16 planes, dst [batch][3][rows][pitch]: truncation leaves
+// remainders that are exact in fp32, and a non-finite value goes whole into the
+// high plane.  16-bit rows are copied, dst [batch][rows][pitch].  Padding is zero.
+// A thread takes a piece of eight elements of kPrepRows rows.
+constexpr int kPrepRows = 4;
+struct PrepBlocks {
+  RowsJob job;
+  int64_t blocks;              // of this job
+  int64_t row_blocks;
+  int col_blocks, per;         // blocks along a row, pieces of each
+};
+
+__device__ __forceinline__ void split_piece(const float* s, int64_t n, uint4* plane) {
+  float f[8];
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
+    u4_to_f4x2(__ldcs(reinterpret_cast<const uint4*>(s)), __ldcs(reinterpret_cast<const uint4*>(s) + 1), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? s[i] : 0.f;
+  }
+  alignas(16) uint16_t h[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v = f[i];
+    const bool finite = fabsf(v) < __int_as_float(0x7f800000);
+    if (v != v) v = __int_as_float(0x7fc00000);  // a NaN whose high half is one too
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+      h[k][i] = (uint16_t)(top >> 16);
+      v = finite ? v - __uint_as_float(top) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) plane[k] = *reinterpret_cast<const uint4*>(h[k]);
+}
+
+template <bool kSplit>
+__global__ void __launch_bounds__(256) k_prepare_rows(const __grid_constant__ PrepBlocks first,
+                                                      const __grid_constant__ PrepBlocks second) {
   grid_launch_next();
   grid_wait();
-  const int64_t r0 = (int64_t)blockIdx.x * kPadRows, b = blockIdx.z;
-  const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 8;
-  if (c >= pitch) return;
-  const uintptr_t begin = reinterpret_cast<uintptr_t>(src);
-  const Unaligned d{begin, begin + (uintptr_t)(((batch - 1) * batch_stride + (rows - 1) * stride + cols) * 2)};
-  const uint16_t* s = src + b * batch_stride + r0 * stride + c;
-  Unaligned::Piece u[kPadRows];
+  int64_t at = blockIdx.x;
+  const bool two = at >= first.blocks;
+  if (two) at -= first.blocks;
+  const PrepBlocks& q = two ? second : first;
+  const RowsJob& j = q.job;
+  if ((int)threadIdx.x >= q.per) return;
+  const int64_t c = ((at % q.col_blocks) * q.per + threadIdx.x) * 8;
+  at /= q.col_blocks;
+  const int64_t r0 = at % q.row_blocks * kPrepRows, b = at / q.row_blocks;
+  if (c >= j.pitch) return;
+  if constexpr (kSplit) {
+    const float* s = static_cast<const float*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
+    uint4 u[kPrepRows][3];
 #pragma unroll
-  for (int k = 0; k < kPadRows; ++k) u[k] = d.fetch(s + k * stride, r0 + k < rows);
+    for (int k = 0; k < kPrepRows; ++k)
+      if (r0 + k < j.rows) split_piece(s + k * j.stride, j.cols - c, u[k]);
 #pragma unroll
-  for (int k = 0; k < kPadRows; ++k)
-    if (r0 + k < rows)
-      *reinterpret_cast<uint4*>(dst + (b * rows + r0 + k) * pitch + c) = d.finish(u[k], s + k * stride, cols - c);
+    for (int k = 0; k < kPrepRows; ++k)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        if (r0 + k < j.rows)
+          *reinterpret_cast<uint4*>(j.dst + ((b * 3 + p) * j.rows + r0 + k) * j.pitch + c) = u[k][p];
+  } else {
+    const uint16_t* s = static_cast<const uint16_t*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(j.src);
+    const Unaligned d{begin,
+                      begin + (uintptr_t)(((j.batch - 1) * j.batch_stride + (j.rows - 1) * j.stride + j.cols) * 2)};
+    Unaligned::Piece u[kPrepRows];
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) u[k] = d.fetch(s + k * j.stride, r0 + k < j.rows);
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k)
+      if (r0 + k < j.rows)
+        *reinterpret_cast<uint4*>(j.dst + (b * j.rows + r0 + k) * j.pitch + c) =
+            d.finish(u[k], s + k * j.stride, j.cols - c);
+  }
 }
 
 bool aligned_rows(const void* p, int64_t stride, int type) {
@@ -958,20 +979,23 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
   return e;
 }
 
-cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
-                            int64_t rows, int64_t cols, int64_t batch, cudaStream_t s) {
-  const int64_t pieces = pitch / 8, blocks = (pieces + 255) / 256;
-  const unsigned threads = (unsigned)(((pieces + blocks - 1) / blocks + 31) / 32 * 32);
-  return launch_early(k_pad_rows, dim3((unsigned)((rows + kPadRows - 1) / kPadRows), (unsigned)blocks, (unsigned)batch),
-                      dim3(threads), 0, s,
-                      static_cast<const uint16_t*>(src), stride, batch_stride, static_cast<uint16_t*>(dst), pitch,
-                      rows, cols, batch);
-}
-
-cudaError_t launch_split_rows(const SplitRows& first, const SplitRows& second, cudaStream_t s) {
-  const int64_t rows = std::max(first.rows, second.rows), pitch = std::max(first.pitch, second.pitch);
-  const dim3 grid((unsigned)rows, (unsigned)((pitch + 2047) / 2048), (unsigned)(first.batch + second.batch));
-  return launch_early(k_split_rows, grid, dim3(256), 0, s, first, second);
+cudaError_t launch_prepare_rows(bool split, const RowsJob& first, const RowsJob& second, cudaStream_t s) {
+  unsigned threads = 32;
+  const auto blocks = [&](const RowsJob& j) {
+    PrepBlocks p{j, 0, 1, 1, 1};
+    if (j.batch == 0) return p;
+    const int64_t pieces = j.pitch / 8;
+    p.col_blocks = (int)((pieces + 255) / 256);
+    p.per = (int)((pieces + p.col_blocks - 1) / p.col_blocks);
+    p.row_blocks = (j.rows + kPrepRows - 1) / kPrepRows;
+    p.blocks = j.batch * p.row_blocks * p.col_blocks;
+    threads = std::max(threads, (unsigned)((p.per + 31) / 32 * 32));
+    return p;
+  };
+  const PrepBlocks a = blocks(first), b = blocks(second);
+  const dim3 grid((unsigned)(a.blocks + b.blocks));
+  return split ? launch_early(k_prepare_rows<true>, grid, dim3(threads), 0, s, a, b)
+               : launch_early(k_prepare_rows<false>, grid, dim3(threads), 0, s, a, b);
 }
 
 }  // namespace muon

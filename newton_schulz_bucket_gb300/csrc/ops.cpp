@@ -172,33 +172,27 @@ struct Operand {
   const void* p;
   int64_t stride, batch_stride;
 };
-// `waiting` holds an fp32 split that has not been launched: two go together.
+// `waiting` holds a job that has not been launched: two go together.
 Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch,
-                    SplitRows* waiting, cudaStream_t s, cudaError_t* e) {
-  if (dtype == DT_F32) {
-    const int64_t pitch = (cols + 7) / 8 * 8;
-    void* dst = c.take((size_t)(batch * 3 * rows * pitch * 2));
-    const SplitRows mine{static_cast<const float*>(o.p), o.stride, o.batch_stride, static_cast<uint16_t*>(dst), pitch,
-                         rows, cols, batch};
-    if (waiting->batch == 0) {
-      *waiting = mine;
-    } else {
-      if (launch && *e == cudaSuccess) *e = launch_split_rows(*waiting, mine, s);
-      *waiting = SplitRows{};
-    }
-    return {dst, pitch, rows * pitch};
-  }
-  const bool ok = (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
+                    RowsJob* waiting, cudaStream_t s, cudaError_t* e) {
+  const bool split = dtype == DT_F32;
+  const bool ok = !split && (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
                   (batch == 1 || o.batch_stride % 8 == 0);
   if (ok) return o;
   const int64_t pitch = (cols + 7) / 8 * 8;
-  void* dst = c.take((size_t)(batch * rows * pitch * 2));
-  if (launch && *e == cudaSuccess) *e = launch_pad_rows(o.p, o.stride, o.batch_stride, dst, pitch, rows, cols, batch, s);
+  void* dst = c.take((size_t)(batch * (split ? 3 : 1) * rows * pitch * 2));
+  const RowsJob mine{o.p, o.stride, o.batch_stride, static_cast<uint16_t*>(dst), pitch, rows, cols, batch};
+  if (waiting->batch == 0) {
+    *waiting = mine;
+  } else {
+    if (launch && *e == cudaSuccess) *e = launch_prepare_rows(split, *waiting, mine, s);
+    *waiting = RowsJob{};
+  }
   return {dst, pitch, rows * pitch};
 }
 
 // One product.  `ready` operands went through tma_operand already.
-cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool launch, SplitRows waiting,
+cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool launch, RowsJob waiting,
                         cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const bool a_along = p.a_k == 1, b_along = p.b_k == 1;
@@ -216,7 +210,7 @@ cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool la
     (b_along ? p.b_n : p.b_k) = b.stride;
     p.b_e = b.batch_stride;
   }
-  if (launch && e == cudaSuccess && waiting.batch) e = launch_split_rows(waiting, SplitRows{}, s);
+  if (launch && e == cudaSuccess && waiting.batch) e = launch_prepare_rows(p.dtype == DT_F32, waiting, RowsJob{}, s);
   if (linear_few_fits(p)) {
     if (!launch || e != cudaSuccess) return e;
     e = ops_error_word(&p.err);
@@ -232,7 +226,7 @@ cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool la
 muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, bool launch, cudaStream_t s) {
   if (!backward) {
     if (a->rows == 0) return MUON_OK;
-    return cuda_status("muon_linear", run_product(forward_product(a), false, false, c, launch, SplitRows{}, s));
+    return cuda_status("muon_linear", run_product(forward_product(a), false, false, c, launch, RowsJob{}, s));
   }
   const char* what = "muon_linear_backward";
   const int64_t b = dtype_size(a->dtype);
@@ -251,18 +245,18 @@ muon_status_t run_linear(const muon_linear_args* a, bool backward, Carve& c, boo
   g.db = a->db;
   g.dz_stride = (a->out + 7) / 8 * 8;
   if (act && products) g.dz = c.take((size_t)(a->rows * g.dz_stride * b));
-  if (a->db)
+  if (a->db && a->rows > kGradSingle)
     g.part = static_cast<float*>(c.take(((a->rows + kGradChunk - 1) / kGradChunk + mats) * a->out * sizeof(float)));
   cudaError_t e = cudaSuccess;
   if (launch && (act || a->db)) e = launch_grad_prep(g, s);
   Operand dz{act ? g.dz : a->dy, act ? g.dz_stride : a->dy_stride, 0};
   Operand x{a->x, a->x_stride, 0};
-  SplitRows waiting{};
+  RowsJob waiting{};
   if (products) dz = tma_operand(a->dtype, dz, a->rows, a->out, 1, c, launch, &waiting, s, &e);  // once for both
   if (a->dw) x = tma_operand(a->dtype, x, a->rows, a->in, 1, c, launch, &waiting, s, &e);
   if (a->dx && e == cudaSuccess) {
     e = run_product(dx_product(a, dz.p, dz.stride), true, false, c, launch, waiting, s);
-    waiting = SplitRows{};
+    waiting = RowsJob{};
   }
   if (a->dw && e == cudaSuccess)
     e = run_product(dw_product(a, x.p, x.stride, dz.p, dz.stride), true, true, c, launch, waiting, s);

@@ -52,7 +52,7 @@ struct GradPrep {
   const void* z;
   void* dz;                    // row pitch dz_stride
   int64_t dz_stride;
-  float* part;                 // [chunks + ranges][cols] partial sums
+  float* part;                 // rows > kGradSingle: [chunks + ranges][cols] partial sums
   void* db;                    // [ranges][cols]
 };
 
@@ -69,20 +69,20 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
 bool linear_few_fits(const Product& p);
 cudaError_t launch_linear_few(const Product& p, cudaStream_t s);
 int num_sms();
-// 16-bit rows copied to a pitch that TMA can read: rows of every matrix.
-cudaError_t launch_pad_rows(const void* src, int64_t stride, int64_t batch_stride, void* dst, int64_t pitch,
-                            int64_t rows, int64_t cols, int64_t batch, cudaStream_t s);
-// fp32 rows as three bf16 planes: dst [batch][3][rows][pitch]; batch 0: none.
-struct SplitRows {
-  const float* src;
+// Rows made readable for TMA: 16-bit ones copied to a pitch of whole 16 bytes, dst
+// [batch][rows][pitch]; fp32 ones as three bf16 planes, dst [batch][3][rows][pitch].
+// batch 0: no job.
+struct RowsJob {
+  const void* src;
   int64_t stride, batch_stride;
   uint16_t* dst;
   int64_t pitch, rows, cols, batch;
 };
-cudaError_t launch_split_rows(const SplitRows& first, const SplitRows& second, cudaStream_t s);
+cudaError_t launch_prepare_rows(bool split, const RowsJob& first, const RowsJob& second, cudaStream_t s);
 cudaError_t ops_error_word(int** err);  // device address of the error word of the current device
 
-constexpr int kGradChunk = 128;  // rows of one partial column sum
+constexpr int kGradChunk = 128;   // rows of one partial column sum
+constexpr int kGradSingle = 256;  // up to these rows are summed at once
 
 cudaError_t launch_grad_prep(const GradPrep& g, cudaStream_t s);
 

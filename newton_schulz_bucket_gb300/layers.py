@@ -273,6 +273,7 @@ def gate(logits, top_k, renormalize=True):
     index -1 and weight 0."""
     dev, stream, code = _start(logits, "logits", 2)
     tokens, experts = logits.shape
+    top_k = int(top_k)
     idx = _empty((tokens, top_k), dtype=_I32, device=dev)
     wts = _empty((tokens, top_k), dtype=_F32, device=dev)
     st = _c.load().muon_gate(code, tokens, experts, top_k, renormalize, logits.data_ptr(), _rows(logits, "logits"),
@@ -328,7 +329,7 @@ def dispatch(x, indices, n_experts):
         raise ValueError(f"indices must be [tokens, top_k] with tokens = {tokens}, got {list(indices.shape)}")
     if indices.dtype != _I32 and indices.dtype != _I64:
         raise ValueError(f"indices has dtype {indices.dtype}, expected int32 or int64")
-    top_k = indices.shape[1]
+    top_k, n_experts = indices.shape[1], int(n_experts)
     ip = _contiguous(indices, "indices", dev, indices.dtype, indices.shape)
     L = _c.load()
     n = C.c_size_t()
