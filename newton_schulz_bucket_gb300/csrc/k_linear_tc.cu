@@ -47,7 +47,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "linear.cuh"
 
@@ -266,25 +265,46 @@ __device__ __forceinline__ void stage_block(uint32_t taddr, float* sw, int lane,
 }
 
 // Rows row0 .. row0 + 31 (those < M) and columns col0 .. col0 + 31 (those < N)
-// of the output from the staging block, one column a lane, for rows that TMA
+// of an fp32 output from the staging block, one column a lane, for rows that TMA
 // cannot store.
 __device__ __forceinline__ void write_block(const TcProduct& p, const float* sw, int lane, int row0, int col0,
                                             int64_t d_base) {
   if (col0 + lane < p.N) {
     const int rows = min(32, p.M - row0);
-    const int64_t at = d_base + (int64_t)row0 * p.N + col0 + lane;
+    float* d = static_cast<float*>(p.D) + d_base + (int64_t)row0 * p.N + col0 + lane;
     const float* col = sw + (lane & 3);
-    const auto value = [&](int rr) { return col[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2)]; };
-    // the type outside the loop, several rows in flight
-    const auto store = [&](auto* d) {
-      using T = std::remove_reference_t<decltype(*d)>;
-      d += at;
 #pragma unroll 8
-      for (int rr = 0; rr < rows; ++rr) d[(int64_t)rr * p.N] = from_f32<T>(value(rr));
-    };
-    if (p.type == DT_BF16) store(static_cast<__nv_bfloat16*>(p.D));
-    else if (p.type == DT_F16) store(static_cast<__half*>(p.D));
-    else store(static_cast<float*>(p.D));
+    for (int rr = 0; rr < rows; ++rr) d[(int64_t)rr * p.N] = col[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2)];
+  }
+  __syncwarp();  // the block is overwritten next
+}
+
+// 32 rows x 64 columns of a 16-bit output from the block that stage_rounded
+// wrote, for rows that TMA cannot store: two columns a lane where rows start on 4
+// bytes, else one at a time.  (Aligned 16-byte windows put together by shifts,
+// with single elements at a row's ends, took 1.3 times as long.)
+__device__ __forceinline__ void write_rounded(const TcProduct& p, const uint8_t* sw, int lane, int row0, int col0,
+                                              int64_t d_base) {
+  const int rows = min(32, p.M - row0), n = p.N - col0;
+  uint16_t* d = static_cast<uint16_t*>(p.D) + d_base + (int64_t)row0 * p.N + col0;
+  if ((p.N & 1) == 0 && (reinterpret_cast<uintptr_t>(p.D) & 3) == 0) {
+    if (2 * lane < n) {
+#pragma unroll 8
+      for (int rr = 0; rr < rows; ++rr)
+        *reinterpret_cast<uint32_t*>(d + (int64_t)rr * p.N + 2 * lane) =
+            *reinterpret_cast<const uint32_t*>(sw + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h * 32 + lane;
+      if (c < n) {
+#pragma unroll 8
+        for (int rr = 0; rr < rows; ++rr)
+          d[(int64_t)rr * p.N + c] =
+              *reinterpret_cast<const uint16_t*>(sw + rr * 128 + (((c >> 3) ^ (rr & 7)) << 4) + (c & 7) * 2);
+      }
+    }
   }
   __syncwarp();  // the block is overwritten next
 }
@@ -536,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* sw = smem + L::kEpi + (warp - 2) * 4096;
         const bool zero = it.k0 >= it.k1;
         const int c0 = half * (BN / 2);  // this warp's columns of the tile
-        if (p.splits == 1 && p.vec && p.type != DT_F32) {
+        const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
+        if (p.splits == 1 && p.type != DT_F32) {
 #pragma unroll 1
           for (int c = c0; c < c0 + BN / 2; c += 64) {
             if (it.n0 + c >= p.N || row0 >= p.M) break;  // the same for the whole warp
@@ -548,12 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             tmem_wait_ld();
             stage_rounded(v, sw, lane, zero, p.type);
+            if (!p.vec) {
+              __syncwarp();
+              write_rounded(p, sw, lane, row0, it.n0 + c, d_base);
+              continue;
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tma_store_3d(&mapD, saddr(sw), it.n0 + c, row0, it.e);
           }
         } else {
-          const int64_t d_base = group_sum ? (int64_t)it.e * p.M * p.N : 0;
 #pragma unroll 1
           for (int c = c0; c < c0 + BN / 2; c += 32) {
             if (it.n0 + c >= p.N || row0 >= p.M) break;
@@ -619,25 +644,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of a split sum, in order, and runs the epilogue: output
-// [rows][cols], 8 columns a thread.
+// [rows][cols], VEC columns a thread: 8 (16-bit types whose rows start on 16
+// bytes) or 1.
+template <int VEC>
 __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcProduct p, int rows, int cols) {
   grid_launch_next();
   grid_wait();
-  const int64_t per_row = (cols + 7) / 8;
+  const int64_t per_row = cols / VEC;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= per_row * rows) return;
-  const int64_t row = i / per_row, c = (i - row * per_row) * 8;
-  float v[8] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.part + ((int64_t)s * rows + row) * p.part_pitch + c);
-    float f[8];
-    u4_to_f4x2(src[0], src[1], f);
+  const int64_t row = i / per_row, c = (i - row * per_row) * VEC;
+  const float* part = p.part + row * p.part_pitch + c;
+  const int64_t between = (int64_t)rows * p.part_pitch;
+  if constexpr (VEC == 1) {
+    float z = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) z += part[s * between];
+    if (p.bias) z += ld_el(p.bias, c, p.type);
+    if (p.preact) st_el(p.preact, row * cols + c, z, p.type);
+    z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
+    if (p.residual) z += ld_el(p.residual, row * p.r_m + c, p.type);
+    st_el(p.D, row * cols + c, z, p.type);
+  } else {
+    float v[8] = {}, b[8];
+    for (int s = 0; s < p.splits; ++s) {
+      const uint4* src = reinterpret_cast<const uint4*>(part + s * between);
+      float f[8];
+      u4_to_f4x2(src[0], src[1], f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += f[k];
-  }
-  const int n = (int)min((int64_t)8, cols - c);
-  if (p.vec && n == 8 && p.type != DT_F32) {
-    float b[8];
+      for (int k = 0; k < 8; ++k) v[k] += f[k];
+    }
     if (p.bias) {
       unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + c), b, p.type);
 #pragma unroll
@@ -651,15 +687,6 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ TcP
       for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + row * cols + c) = pack8(v, p.type);
-    return;
-  }
-  for (int k = 0; k < n; ++k) {
-    float z = v[k];
-    if (p.bias) z += ld_el(p.bias, c + k, p.type);
-    if (p.preact) st_el(p.preact, row * cols + c + k, z, p.type);
-    z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
-    if (p.residual) z += ld_el(p.residual, row * p.r_m + c + k, p.type);
-    st_el(p.D, row * cols + c + k, z, p.type);
   }
 }
 
@@ -756,7 +783,7 @@ __global__ void __launch_bounds__(256) k_prepare_rows(const __grid_constant__ Pr
   const int64_t c = ((at % q.col_blocks) * q.per + threadIdx.x) * 8;
   at /= q.col_blocks;
   const int64_t r0 = at % q.row_blocks * kPrepRows, b = at / q.row_blocks;
-  if (c >= j.pitch) return;
+  if (c >= j.pitch || (j.offsets && __ldg(j.offsets + b) >= __ldg(j.offsets + b + 1))) return;
   if constexpr (kSplit) {
     const float* s = static_cast<const float*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
     uint4 u[kPrepRows][3];
@@ -912,7 +939,7 @@ TilePlan tile_plan(const Product& p) {
   const auto offer = [&](int bn, int tile_rows, int64_t tiles, double cols, double blocks, double bytes) {
     const double per_kb = (p.dtype == DT_F32 ? 6 : 1) * (0.28 * cols / 256 > 0.2 ? 0.28 * cols / 256 : 0.2);
     for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && (p.mode != GROUP_NONE || kb / s < 4)) break;
+      if (s > 1 && (p.mode != GROUP_NONE || kb * (p.dtype == DT_F32 ? 4 : 1) / s < 4)) break;
       const double waves = (double)((tiles * s + pairs - 1) / pairs), uneven = waves * pairs / (double)(tiles * s);
       double t = waves * (blocks / s * per_kb + 1.0);
       const double stream = bytes / 6.2e6 * uneven;
@@ -973,8 +1000,12 @@ cudaError_t launch_linear_tc(const Product& p, const TilePlan& t, float* part, c
   q.err = p.err;
   cudaError_t e = t.bn == 0 ? run_rows(p, q, s) : (t.bn == 256 ? run_sum<256>(p, q, s) : run_sum<128>(p, q, s));
   if (e == cudaSuccess && t.splits > 1) {
-    const int64_t n = (p.N + 7) / 8 * p.M;
-    e = launch_early(k_linear_join, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, q, (int)p.M, (int)p.N);
+    // (vec: columns are whole pieces of 8)
+    const bool vec = q.vec && q.type != DT_F32;
+    const int64_t n = (vec ? p.N / 8 : p.N) * p.M;
+    const dim3 grid((unsigned)((n + 255) / 256));
+    e = vec ? launch_early(k_linear_join<8>, grid, dim3(256), 0, s, q, (int)p.M, (int)p.N)
+            : launch_early(k_linear_join<1>, grid, dim3(256), 0, s, q, (int)p.M, (int)p.N);
   }
   return e;
 }

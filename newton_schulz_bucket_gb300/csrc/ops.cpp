@@ -174,14 +174,15 @@ struct Operand {
 };
 // `waiting` holds a job that has not been launched: two go together.
 Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch,
-                    RowsJob* waiting, cudaStream_t s, cudaError_t* e) {
+                    RowsJob* waiting, cudaStream_t s, cudaError_t* e, const int32_t* offsets = nullptr) {
   const bool split = dtype == DT_F32;
   const bool ok = !split && (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
                   (batch == 1 || o.batch_stride % 8 == 0);
   if (ok) return o;
   const int64_t pitch = (cols + 7) / 8 * 8;
   void* dst = c.take((size_t)(batch * (split ? 3 : 1) * rows * pitch * 2));
-  const RowsJob mine{o.p, o.stride, o.batch_stride, static_cast<uint16_t*>(dst), pitch, rows, cols, batch};
+  const RowsJob mine{o.p, o.stride, o.batch_stride, static_cast<uint16_t*>(dst), pitch, rows, cols, batch,
+                     offsets};
   if (waiting->batch == 0) {
     *waiting = mine;
   } else {
@@ -205,7 +206,8 @@ cudaError_t run_product(Product p, bool a_ready, bool b_ready, Carve& c, bool la
   }
   if (!b_ready) {
     const Operand b = tma_operand(p.dtype, {p.B, b_along ? p.b_n : p.b_k, p.b_e}, b_along ? p.N : p.K,
-                                  b_along ? p.K : p.N, mats, c, launch, &waiting, s, &e);
+                                  b_along ? p.K : p.N, mats, c, launch, &waiting, s, &e,
+                                  p.mode == GROUP_ROWS ? p.offsets : nullptr);
     p.B = b.p;
     (b_along ? p.b_n : p.b_k) = b.stride;
     p.b_e = b.batch_stride;

@@ -77,6 +77,7 @@ struct RowsJob {
   int64_t stride, batch_stride;
   uint16_t* dst;
   int64_t pitch, rows, cols, batch;
+  const int32_t* offsets;      // nullable: matrix b is wanted where offsets[b] < offsets[b + 1]
 };
 cudaError_t launch_prepare_rows(bool split, const RowsJob& first, const RowsJob& second, cudaStream_t s);
 cudaError_t ops_error_word(int** err);  // device address of the error word of the current device
