@@ -2,15 +2,17 @@
 //
 // dispatch: a stable counting sort of the assignments by expert.  Blocks of
 // kSortChunk assignments count their experts, a scan turns the counts into
-// first rows, and the blocks place their assignments in order; then each token's
-// row is read once and written to its top_k rows.  Up to kSortChunk assignments
-// take one launch.
+// first rows, and the blocks place their assignments in order; up to kSortCluster
+// assignments one cluster of blocks does all that in one launch.  Then each
+// token's row is read once and written to its top_k rows.  Up to kSortChunk
+// assignments order and rows take one launch together.
 // combine and the gradients go token by token the other way: a token's row is
 // held in registers while its top_k expert rows stream by, so every byte
 // crosses HBM once.  No atomics on results: slots, sums and dot products are
 // the same bits every time.  Bound by HBM for many tokens: 8192 tokens to eight
 // experts each, hidden 7168 bf16, 175 us there with the order (6.0 TB/s), 156 us
 // back (6.8), 299 us for the gradient of the way back (6.7).
+#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -88,17 +90,48 @@ __device__ __forceinline__ int block_prefix(int v, int* w) {
   return before + incl - v;
 }
 
+// Slots of 1024 assignments, i this thread's and e its expert (-1: none), in
+// order: next[e] is e's first free row, before and after.  Each warp counts its
+// own (equal lanes vote), a prefix over the warps makes the counts stable.
+// warp_count: [32][experts].
+__device__ __forceinline__ void place_round(const SortArgs& a, int64_t i, int64_t n, int e, int* next,
+                                            uint16_t* warp_count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int k = threadIdx.x; k < 32 * a.experts; k += 1024) warp_count[k] = 0;
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  const int before = __popc(same & ((1u << lane) - 1));
+  __syncthreads();
+  if (e >= 0 && before == 0) warp_count[warp * a.experts + e] = (uint16_t)__popc(same);
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.experts; k += 1024) {
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < 32; ++w) {
+      const int c = warp_count[w * a.experts + k];
+      warp_count[w * a.experts + k] = (uint16_t)sum;  // at most 1024
+      sum += c;
+    }
+    next[k] += sum;  // the round's own first row is next - sum
+    warp_count[32 * a.experts + k] = (uint16_t)sum;
+  }
+  __syncthreads();
+  if (i < n)
+    a.slot[i] = e >= 0 ? next[e] - warp_count[32 * a.experts + e] + warp_count[warp * a.experts + e] + before : -1;
+  __syncthreads();
+}
+size_t place_smem(int experts) { return sizeof(int) * experts + sizeof(uint16_t) * 33 * experts; }
+
 __global__ void __launch_bounds__(1024) k_sort_place(SortArgs a, int64_t n) {
   extern __shared__ int next[];
   __shared__ int warps[32];
   grid_launch_next();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   grid_wait();
   {
     const int count = tid < a.experts ? a.total[tid] : 0;
     const int first = block_prefix(count, warps);  // the expert's first row
     if (tid < a.experts) {
-      next[tid] = first + (n ? a.counts[(int64_t)blockIdx.x * a.experts + tid] : 0);
+      next[tid] = first + a.counts[(int64_t)blockIdx.x * a.experts + tid];
       if (blockIdx.x == 0) {
         a.offsets[tid] = first;
         if (tid == a.experts - 1) a.offsets[a.experts] = first + count;
@@ -106,18 +139,55 @@ __global__ void __launch_bounds__(1024) k_sort_place(SortArgs a, int64_t n) {
     }
   }
   const int64_t i = (int64_t)blockIdx.x * kSortChunk + tid;
-  const int e = i < n ? expert_of(a, i) : -1;
-  const unsigned same = __match_any_sync(0xffffffffu, e);
-  const int before = __popc(same & ((1u << lane) - 1));
+  place_round(a, i, n, i < n ? expert_of(a, i) : -1, next, reinterpret_cast<uint16_t*>(next + a.experts));
+}
+
+// The whole order in one launch, for up to kSortCluster assignments: a cluster of
+// eight blocks, each with a run of them.  Counts meet in distributed shared
+// memory instead of scratch.
+constexpr int kClusterBlocks = 8;
+__global__ void __launch_bounds__(1024) k_sort_cluster(SortArgs a, int64_t n) {
+  extern __shared__ int next[];  // [experts] rows, [experts] counts, then place_round's
+  __shared__ int warps[32];
+  int* hist = next + a.experts;
+  grid_launch_next();
+  const int tid = threadIdx.x, rank = blockIdx.x;
+  const int64_t per = (n + kClusterBlocks * kSortChunk - 1) / (kClusterBlocks * kSortChunk) * kSortChunk;
+  const int64_t i0 = rank * per, i1 = min(i0 + per, n);
+  for (int e = tid; e < a.experts; e += 1024) hist[e] = 0;
   __syncthreads();
-  for (int w = 0; w < kSortChunk / 32; ++w) {  // warp by warp: the order of the assignments
-    if (warp == w) {
-      const int first = e >= 0 ? next[e] : 0;
-      __syncwarp();
-      if (e >= 0 && before == 0) next[e] = first + __popc(same);
-      if (i < n) a.slot[i] = e >= 0 ? first + before : -1;
+  grid_wait();
+  for (int64_t i = i0 + tid; i < i1; i += 1024) {
+    const int e = expert_of(a, i);
+    if (e >= 0) atomicAdd(&hist[e], 1);  // whole numbers: the order of the additions does not show
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  int total = 0, before = 0;
+  if (tid < a.experts) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(hist + tid);
+#pragma unroll
+    for (int r = 0; r < kClusterBlocks; ++r) {
+      uint32_t remote;
+      int v;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(r));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+      before += r < rank ? v : 0;
+      total += v;
     }
-    __syncthreads();
+  }
+  // no block leaves, or reuses its counts, while another reads them
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int first = block_prefix(total, warps);
+  if (tid < a.experts) {
+    next[tid] = first + before;
+    if (rank == 0) {
+      a.offsets[tid] = first;
+      if (tid == a.experts - 1) a.offsets[a.experts] = first + total;
+    }
+  }
+  for (int64_t c = i0; c < i0 + per; c += kSortChunk) {  // the same rounds for every thread of the block
+    const int64_t i = c + tid;
+    place_round(a, i, i1, i < i1 ? expert_of(a, i) : -1, next, reinterpret_cast<uint16_t*>(hist + a.experts));
   }
 }
 
@@ -371,7 +441,8 @@ cudaError_t launch_rows(RowOp op, const SortArgs& a, cudaStream_t s) {
   // up to four warps (more blocks an SM, at different points: combine 166 -> 159 us
   // against eight) that divide a block's pieces into even rounds
   const int64_t per = (pieces + y - 1) / y, rounds = (per + 127) / 128;
-  const unsigned threads = (unsigned)(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  unsigned threads = (unsigned)(((per + rounds - 1) / rounds + 31) / 32 * 32);
+  if (op == OP_DISPATCH_SMALL) threads = 128;  // they count assignments first
   const dim3 grid((unsigned)(a.tokens + (op == OP_DISPATCH_SMALL)), (unsigned)y), block(threads);
   if (op == OP_GATHER) return launch_early(k_gather<T, VEC>, grid, block, 0, s, a);
   if (op == OP_DISPATCH_SMALL) return launch_early(k_dispatch_small<T, VEC>, grid, block, 0, s, a);
@@ -400,17 +471,52 @@ cudaError_t rows(RowOp op, const SortArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Shared memory beyond the default for many experts (once per device).
+static cudaError_t prepare_sort() {
+  static bool ready[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && ready[dev]) return cudaSuccess;
+  const int most = (int)(place_smem(1024) + sizeof(int) * 1024);
+  e = cudaFuncSetAttribute(k_sort_place, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && dev < 64) ready[dev] = true;
+  return e;
+}
+
 cudaError_t launch_dispatch(const SortArgs& a, cudaStream_t s) {
   const int64_t n = a.tokens * a.top_k;
   if (n <= kSortChunk) return rows(OP_DISPATCH_SMALL, a, s);
-  const unsigned chunks = (unsigned)((n + kSortChunk - 1) / kSortChunk);
-  const size_t smem = sizeof(int) * a.experts;
+  cudaError_t e = prepare_sort();
+  if (e != cudaSuccess) return e;
   SortArgs b = a;
-  b.total = a.counts + (int64_t)chunks * a.experts;
-  cudaError_t e = launch_early(k_sort_count, dim3(chunks), dim3(kSortChunk), smem, s, b, n);
-  if (e == cudaSuccess)
-    e = launch_early(k_sort_scan, dim3((a.experts + 31) / 32), dim3(1024), 0, s, b, (int)chunks);
-  if (e == cudaSuccess) e = launch_early(k_sort_place, dim3(chunks), dim3(kSortChunk), smem, s, b, n);
+  if (n <= kSortCluster) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(kClusterBlocks);
+    lc.blockDim = dim3(1024);
+    lc.dynamicSmemBytes = place_smem(a.experts) + sizeof(int) * a.experts;
+    lc.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kClusterBlocks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 2;
+    e = cudaLaunchKernelEx(&lc, k_sort_cluster, b, n);
+  } else {
+    const unsigned chunks = (unsigned)((n + kSortChunk - 1) / kSortChunk);
+    b.total = a.counts + (int64_t)chunks * a.experts;
+    e = launch_early(k_sort_count, dim3(chunks), dim3(kSortChunk), sizeof(int) * a.experts, s, b, n);
+    if (e == cudaSuccess)
+      e = launch_early(k_sort_scan, dim3((a.experts + 31) / 32), dim3(1024), 0, s, b, (int)chunks);
+    if (e == cudaSuccess) e = launch_early(k_sort_place, dim3(chunks), dim3(kSortChunk), place_smem(a.experts), s, b, n);
+  }
   if (e == cudaSuccess && a.xs) e = rows(OP_GATHER, b, s);
   return e;
 }

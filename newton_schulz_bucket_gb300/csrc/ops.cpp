@@ -315,7 +315,7 @@ muon_status_t check_row_stride(const char* what, int64_t stride, int64_t hidden)
 }
 
 size_t dispatch_bytes(int64_t tokens, int32_t top_k, int32_t experts) {
-  if (tokens * top_k <= kSortChunk) return 0;
+  if (tokens * top_k <= kSortCluster) return 0;
   const size_t chunks = (size_t)((tokens * top_k + kSortChunk - 1) / kSortChunk);
   return align256((chunks + 1) * experts * sizeof(int32_t));
 }

@@ -121,7 +121,10 @@ struct SortArgs {
   void* dys;
   float* dweights;
 };
-constexpr int kSortChunk = 1024;  // assignments one block counts and places; up to these need no workspace
+constexpr int kSortChunk = 1024;  // assignments one block counts and places
+// Up to these are ordered by one cluster of blocks, without workspace (8000
+// assignments 6.3 us against 8.8 in three launches, 32000 14.7 against 11.6).
+constexpr int kSortCluster = 1 << 14;
 cudaError_t launch_dispatch(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine_backward(const SortArgs& a, cudaStream_t s);

@@ -81,6 +81,27 @@ def test_many_assignments_keep_their_order():
     assert torch.equal(offsets.long(), torch.searchsorted(key.sort()[0], torch.arange(38, device="cuda")))
 
 
+@pytest.mark.parametrize("tokens,top_k,experts", [(1025, 1, 7), (513, 2, 1024), (3000, 3, 300), (8192, 8, 64),
+                                                  (65536, 1, 5), (65537, 1, 1024)])
+def test_order_of_any_number(tokens, top_k, experts):
+    """One block, one cluster of blocks, many blocks: the stable sort by expert."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    idx = torch.randint(0, experts, (tokens, top_k), generator=g, device="cuda", dtype=torch.int32)
+    idx[torch.rand(tokens, top_k, generator=g, device="cuda") < 0.3] = experts // 2
+    idx[torch.rand(tokens, top_k, generator=g, device="cuda") < 0.1] = -1
+    x = torch.arange(tokens, device="cuda", dtype=torch.float32)[:, None].contiguous()
+    flat = idx.reshape(-1).long()
+    key = torch.where(flat >= 0, flat, experts)
+    order = torch.sort(key, stable=True)[1]
+    n = int((flat >= 0).sum())
+    for _ in range(2):
+        xs, slot, offsets = muon.dispatch(x, idx, experts)
+        s = slot.reshape(-1)
+        assert torch.equal(s[order[:n]].long(), torch.arange(n, device="cuda")) and (s[flat < 0] == -1).all()
+        assert torch.equal(xs[:n, 0].long(), order[:n] // top_k) and not xs[n:].any()
+        assert torch.equal(offsets.long(), torch.searchsorted(key.sort()[0], torch.arange(experts + 1, device="cuda")))
+
+
 def test_all_to_one_and_all_dropped():
     x = torch.randn(300, 24, device="cuda").bfloat16()
     one = torch.full((300, 1), 6, dtype=torch.int32, device="cuda")

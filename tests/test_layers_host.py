@@ -96,11 +96,11 @@ def test_gate_refuses(lib):
 def test_sort_refuses(lib):
     n = C.c_size_t()
     assert lib.muon_dispatch_workspace(4, 2, 8, C.byref(n)) == OK and n.value == 0  # few: one launch, no scratch
-    assert lib.muon_dispatch_workspace(4000, 2, 8, C.byref(n)) == OK and n.value > 0
+    assert lib.muon_dispatch_workspace(40000, 2, 8, C.byref(n)) == OK and n.value > 0
     for t, k, e in ((-1, 2, 8), (4, 0, 8), (4, 33, 8), (4, 2, 0), (4, 2, 1025), (1 << 30, 4, 8)):
         assert lib.muon_dispatch_workspace(t, k, e, C.byref(n)) == INVALID
-    lib.muon_dispatch_workspace(4000, 2, 8, C.byref(n))
-    good = [2, 4000, 16, 2, 8, P, 16, P, 32, P, P, P, P, n.value, None]
+    lib.muon_dispatch_workspace(40000, 2, 8, C.byref(n))
+    good = [2, 40000, 16, 2, 8, P, 16, P, 32, P, P, P, P, n.value, None]
     for i, v in ((0, 9), (1, -1), (2, 0), (3, 0), (4, 0), (5, None), (6, 15), (7, None), (8, 16), (10, None),
                  (11, None), (12, None), (12, P + 8), (13, n.value - 1)):
         bad = list(good)
