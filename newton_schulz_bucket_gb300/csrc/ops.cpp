@@ -176,6 +176,7 @@ struct Operand {
 Operand tma_operand(int32_t dtype, Operand o, int64_t rows, int64_t cols, int64_t batch, Carve& c, bool launch,
                     RowsJob* waiting, cudaStream_t s, cudaError_t* e, const int32_t* offsets = nullptr) {
   const bool split = dtype == DT_F32;
+  if (rows == 1 && batch == 1 && !split) o.stride = (o.stride + 7) / 8 * 8;  // no second row: any pitch does
   const bool ok = !split && (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.stride % 8 == 0 &&
                   (batch == 1 || o.batch_stride % 8 == 0);
   if (ok) return o;
