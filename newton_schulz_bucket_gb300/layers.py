@@ -135,8 +135,12 @@ def _linear_call(backward):
 
 def _run(backward, dev, stream, head, strides, ptrs):
     """One call: head = dtype .. out, then strides, then pointers x .. db."""
-    # what the size depends on: the problem, which tensors there are, and 16-byte alignment
-    key = (backward, head, strides, tuple([p & 15 if p else -1 for p in ptrs]))
+    # what the size depends on: the problem, 16-byte alignment, and the gradients asked for
+    x, w = ptrs[0], ptrs[1]
+    if backward:
+        key = (head, strides, x & 15, w & 15, ptrs[6] & 15, ptrs[9] > 0, ptrs[10] > 0, ptrs[11] > 0)
+    else:
+        key = (head, strides, x & 15, w & 15)
     size = _scratch_sizes.get(key)
     if size is None:
         n = C.c_size_t()
