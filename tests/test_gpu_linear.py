@@ -234,6 +234,40 @@ def test_side_stream_and_graph():
     assert all(torch.equal(p, q) for p, q in zip(d, again))
 
 
+def test_graph_that_forks_and_joins():
+    """Calls on two streams inside one capture, each starting from the other's
+    result, next to PyTorch's own kernels and a memset."""
+    x, w, b, r, dy, z = _problem(160, 256, 256, torch.bfloat16, 20)
+    w2 = _normal(_gen(21), 256, 256, std=1 / 16, dtype=torch.bfloat16)
+
+    def run(side):
+        main = torch.cuda.current_stream()
+        a = muon.linear(x, w, activation="silu")
+        if side is not None:
+            side.wait_stream(main)
+        c = muon.linear(a, w2, stream=side) if side is not None else muon.linear(a, w2)
+        d = muon.linear(a, w, activation="relu")
+        zero = torch.zeros_like(d)
+        if side is not None:
+            main.wait_stream(side)
+        e = muon.linear(c + zero, w, residual=d)
+        g = muon.linear_backward(e, c, w2, bias=True)
+        return a, c, d, e, *g
+
+    want = run(None)
+    side = torch.cuda.Stream()
+    eager = run(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(eager, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(held, want))
+
+
 PAD = 512
 
 
