@@ -38,7 +38,10 @@ __device__ __forceinline__ bool aligned16(const void* p) {
 // one before it drains (once all of that one's blocks have called
 // grid_launch_next or left), and touches no memory before grid_wait returns, by
 // which time the one before it is done.  Every such kernel waits in every
-// block, so that completion carries over from launch to launch.
+// block, so that completion carries over from launch to launch.  Non-coherent
+// loads (__ldg, ld.global.nc, const __restrict__) are not for these kernels: they
+// are defined for memory that nobody writes while the kernel is resident, and the
+// launch before may still be writing then.
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>

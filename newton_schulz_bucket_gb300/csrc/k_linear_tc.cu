@@ -105,7 +105,7 @@ __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_add
 }
 
 __device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
-  const int v = __ldg(p.offsets + e);
+  const int v = p.offsets[e];  // (an earlier launch may have written them while this one was resident)
   return v < 0 ? 0 : (v > hi ? hi : v);
 }
 
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(256) k_prepare_rows(const __grid_constant__ Pr
   const int64_t c = ((at % q.col_blocks) * q.per + threadIdx.x) * 8;
   at /= q.col_blocks;
   const int64_t r0 = at % q.row_blocks * kPrepRows, b = at / q.row_blocks;
-  if (c >= j.pitch || (j.offsets && __ldg(j.offsets + b) >= __ldg(j.offsets + b + 1))) return;
+  if (c >= j.pitch || (j.offsets && j.offsets[b] >= j.offsets[b + 1])) return;
   if constexpr (kSplit) {
     const float* s = static_cast<const float*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
     uint4 u[kPrepRows][3];
