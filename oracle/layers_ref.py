@@ -8,7 +8,7 @@ import math
 import numpy as np
 
 ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def _sigmoid(z):
@@ -24,7 +24,7 @@ def act(z, kind):
     if kind == "silu":
         return z * _sigmoid(z)
     if kind == "gelu":
-        return z * (1.0 + _erf(z / math.sqrt(2.0))) / 2.0
+        return z * _erfc(-z / math.sqrt(2.0)) / 2.0
     if kind == "gelu_tanh":
         return z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3))) / 2.0
     raise KeyError(kind)
@@ -40,7 +40,7 @@ def act_slope(z, kind):
         s = _sigmoid(z)
         return s + z * s * (1.0 - s)
     if kind == "gelu":
-        return (1.0 + _erf(z / math.sqrt(2.0))) / 2.0 + z * np.exp(-z * z / 2.0) / math.sqrt(2.0 * math.pi)
+        return _erfc(-z / math.sqrt(2.0)) / 2.0 + z * np.exp(-z * z / 2.0) / math.sqrt(2.0 * math.pi)
     if kind == "gelu_tanh":
         c = math.sqrt(2.0 / math.pi)
         t = np.tanh(c * (z + 0.044715 * z ** 3))

@@ -1,0 +1,56 @@
+"""The layer products at the ends of their range: tails of the activations,
+pre-activations near the type's largest value, the worst mantissas and the
+non-finite values of fp32 operands, very long sums and very wide matrices."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_bucket_gb300 as muon
+
+from layers_tol import TINY, U, to64
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+SMOOTH = ["silu", "gelu", "gelu_tanh"]
+
+
+def _tail(z, kind):
+    """(act(z), act'(z), a bound of their relative error in fp32) for z <= -3,
+    without the cancellation that 1 + erf or 1 + tanh has there."""
+    phi = np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if kind == "gelu":
+        # erfc: 4 ulp of its own; its argument is off by 1.5 roundings of 2^-24, which
+        # z^2 + 1 magnifies; the exponential of z^2 / 2 likewise, and its own error
+        # grows by 1.2 ulp a unit of its argument
+        cdf = np.array([math.erfc(-v / math.sqrt(2)) / 2 for v in z])
+        return z * cdf, cdf + z * phi, 2 * z * z + 16
+    if kind == "silu":
+        w, dw = z, np.ones_like(z)
+    else:
+        w = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        dw = 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    p = 1 / (1 + np.exp(-w))
+    # w is off by 6 roundings of 2^-24 at most, the exponential by 2 + 1.2 |w| ulp
+    return z * p, p + z * p * (1 - p) * dw, 5 * np.abs(w) + 24
+
+
+@pytest.mark.parametrize("kind", SMOOTH)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_activation_tails_keep_their_relative_error(dtype, kind):
+    """z in [-9, -3], through a 1 x 1 weight of 1 (products are exact).  The slope
+    adds two terms of opposite sign of which the larger is at most 1.6 times the
+    sum there."""
+    dt = DT[dtype]
+    z = torch.linspace(-9, -3, 400, device="cuda").to(dt)[:, None].contiguous()
+    one = torch.ones(1, 1, dtype=dt, device="cuda")
+    y = muon.linear(z, one, activation=kind)
+    dx = muon.linear_backward(torch.ones_like(z), z, one, preact=z, activation=kind, dw=False)[0]
+    muon.check_ops_error()
+    want, slope, rel = _tail(to64(z)[:, 0], kind)
+    for what, got, ref, r in (("y", y, want, rel * 2.0 ** -23), ("dx", dx, slope, 2.6 * rel * 2.0 ** -23)):
+        err = np.abs(to64(got)[:, 0] - ref)
+        tol = (r + 1.01 * U[dt]) * np.abs(ref) + TINY[dt]
+        assert (err <= tol).all(), f"{what}: {np.max(err / np.abs(ref)):.3g} of the value, allowed {np.max(r):.3g}"
