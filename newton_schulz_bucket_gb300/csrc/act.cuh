@@ -93,7 +93,9 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case ACT_GELU_TANH: {
       const float p = sigmoid<kFast>(2.f * kSqrt2OverPi * (z + kTanhCubic * z * z * z));
-      return p + 2.f * z * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kTanhCubic * z * z);
+      // p (1 - p) is zero outside -16 .. 16, where z^2 may overflow
+      const float c = fminf(fmaxf(z, -16.f), 16.f);
+      return p + 2.f * c * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kTanhCubic * c * c);
     }
     default: return 1.f;
   }

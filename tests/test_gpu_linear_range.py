@@ -54,3 +54,19 @@ def test_activation_tails_keep_their_relative_error(dtype, kind):
         err = np.abs(to64(got)[:, 0] - ref)
         tol = (r + 1.01 * U[dt]) * np.abs(ref) + TINY[dt]
         assert (err <= tol).all(), f"{what}: {np.max(err / np.abs(ref)):.3g} of the value, allowed {np.max(r):.3g}"
+
+
+@pytest.mark.parametrize("kind", ["relu", *SMOOTH])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_slopes_of_large_preactivations(dtype, kind):
+    """Finite pre-activations of any size: the value is z or 0, the slope 1 or 0."""
+    dt = DT[dtype]
+    most = float(torch.finfo(dt).max)
+    z = [v for v in (100.0, 1e4, 1e10, 1.9e19, 5e19, 1e20, 1e30, most / 2, most) if v <= most]
+    z = torch.tensor([*z, *(-v for v in z)], dtype=torch.float64, device="cuda").to(dt)[:, None]
+    one = torch.ones(1, 1, dtype=dt, device="cuda")
+    up = (z > 0).to(dt)
+    dx, dw, db = muon.linear_backward(torch.ones_like(z), torch.ones_like(z), one, preact=z, activation=kind, bias=True)
+    assert torch.equal(dx, up)
+    assert dw.item() == db.item() == up.sum().item()
+    assert torch.equal(muon.linear(z, one, activation=kind), z * up)
