@@ -78,8 +78,10 @@ typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_weight_layout_t;
  * (the residual's gradient is dy itself).  All tensors are of `dtype`.  fp32
  * operands are cut into three bf16 numbers that together hold their 24 bits (in
  * scratch), and six partial products summed in fp32 make a product to within
- * 2^-22 of its size; below about 2^-100 an operand loses low bits, and where an
- * infinite operand would make a sum infinite the result may be NaN. */
+ * 2^-22 of its size (2^-24 is left out, the rest is the sum's rounding; a product
+ * within 2^-7 of the largest number may come out infinite); below about 2^-100 an
+ * operand loses low bits, and where an infinite operand would make a sum infinite
+ * the result may be NaN. */
 typedef struct {
   int32_t dtype;       /* muon_dtype_t                                        */
   int32_t activation;  /* muon_activation_t                                   */

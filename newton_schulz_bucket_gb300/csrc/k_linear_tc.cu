@@ -1,11 +1,13 @@
 // A layer's product on the tensor cores: D(m, n) = act(sum_k A(m, k) B(k, n) +
 // bias) + residual in fp16 / bf16 operands with fp32 sums.
 //
-// fp32 tensors.  Each operand is cut into three bf16 numbers, x = h + m + l with
-// 8 significant bits each (truncated, so the three hold all 24 bits), and the
-// product is the sum of the six partial products down to h l, m m and l h; what
-// is left out is below 2^-23 of the whole.  Six bf16 products are 4 to 5 times
-// as fast as one in fp32 FMA.
+// fp32 tensors.  Each operand is cut into three bf16 numbers, x = h + m + l, each
+// the nearest to what is left (8 significant bits, so the three hold all 24), and
+// the product is the sum of the six partial products down to h l, m m and l h.  A
+// part is at most 2^-8 (m) and 2^-17 (l) of the operand's power of two, so that what is
+// left out, m l + l m + l l, is below 2^-24 of the product and of either sign (cut off
+// instead of rounded, the parts would leave out up to 2^-21, always towards zero).  Six
+// bf16 products are 4 to 5 times as fast as one in fp32 FMA.
 //
 // A cluster of two CTAs computes one 256 x N tile (N <= 256) with tcgen05.mma
 // cta_group::2, as the Newton-Schulz products do: each CTA stages its 128 rows
@@ -732,9 +734,10 @@ struct Unaligned {
 };
 
 // Operands that TMA cannot read as they are, up to two tensors a launch.  fp32
-// rows become three bf16 planes, dst [batch][3][rows][pitch]: truncation leaves
-// remainders that are exact in fp32, and a non-finite value goes whole into the
-// high plane.  16-bit rows are copied, dst [batch][rows][pitch].  Padding is zero.
+// rows become three bf16 planes, dst [batch][3][rows][pitch]: each is what is left
+// rounded to nearest, whose remainder is exact in fp32, and a non-finite value goes
+// whole into the high plane.  16-bit rows are copied, dst [batch][rows][pitch].
+// Padding is zero.
 // A thread takes a piece of eight elements of kPrepRows rows.
 constexpr int kPrepRows = 4;
 struct PrepBlocks {
@@ -757,12 +760,14 @@ __device__ __forceinline__ void split_piece(const float* s, int64_t n, uint4* pl
   for (int i = 0; i < 8; ++i) {
     float v = f[i];
     const bool finite = fabsf(v) < __int_as_float(0x7f800000);
-    if (v != v) v = __int_as_float(0x7fc00000);  // a NaN whose high half is one too
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-      h[k][i] = (uint16_t)(top >> 16);
-      v = finite ? v - __uint_as_float(top) : 0.f;
+      __nv_bfloat16 part = __float2bfloat16_rn(v);
+      // not carried past the largest number: cut off there
+      if (k == 0 && finite && fabsf(v) >= __int_as_float(0x7f7f8000))
+        part = __ushort_as_bfloat16((uint16_t)(__float_as_uint(v) >> 16));
+      h[k][i] = __bfloat16_as_ushort(part);
+      v = finite ? v - __bfloat162float(part) : 0.f;
     }
   }
 #pragma unroll

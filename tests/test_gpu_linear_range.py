@@ -70,3 +70,32 @@ def test_slopes_of_large_preactivations(dtype, kind):
     assert torch.equal(dx, up)
     assert dw.item() == db.item() == up.sum().item()
     assert torch.equal(muon.linear(z, one, activation=kind), z * up)
+
+
+@pytest.mark.parametrize("rows", [8, 300])
+def test_fp32_products_of_the_worst_mantissas(rows):
+    """One-term sums to within 2^-22 of the product, as the header states: of
+    numbers whose three parts are all as large as they can be, and of any.
+    (Left-out partial products 2^-24, one truncating add at the product's size
+    2^-23, the adds of the smaller ones below 2^-29.)"""
+    g = np.random.default_rng(3)
+    bits = np.concatenate([np.array([0x3f80ffff, 0x3f80fffe, 0x3f80feff, 0x3f807fff, 0x3f808000, 0x3f808001, 0x3f80ff7f,
+                                     0x3fffffff, 0x3f817f7f], dtype=np.uint32),
+                           g.integers(0x3f800000, 0x40000000, 400, dtype=np.uint32),
+                           0x3f800000 + (g.integers(0, 128, 400, dtype=np.uint32) << 16) + g.integers(0xff00, 0x10000, 400, dtype=np.uint32)])
+    a = bits.view(np.float32).astype(np.float64)
+    x, w = np.resize(a, rows), a * np.where(np.arange(a.size) % 3 == 0, -2.0 ** 20, 2.0 ** -30)
+    y = muon.linear(torch.tensor(x, dtype=torch.float32, device="cuda")[:, None],
+                    torch.tensor(w, dtype=torch.float32, device="cuda")[None])
+    want = x[:, None] * w
+    rel = np.abs(to64(y) - want) / np.abs(want)
+    assert rel.max() <= 2.0 ** -22, rel.max() * 2.0 ** 22
+
+
+def test_fp32_products_next_to_the_largest_number():
+    """Operands that rounding to fewer bits would carry past the largest number."""
+    most = float(np.finfo(np.float32).max)
+    x = torch.tensor([[most], [-most], [most * (1 - 2.0 ** -10)], [3.3961775e38]], device="cuda")
+    w = torch.tensor([[0.25, -0.4999, 1e-30, 2.0 ** -40]], device="cuda")
+    want = to64(x) * to64(w)
+    assert (np.abs(to64(muon.linear(x, w)) - want) <= 2.0 ** -22 * np.abs(want)).all()
