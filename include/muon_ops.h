@@ -80,8 +80,8 @@ typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_weight_layout_t;
  * scratch), and six partial products summed in fp32 make a product to within
  * 2^-22 of its size (2^-24 is left out, the rest is the sum's rounding; a product
  * within 2^-7 of the largest number may come out infinite); below about 2^-100 an
- * operand loses low bits, and where an infinite operand would make a sum infinite
- * the result may be NaN. */
+ * operand loses low bits, and below 2^-134 it counts as zero.  Infinities and NaN
+ * follow the formula. */
 typedef struct {
   int32_t dtype;       /* muon_dtype_t                                        */
   int32_t activation;  /* muon_activation_t                                   */

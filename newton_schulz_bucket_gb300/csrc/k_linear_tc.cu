@@ -9,6 +9,11 @@
 // instead of rounded, the parts would leave out up to 2^-21, always towards zero).  Six
 // bf16 products are 4 to 5 times as fast as one in fp32 FMA.
 //
+// An infinity or a NaN goes into the low part, with h = +-1 and m = 0 beside it: of
+// the six products only h l and l h then see it, each time against the other
+// operand's h, which is zero only where that operand is (in the high part it would
+// meet the zero m and l of every short number, and make NaN of 1 times infinity).
+//
 // A cluster of two CTAs computes one 256 x N tile (N <= 256) with tcgen05.mma
 // cta_group::2, as the Newton-Schulz products do: each CTA stages its 128 rows
 // of the M operand and its half of the N operand's rows in a ring of TMA tiles,
@@ -736,7 +741,7 @@ struct Unaligned {
 // Operands that TMA cannot read as they are, up to two tensors a launch.  fp32
 // rows become three bf16 planes, dst [batch][3][rows][pitch]: each is what is left
 // rounded to nearest, whose remainder is exact in fp32, and a non-finite value goes
-// whole into the high plane.  16-bit rows are copied, dst [batch][rows][pitch].
+// into the low plane beside +-1, 0.  16-bit rows are copied, dst [batch][rows][pitch].
 // Padding is zero.
 // A thread takes a piece of eight elements of kPrepRows rows.
 constexpr int kPrepRows = 4;
@@ -747,27 +752,39 @@ struct PrepBlocks {
   int col_blocks, per;         // blocks along a row, pieces of each
 };
 
-__device__ __forceinline__ void split_piece(const float* s, int64_t n, uint4* plane) {
-  float f[8];
+__device__ __forceinline__ void load_piece(const float* s, int64_t n, float* f) {
   if (n >= 8 && (reinterpret_cast<uintptr_t>(s) & 15) == 0) {
     u4_to_f4x2(__ldcs(reinterpret_cast<const uint4*>(s)), __ldcs(reinterpret_cast<const uint4*>(s) + 1), f);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = i < n ? s[i] : 0.f;
   }
-  alignas(16) uint16_t h[3][8];
+}
+__device__ __forceinline__ void split_piece(const float* f, uint4* plane) {
+  alignas(16) __nv_bfloat16 h[3][8];
+  bool plain = true;  // not infinite or NaN, nor carried there by the first rounding
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float v = f[i];
-    const bool finite = fabsf(v) < __int_as_float(0x7f800000);
+    plain &= fabsf(f[i]) < __int_as_float(0x7f7f8000);
+    h[0][i] = __float2bfloat16_rn(f[i]);
+    const float v = f[i] - __bfloat162float(h[0][i]);
+    h[1][i] = __float2bfloat16_rn(v);
+    h[2][i] = __float2bfloat16_rn(v - __bfloat162float(h[1][i]));
+  }
+  if (!plain) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      __nv_bfloat16 part = __float2bfloat16_rn(v);
-      // not carried past the largest number: cut off there
-      if (k == 0 && finite && fabsf(v) >= __int_as_float(0x7f7f8000))
-        part = __ushort_as_bfloat16((uint16_t)(__float_as_uint(v) >> 16));
-      h[k][i] = __bfloat16_as_ushort(part);
-      v = finite ? v - __bfloat162float(part) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(f[i]) < __int_as_float(0x7f7f8000)) continue;
+      if (fabsf(f[i]) < __int_as_float(0x7f800000)) {  // cut off, not rounded up
+        const float top = __uint_as_float(__float_as_uint(f[i]) & 0xffff0000u), v = f[i] - top;
+        h[0][i] = __float2bfloat16_rn(top);
+        h[1][i] = __float2bfloat16_rn(v);
+        h[2][i] = __float2bfloat16_rn(v - __bfloat162float(h[1][i]));
+      } else {
+        h[0][i] = __float2bfloat16_rn(copysignf(1.f, f[i]));
+        h[1][i] = __float2bfloat16_rn(0.f);
+        h[2][i] = __float2bfloat16_rn(f[i]);
+      }
     }
   }
 #pragma unroll
@@ -791,16 +808,19 @@ __global__ void __launch_bounds__(256) k_prepare_rows(const __grid_constant__ Pr
   if (c >= j.pitch || (j.offsets && j.offsets[b] >= j.offsets[b + 1])) return;
   if constexpr (kSplit) {
     const float* s = static_cast<const float*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
-    uint4 u[kPrepRows][3];
+    float f[kPrepRows][8];  // in flight together
 #pragma unroll
     for (int k = 0; k < kPrepRows; ++k)
-      if (r0 + k < j.rows) split_piece(s + k * j.stride, j.cols - c, u[k]);
+      if (r0 + k < j.rows) load_piece(s + k * j.stride, j.cols - c, f[k]);
 #pragma unroll
-    for (int k = 0; k < kPrepRows; ++k)
+    for (int k = 0; k < kPrepRows; ++k) {
+      if (r0 + k >= j.rows) break;
+      uint4 u[3];
+      split_piece(f[k], u);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
-        if (r0 + k < j.rows)
-          *reinterpret_cast<uint4*>(j.dst + ((b * 3 + p) * j.rows + r0 + k) * j.pitch + c) = u[k][p];
+        *reinterpret_cast<uint4*>(j.dst + ((b * 3 + p) * j.rows + r0 + k) * j.pitch + c) = u[p];
+    }
   } else {
     const uint16_t* s = static_cast<const uint16_t*>(j.src) + b * j.batch_stride + r0 * j.stride + c;
     const uintptr_t begin = reinterpret_cast<uintptr_t>(j.src);

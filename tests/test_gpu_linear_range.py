@@ -99,3 +99,46 @@ def test_fp32_products_next_to_the_largest_number():
     w = torch.tensor([[0.25, -0.4999, 1e-30, 2.0 ** -40]], device="cuda")
     want = to64(x) * to64(w)
     assert (np.abs(to64(muon.linear(x, w)) - want) <= 2.0 ** -22 * np.abs(want)).all()
+
+
+def _same(got, want, tol):
+    """Infinities and NaN where the formula has them, finite values within tol."""
+    got, want = got.double().cpu(), want.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isposinf(got), torch.isposinf(want))
+    assert torch.equal(torch.isneginf(got), torch.isneginf(want))
+    live = torch.isfinite(want)
+    assert ((got - want).abs()[live] <= tol).all()
+
+
+@pytest.mark.parametrize("n", [130, 1024])
+@pytest.mark.parametrize("rows", [6, 40, 200])
+def test_fp32_infinities_follow_the_formula(rows, n):
+    """An infinity in either operand, against weights that fill 8, 16 and 24 bits,
+    zeros, infinities of both signs and NaN; forward, both gradients, and
+    through experts.  Finite sums: 96 terms of size 4."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    k, inf = 96, math.inf
+    x = torch.randn(rows, k, generator=g, device="cuda")
+    w = torch.randn(k, n, generator=g, device="cuda")
+    w[3, :8] = torch.tensor([1.0, -1.0, 0.5, 1.0 + 2.0 ** -12, 0.1, -0.1, 0.0, -0.0])
+    w[3, 8:11] = torch.tensor([inf, -inf, math.nan])
+    w[60, 20], w[61, 20], w[62, 21] = inf, -inf, -inf
+    x[0, 3], x[1, 3], x[2, 60], x[3, 5] = inf, -inf, inf, math.nan
+    x[4, 3], x[4, 60] = inf, -inf
+    x[5, 62] = 0.0
+    dy = torch.randn(rows, n, generator=g, device="cuda")
+    dy[rows - 1, 4], dy[0, 2], dy[1, 1] = inf, -inf, math.nan
+    tol = (1024 + 16) * 2.0 ** -23 * 16 * n
+    d = [t.double().cpu() for t in (x, w, dy)]
+    _same(muon.linear(x, w), d[0] @ d[1], tol)
+    dx, dw, _ = muon.linear_backward(dy, x, w)
+    _same(dx, d[2] @ d[1].T, tol)
+    _same(dw, d[0].T @ d[2], tol)
+    off = torch.tensor([0, 5, 5, rows], dtype=torch.int32, device="cuda")
+    we = torch.stack([w, w, w.flip(1)])
+    _same(muon.expert_linear(x, off, we), torch.cat([d[0][:5] @ d[1], d[0][5:] @ d[1].flip(1)]), tol)
+    dx, dw, _ = muon.expert_linear_backward(dy, x, off, we)
+    _same(dx, torch.cat([d[2][:5] @ d[1].T, d[2][5:] @ d[1].flip(1).T]), tol)
+    _same(dw, torch.stack([d[0][:5].T @ d[2][:5], 0 * w.nan_to_num(0, 0, 0).double().cpu(), d[0][5:].T @ d[2][5:]]), tol)
+    muon.check_ops_error()
