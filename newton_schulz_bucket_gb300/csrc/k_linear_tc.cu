@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t aph = 0;
     for (; more; more = walk.next(p, it)) {
-      if (!mbar_wait(tfull(acc), aph, abort_flag, p.err, 8)) break;
+      const long long limit = sum_wait(it.k1 - it.k0, kProducts - p.first);
+      if (!mbar_wait(tfull(acc), aph, abort_flag, p.err, 8, limit)) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(quarter * 32) << 16);
       const int row0 = it.m0 + (int)rank * 128 + quarter * 32;
@@ -627,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = p.first; ok && i < kProducts; ++i) {
         if (rem) {
           const int st = (s + blocks - 1) % S;
-          if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32))) break;
+          // (the sum's last block: it comes when all others have been taken)
+          if (!(ok = mbar_wait(fix(st), (fph >> st) & 1, abort_flag, p.err, 32, sum_wait(it.k1 - it.k0, 1)))) break;
           fph ^= 1u << st;
           uint8_t* stage = smem + st * L::kStage;
           for (int box = 0; box < (int)(L::kStage / (64 * BK * 2)); ++box)  // 64 rows of k, 128 bytes each

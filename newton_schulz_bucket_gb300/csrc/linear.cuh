@@ -11,6 +11,13 @@ namespace muon {
 
 constexpr int BK = 64;  // steps of the sum in one block of the ring: a 128-byte swizzle row
 
+// Cycles after which a wait for a tile's whole sum gives up: the bound of a short
+// wait, and 4096 for each block of each partial product (which takes 400 to 700), so
+// that no length the calls accept runs into it.
+__device__ __forceinline__ long long sum_wait(int steps, int products) {
+  return kWaitCycles + (long long)((steps + BK - 1) / BK) * products * 4096;
+}
+
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t p;

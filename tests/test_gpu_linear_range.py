@@ -142,3 +142,19 @@ def test_fp32_infinities_follow_the_formula(rows, n):
     _same(dx, torch.cat([d[2][:5] @ d[1].T, d[2][5:] @ d[1].flip(1).T]), tol)
     _same(dw, torch.stack([d[0][:5].T @ d[2][:5], 0 * w.nan_to_num(0, 0, 0).double().cpu(), d[0][5:].T @ d[2][5:]]), tol)
     muon.check_ops_error()
+
+
+def test_a_sum_of_more_rows_than_a_short_wait_allows():
+    """150 million fp32 rows through one expert: its sum takes longer than the
+    bound of the other waits (2^32 cycles).  Sums of +-1 are exact."""
+    rows = 150_000_001
+    if torch.cuda.mem_get_info()[0] < 32 << 30:
+        pytest.skip("needs 32 GiB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, dy = (torch.randint(0, 2, (rows, 1), generator=g, device="cuda", dtype=torch.int8).float().mul_(2).sub_(1)
+             for _ in range(2))
+    off = torch.tensor([0, rows - 5], dtype=torch.int32, device="cuda")
+    w = torch.ones(1, 1, 1, device="cuda")
+    _, dw, _ = muon.expert_linear_backward(dy, x, off, w, dx=False)
+    muon.check_ops_error()
+    assert dw.item() == (x * dy)[:rows - 5].double().sum().item()
