@@ -118,7 +118,8 @@ MUON_API muon_status_t muon_linear_workspace(const muon_linear_args* args, int32
 /* y = act(x W + b) + residual.  Errors, before any launch: INVALID_ARG (NULL
  * args, x, w or y with rows > 0, offsets NULL with experts > 0; a size, enum or
  * stride out of range; workspace too small or not 256-byte aligned; a stream
- * of another device), UNSUPPORTED (more than 2^31 - 1 output tiles), CUDA. */
+ * of another device), UNSUPPORTED (a launch of more than 2^31 - 1025 tiles or
+ * blocks), CUDA. */
 MUON_API muon_status_t muon_linear(const muon_linear_args* args, void* stream);
 
 /* The gradients (above).  Errors: as muon_linear; also INVALID_ARG where dy, or
@@ -162,7 +163,7 @@ MUON_API muon_status_t muon_dispatch_workspace(int64_t tokens, int32_t top_k, in
  * offsets[experts] on are zero.  indices: int32 or int64 (index_bits 32 or
  * 64) [tokens, top_k] contiguous.  xs and slot and offsets are written; xs may
  * be NULL (the order alone; x is then not read).  Errors: INVALID_ARG (NULL
- * pointers, sizes, tokens * top_k > 2^31 - 1, dtype, workspace, stream), CUDA. */
+ * pointers, sizes, tokens * top_k > 2^31 - 1025, dtype, workspace, stream), CUDA. */
 MUON_API muon_status_t muon_dispatch(int32_t dtype, int64_t tokens, int64_t hidden, int32_t top_k,
                                      int32_t experts, const void* x, int64_t x_stride,
                                      const void* indices, int32_t index_bits, void* xs,

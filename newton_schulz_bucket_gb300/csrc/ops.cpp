@@ -32,6 +32,7 @@ bool dtype_ok(int32_t t) { return t == DT_F32 || t == DT_F16 || t == DT_BF16; }
 int64_t dtype_size(int32_t t) { return t == DT_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxDim = 1ll << 30;
+constexpr int64_t kMaxBlocks = 0x7fffffffll - 1024;  // (item counters run ahead by a grid's pairs)
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Launches go to the current device, so the stream has to be one of its own.
@@ -83,17 +84,24 @@ muon_status_t check_linear(const muon_linear_args* a, bool backward, const char*
   if (a->x_stride > (1ll << 36) || a->w_stride > (1ll << 36) || a->w_expert_stride > (1ll << 36) ||
       a->residual_stride > (1ll << 36) || a->dy_stride > (1ll << 36))
     return fail(MUON_ERR_INVALID_ARG, "%s: a stride exceeds 2^36 elements", what);
-  if (a->experts > 1 && a->w_expert_stride < (w_rows - 1) * a->w_stride + w_row)
+  if (a->experts > 1 && (a->w_expert_stride < w_row || (a->w_expert_stride - w_row) / a->w_stride < w_rows - 1))
     return fail(MUON_ERR_INVALID_ARG, "%s: w_expert_stride is shorter than one matrix", what);
   if (a->experts > 0 && !a->offsets)
     return fail(MUON_ERR_INVALID_ARG, "%s: offsets is NULL with experts > 0", what);
-  // tiles of the smallest kind (64 x 64) that any launch of the call counts
-  const auto tiles = [](int64_t m, int64_t n, int64_t extra) { return ((m + 63) / 64 + extra) * ((n + 63) / 64); };
-  if (tiles(a->rows, a->out, a->experts + 1) > 0x7fffffffll || tiles(a->rows, a->in, a->experts + 1) > 0x7fffffffll ||
-      tiles(a->in, a->out, 0) * (a->experts ? a->experts : 1) > 0x7fffffffll || a->out > (1ll << 22) - 64 ||
-      a->in > (1ll << 22) - 64)
-    return fail(MUON_ERR_UNSUPPORTED, "%s: [%lld, %lld] x [%lld, %lld] with %d experts has too many tiles", what,
-                (long long)a->rows, (long long)a->in, (long long)a->in, (long long)a->out, a->experts);
+  // what the kernels count in 32 bits, in the smallest tiles that tile_plan may take
+  const auto up = [](int64_t v, int64_t by) { return (v + by - 1) / by; };
+  const int64_t mats = a->experts ? a->experts : 1, wide = a->in > a->out ? a->in : a->out;
+  const int64_t narrow = a->in > a->out ? a->out : a->in, row_blocks = up(a->rows, 4) * up(wide, 2048);
+  const int64_t counts[] = {
+      (up(a->rows, 64) + mats) * up(wide, 256) * 16,                     // rows form: token tiles x features x parts
+      up(wide, 128) * up(narrow, 128),                                   // sum form: a matrix's tiles
+      2 * row_blocks, row_blocks + mats * up(w_rows, 4) * up(w_row, 2048),  // operands padded or split, two a launch
+      up(a->rows, 128) * up(a->out, 32), up(a->out, 256) * mats,         // the gradient's first pass
+      up(a->rows * wide, 256), up(narrow * wide, 256)};                  // the join of a split sum
+  for (const int64_t n : counts)
+    if (n > kMaxBlocks)
+      return fail(MUON_ERR_UNSUPPORTED, "%s: [%lld, %lld] x [%lld, %lld] with %d experts has too many tiles", what,
+                  (long long)a->rows, (long long)a->in, (long long)a->in, (long long)a->out, a->experts);
   if (!backward) {
     if (!a->w || (a->rows > 0 && (!a->x || !a->y)))
       return fail(MUON_ERR_INVALID_ARG, "%s: x, w and y must be non-NULL", what);

@@ -158,3 +158,19 @@ def test_a_sum_of_more_rows_than_a_short_wait_allows():
     _, dw, _ = muon.expert_linear_backward(dy, x, off, w, dx=False)
     muon.check_ops_error()
     assert dw.item() == (x * dy)[:rows - 5].double().sum().item()
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("n_in,n_out", [((1 << 22) + 72, 8), (16, (1 << 22) + 72)])
+def test_widths_past_4_million(n_in, n_out, rows):
+    """Sums of +-1: exact in fp32, one rounding at the store."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, w, dy = (torch.randint(0, 2, s, generator=g, device="cuda", dtype=torch.int8).bfloat16().mul_(2).sub_(1)
+                for s in ((rows, n_in), (n_in, n_out), (rows, n_out)))
+    d = [t.double() for t in (x, w, dy)]
+    assert torch.equal(muon.linear(x, w), (d[0] @ d[1]).bfloat16())
+    dx, dw, db = muon.linear_backward(dy, x, w, bias=True)
+    assert torch.equal(dx, (d[2] @ d[1].T).bfloat16())
+    assert torch.equal(dw, (d[0].T @ d[2]).bfloat16())
+    assert torch.equal(db, d[2].sum(0).bfloat16())
+    muon.check_ops_error()
