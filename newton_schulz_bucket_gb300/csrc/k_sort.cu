@@ -433,9 +433,10 @@ template <typename T, bool VEC>
 cudaError_t launch_rows(RowOp op, const SortArgs& a, cudaStream_t s) {
   constexpr int N = Piece<T, VEC>::N;
   const int64_t pieces = (a.hidden + N - 1) / N;
-  // enough blocks to fill the GPU (a token's dot products stay in one block)
+  // enough blocks to fill the GPU (a token's dot products stay in one block; without
+  // tokens there are no rows to share out)
   int64_t y = 1;
-  if (op != OP_COMBINE_BACKWARD) {
+  if (op != OP_COMBINE_BACKWARD && a.tokens > 0) {
     while (a.tokens * y < 304 && pieces / (2 * y) >= 32) y *= 2;
   }
   // up to four warps (more blocks an SM, at different points: combine 166 -> 159 us
