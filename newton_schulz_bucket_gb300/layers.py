@@ -4,7 +4,8 @@ order and back, each with its gradient.
 
 Like the plan's steps, these calls work on plain device tensors: no autograd
 graph is built, forward and backward are separate calls, and the gradients they
-return are what ``MuonPlan.step`` takes.  All arithmetic is in the library's
+return are what ``MuonPlan.step`` takes.  Where autograd is recording, a tensor
+that requires grad is refused (a ``torch.autograd.Function`` may call them).  All arithmetic is in the library's
 CUDA kernels (include/muon_ops.h holds the contract of each); this module checks
 tensors, allocates outputs and scratch, and marshals pointers.
 
@@ -41,13 +42,29 @@ _PACK = struct.Struct("=4i8q14Q").pack
 assert struct.calcsize("=4i8q14Q") == C.sizeof(_c.muon_linear_args)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
+_grad_enabled = torch.is_grad_enabled
+_Tensor = torch.Tensor
 
 
-def _on_stream(op):
-    """Adds ``stream`` to an operator that runs on the current stream."""
+def _operator(op):
+    """Adds ``stream`` to an operator that runs on the current stream, and refuses
+    tensors whose gradient autograd would expect and not get."""
+
+    def refuse(args, kw):
+        named = (*zip(op.__code__.co_varnames, args), *kw.items())
+        name = next(n for n, t in named if isinstance(t, _Tensor) and t.requires_grad)
+        raise ValueError(f"{name} requires grad, but {op.__name__} builds no autograd graph: detach it or call under "
+                         "torch.no_grad(); gradients come from the _backward calls")
 
     @functools.wraps(op)
     def call(*args, stream=None, **kw):
+        if _grad_enabled():
+            for t in args:
+                if isinstance(t, _Tensor) and t.requires_grad:
+                    refuse(args, kw)
+            for t in kw.values():
+                if isinstance(t, _Tensor) and t.requires_grad:
+                    refuse(args, kw)
         if stream is None:
             return op(*args, **kw)
         like = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
@@ -225,7 +242,7 @@ def _backward(dy, x, w, offsets, preact, activation, dx, dw, bias):
     return gx, gw, gb
 
 
-@_on_stream
+@_operator
 def linear(x, w, bias=None, activation="none", residual=None, keep_preact=False):
     """y = act(x @ w + bias) + residual for x [rows, in] and w [in, out]; with
     keep_preact (y, z), z = x @ w + bias for the way back.
@@ -236,7 +253,7 @@ def linear(x, w, bias=None, activation="none", residual=None, keep_preact=False)
     return _forward(x, w, None, bias, activation, residual, keep_preact)
 
 
-@_on_stream
+@_operator
 def linear_backward(dy, x, w, preact=None, activation="none", dx=True, dw=True, bias=False):
     """(dx, dw, db) of linear for the gradient dy of its result; those not asked
     for are None.  dw has w's shape and memory order.  The residual's gradient
@@ -244,7 +261,7 @@ def linear_backward(dy, x, w, preact=None, activation="none", dx=True, dw=True, 
     return _backward(dy, x, w, None, preact, activation, dx, dw, bias)
 
 
-@_on_stream
+@_operator
 def expert_linear(x, offsets, w, bias=None, activation="none", residual=None, keep_preact=False):
     """linear over an expert tensor w [experts, in, out]: rows
     offsets[e] .. offsets[e + 1] - 1 of x (int32, on the device, as ``dispatch``
@@ -253,7 +270,7 @@ def expert_linear(x, offsets, w, bias=None, activation="none", residual=None, ke
     return _forward(x, w, _given(offsets), bias, activation, residual, keep_preact)
 
 
-@_on_stream
+@_operator
 def expert_linear_backward(dy, x, offsets, w, preact=None, activation="none", dx=True, dw=True, bias=False):
     """(dx, dw, db) of expert_linear; an expert without rows gets zero dw and db."""
     return _backward(dy, x, w, _given(offsets), preact, activation, dx, dw, bias)
@@ -268,7 +285,7 @@ def _given(offsets):
 # ---- gate ----
 
 
-@_on_stream
+@_operator
 def gate(logits, top_k, renormalize=True):
     """(indices int32, weights float32), [tokens, top_k] each: the experts with
     the largest logits in falling order (ties: the lower index) and their
@@ -287,7 +304,7 @@ def gate(logits, top_k, renormalize=True):
     return idx, wts
 
 
-@_on_stream
+@_operator
 def gate_backward(dweights, logits, indices, renormalize=True):
     """The gradient of gate's logits for that of its weights, the choice held
     fixed (indices as gate gave them)."""
@@ -319,7 +336,7 @@ def _slots(slot, rows, what, dev):
     return _contiguous(slot, "slot", dev, _I32, (tokens, top_k)), tokens, top_k
 
 
-@_on_stream
+@_operator
 def dispatch(x, indices, n_experts):
     """(xs, slot, offsets): the rows of x [tokens, hidden] in expert order.
 
@@ -353,7 +370,7 @@ def dispatch(x, indices, n_experts):
     return xs, slot, offsets
 
 
-@_on_stream
+@_operator
 def dispatch_backward(dxs, slot):
     """dx[t] = sum over j of dxs[slot[t, j]]."""
     dev, stream, code = _start(dxs, "dxs", 2)
@@ -367,7 +384,7 @@ def dispatch_backward(dxs, slot):
     return dx
 
 
-@_on_stream
+@_operator
 def combine(ys, slot, weights, residual=None):
     """y[t] = sum over j of weights[t, j] * ys[slot[t, j]], + residual[t]."""
     dev, stream, code = _start(ys, "ys", 2)
@@ -386,7 +403,7 @@ def combine(ys, slot, weights, residual=None):
     return y
 
 
-@_on_stream
+@_operator
 def combine_backward(dy, ys, slot, offsets, weights):
     """(dys, dweights): dys[slot[t, j]] = weights[t, j] * dy[t], zero in the rows
     that no expert owns, and dweights[t, j] = <ys[slot[t, j]], dy[t]> in fp32
