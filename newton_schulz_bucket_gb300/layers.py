@@ -282,6 +282,13 @@ def _given(offsets):
     return offsets
 
 
+def _int32(n):
+    """n as the C ABI's int32 arguments take it: what does not fit becomes a value
+    that is out of every range, not another number."""
+    n = int(n)
+    return n if -1 <= n <= 0x7fffffff else -1
+
+
 # ---- gate ----
 
 
@@ -294,11 +301,12 @@ def gate(logits, top_k, renormalize=True):
     index -1 and weight 0."""
     dev, stream, code = _start(logits, "logits", 2)
     tokens, experts = logits.shape
-    top_k = int(top_k)
-    idx = _empty((tokens, top_k), dtype=_I32, device=dev)
-    wts = _empty((tokens, top_k), dtype=_F32, device=dev)
-    st = _c.load().muon_gate(code, tokens, experts, top_k, renormalize, logits.data_ptr(), _rows(logits, "logits"),
-                             idx.data_ptr(), wts.data_ptr(), stream)
+    top_k = _int32(top_k)
+    k = top_k if 0 < top_k <= experts else 0  # refused below, with nothing allocated for it
+    idx = _empty((tokens, k), dtype=_I32, device=dev)
+    wts = _empty((tokens, k), dtype=_F32, device=dev)
+    st = _c.load().muon_gate(code, tokens, _int32(experts), top_k, renormalize, logits.data_ptr(),
+                             _rows(logits, "logits"), idx.data_ptr(), wts.data_ptr(), stream)
     if st:
         _c.check(st, "muon_gate")
     return idx, wts
@@ -316,7 +324,7 @@ def gate_backward(dweights, logits, indices, renormalize=True):
     ip = _contiguous(indices, "indices", dev, _I32, (tokens, top_k))
     dp = _contiguous(dweights, "dweights", dev, _F32, (tokens, top_k))
     out = _empty((tokens, experts), dtype=logits.dtype, device=dev)
-    st = _c.load().muon_gate_backward(code, tokens, experts, top_k, renormalize, dp, logits.data_ptr(),
+    st = _c.load().muon_gate_backward(code, tokens, _int32(experts), top_k, renormalize, dp, logits.data_ptr(),
                                       _rows(logits, "logits"), ip, out.data_ptr(), stream)
     if st:
         _c.check(st, "muon_gate_backward")
@@ -350,7 +358,7 @@ def dispatch(x, indices, n_experts):
         raise ValueError(f"indices must be [tokens, top_k] with tokens = {tokens}, got {list(indices.shape)}")
     if indices.dtype != _I32 and indices.dtype != _I64:
         raise ValueError(f"indices has dtype {indices.dtype}, expected int32 or int64")
-    top_k, n_experts = indices.shape[1], int(n_experts)
+    top_k, n_experts = indices.shape[1], _int32(n_experts)
     ip = _contiguous(indices, "indices", dev, indices.dtype, indices.shape)
     L = _c.load()
     n = C.c_size_t()
@@ -418,7 +426,7 @@ def combine_backward(dy, ys, slot, offsets, weights):
     op = _contiguous(offsets, "offsets", dev, _I32, offsets.shape)
     dys = _empty((rows, hidden), dtype=ys.dtype, device=dev)
     dwts = _empty((tokens, top_k), dtype=_F32, device=dev)
-    st = _c.load().muon_combine_backward(code, tokens, hidden, top_k, offsets.shape[0] - 1, dy.data_ptr(),
+    st = _c.load().muon_combine_backward(code, tokens, hidden, top_k, _int32(offsets.shape[0] - 1), dy.data_ptr(),
                                          _rows(dy, "dy"), ys.data_ptr(), _rows(ys, "ys"), sp, op, wp,
                                          dys.data_ptr(), dwts.data_ptr(), stream)
     if st:
