@@ -65,9 +65,10 @@ typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_weight_layout_t;
 /* One product with its epilogue, or its gradient.
  *
  * experts = 0: one matrix.  experts = E >= 1: w is [E] matrices, and rows
- * offsets[e] .. offsets[e + 1] - 1 of x (device int32 [E + 1], increasing from
- * 0) go through matrix e, with row e of bias [E, out].  Rows from offsets[E]
- * on belong to no expert: their outputs are zero and they add to no gradient.
+ * offsets[e] .. offsets[e + 1] - 1 of x (device int32 [E + 1], not decreasing)
+ * go through matrix e, with row e of bias [E, out].  Rows before offsets[0] and
+ * from offsets[E] on belong to no expert: their outputs are zero and they add to
+ * no gradient.
  * (Offsets outside [0, rows] are clamped, so they cannot lead out of a buffer.)
  *
  * muon_linear reads x, w, bias (nullable), residual (nullable; added after

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kLanes* kRowLanes) k_grad_prep(GradPrep g, int
   }
   if (single) e = 0;  // empty ranges too: their sums are stored here
   // the chunk's rows range by range; rows of no expert are left out
-  for (int64_t a = r0; e < ranges && (a < r1 || (single && g.db)); ++e) {
+  for (int64_t a = max(r0, off_at(g, 0)); e < ranges && (a < r1 || (single && g.db)); ++e) {
     const int64_t b = min(off_at(g, e + 1), r1);
     float sum[VEC] = {};
     if (live) {

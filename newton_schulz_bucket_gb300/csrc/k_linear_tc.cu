@@ -611,13 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++acc == 2) { acc = 0; aph ^= 1; }
     }
     if (!kRows && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    if (p.mode == GROUP_ROWS) {  // rows of no expert
-      const int64_t halves = p.type == DT_F32 ? 2 : 1;  // 16-bit units of an element
-      const int64_t from = halves * range_at(p, p.experts, p.rows) * p.M, to = halves * p.rows * p.M;
+    if (p.mode == GROUP_ROWS) {  // rows of no expert: before the first range and behind the last
+      const int64_t row = (p.type == DT_F32 ? 2ll : 1ll) * p.M;  // in 16-bit units
+      const int64_t head = row * range_at(p, 0, p.rows);
+      const int64_t from = max(head, row * range_at(p, p.experts, p.rows)), to = row * p.rows;
       const int64_t tid = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 64;
       const int64_t n_threads = (int64_t)gridDim.x * (32 * kEpiWarps);
+      zero_span(p.D, 0, head, tid, n_threads);
       zero_span(p.D, from, to, tid, n_threads);
-      if (p.preact) zero_span(p.preact, from, to, tid, n_threads);
+      if (p.preact) {
+        zero_span(p.preact, 0, head, tid, n_threads);
+        zero_span(p.preact, from, to, tid, n_threads);
+      }
     }
   } else if (group_sum) {  // ---- helper: zeros behind a range's end ----
     int s = 0;

@@ -265,8 +265,8 @@ def linear_backward(dy, x, w, preact=None, activation="none", dx=True, dw=True, 
 def expert_linear(x, offsets, w, bias=None, activation="none", residual=None, keep_preact=False):
     """linear over an expert tensor w [experts, in, out]: rows
     offsets[e] .. offsets[e + 1] - 1 of x (int32, on the device, as ``dispatch``
-    gives them) go through w[e] and bias[e].  Rows from offsets[-1] on come out
-    zero."""
+    gives them) go through w[e] and bias[e].  Rows before offsets[0] and from
+    offsets[-1] on come out zero."""
     return _forward(x, w, _given(offsets), bias, activation, residual, keep_preact)
 
 
