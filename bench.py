@@ -4,14 +4,16 @@
 Headline workload: the dense h=4096 transformer (32 layers x 4 shape buckets
 of 32 matrices: [4096,12288], [4096,4096], [4096,16384], [16384,4096]; bf16
 params/grads, fp32 momentum, 5 quintic Newton-Schulz steps), the largest of
-the benchmark configurations.  The line also carries a `per_config` block that
-times every configuration the same way: the fp32 64x128 case, the pages' fused
+the benchmark configurations.  The line also carries a `per_config` block (ms,
+rate and roofline fraction; `--record FILE` writes the whole record) that times
+every configuration the same way: the fp32 64x128 case, the pages' fused
 skinny batch 74 x [24, 10240] («MindSpore HyperParallel X 盘古,Muon优化器实现6倍
 性能跃升», 矩阵融合优化, Fig. 7), the MoE expert tensor with its skinny group,
 the dense model, and the 1000-matrix mixed bag at 5 and 10 steps.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--config NAME]
                     [--impl reference] [--no-per-config] [--no-cpu-baseline] [--no-e2e]
+                    [--record FILE]
 
 `value` is whole-job algorithmic throughput (GB/s of the compulsory G, M, M',
 P, P' traffic for workloads made only of memory-bound skinny groups; TFLOP/s
@@ -459,6 +461,34 @@ def roofline_of(w, dg, peaks):
     return roof
 
 
+def rounded(v):
+    """v with its floats at six significant digits."""
+    if isinstance(v, float):
+        return float(f"{v:.6g}")
+    if isinstance(v, dict):
+        return {k: rounded(x) for k, x in v.items()}
+    return [rounded(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+
+def result_line(record):
+    """The one line for stdout: the contract's fields and a row for every
+    configuration.  It stays below 2500 characters, as a reader that keeps only
+    the end of a long output would lose the head of a longer one.  `--record`
+    writes the whole record (per-group rows, each configuration's roofline, clocks
+    and oracle) to a file."""
+    keep = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "step_ms_this_rank",
+            "higher_is_better", "scaling", "vs_baseline", "dtype", "data", "config", "roofline", "cpu_baseline", "e2e",
+            "gpu_launches", "clocks")
+    line = {k: record[k] for k in keep if k in record}
+    line["roofline"] = {k: v for k, v in record["roofline"].items()
+                        if k not in ("peak_source", "flops_counted", "traffic_detail", "achieved_executed")}
+    if record.get("per_config"):
+        line["per_config"] = {f"{e['workload']} k={e['ns_steps']}":
+                              [e["ms_per_step"], e["value"], e["unit"], e["roofline"].get("frac")]
+                              for e in record["per_config"]}
+    return json.dumps(rounded(line))
+
+
 def plan_options(args):
     """Plan options from the command line: `--path` forces one kernel path
     for every group (default: the planner's choice)."""
@@ -606,6 +636,7 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-per-config", action="store_true")
+    ap.add_argument("--record", default=None, help="write the whole record to this file (JSON)")
     ap.add_argument("--path", default="auto", choices=["auto", "skinny", "tensor", "simt", "resident"],
                     help="force one kernel path for every group (profiling; default: the planner's)")
     args = ap.parse_args()
@@ -687,7 +718,10 @@ def main():
                 "cpu_baseline": cpu, "e2e": e2e,
                 "gpu_launches": launches * args.steps, "clocks": head.get("clocks"),
                 "wall_s_timed": head["wall_s_timed"], "per_config": per_config}
-        print(json.dumps(line), flush=True)
+        if args.record:
+            with open(args.record, "w", encoding="utf-8") as f:
+                json.dump(line, f, indent=1)
+        print(result_line(line), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
