@@ -93,9 +93,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case ACT_GELU_TANH: {
       const float p = sigmoid<kFast>(2.f * kSqrt2OverPi * (z + kTanhCubic * z * z * z));
-      // p (1 - p) is zero outside -16 .. 16, where z^2 may overflow
-      const float c = fminf(fmaxf(z, -16.f), 16.f);
-      return p + 2.f * c * p * (1.f - p) * kSqrt2OverPi * (1.f + 3.f * kTanhCubic * c * c);
+      // z^2 comes in last, on what is zero where it would overflow (infinity times 0
+      // would be NaN)
+      const float a = z * (p * (1.f - p));
+      return fmaf(2.f * kSqrt2OverPi, fmaf(3.f * kTanhCubic, z * (z * a), a), p);
     }
     default: return 1.f;
   }
