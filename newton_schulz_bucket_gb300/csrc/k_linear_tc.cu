@@ -28,8 +28,8 @@
 // weights through 32-column MMAs, and an expert with 257 rows costs two tiles of
 // 160 and 128 columns, not two of 256.  An accumulator lane is a feature, so a
 // warp's stores run along a token's row for any width and alignment.  Measured:
-// [4096 x 4096] x [4096, 16384] with gelu and its pre-activation 346 us back to
-// back (1590 TFLOP/s under the power cap, where cuBLAS alone sustains 1700); 64
+// [4096 x 4096] x [4096, 16384] with gelu_tanh and its pre-activation 344 us back to
+// back (1600 TFLOP/s under the power cap, where cuBLAS alone sustains 1700); 64
 // experts [7168, 2048] with 16 rows each 263 us (7.1 TB/s of weights: HBM), with
 // 256 rows 315 us (1530 TFLOP/s), with 320 rows 410 us: two tiles an expert, bound
 // by neither HBM nor the MMAs alone.
@@ -989,7 +989,9 @@ TilePlan tile_plan(const Product& p) {
       const int64_t tt = (each + tr - 1) / tr;
       const int64_t cols = ((each + tt - 1) / tt + 31) / 32 * 32;
       // a range often has more rows than the average: not where that would
-      // need another tile
+      // need another tile.  (The host knows the average only.  A range far above it
+      // reads its weights once a tile, mostly from L2: 64 experts [7168, 2048], 2048
+      // rows, 270 us spread evenly, 272 with 512 of them in one expert, 288 with 1024.)
       if (p.mode == GROUP_ROWS && tr < 256 && 2 * each > tr) continue;
       offer(0, tr, tm * tt * ranges, (double)cols, (double)kb, bytes);
     }
