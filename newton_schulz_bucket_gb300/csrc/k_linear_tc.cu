@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = p.first; ok && i < kProducts; ++i) {
           for (int k = it.k0; k < it.k1; k += BK) {
             if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 4))) break;
+            if (group_sum && it.k1 - k < BK) mbar_acquire_cluster(full(s), ph);  // both helpers' zeros
             tc_fence_after();
             const uint64_t a = da + s * (stage_bytes >> 4), b = db + s * (stage_bytes >> 4);
             if (elect_lane()) {

@@ -32,6 +32,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t a, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Acquires, at cluster scope, what was released into a phase that has completed: for
+// ordinary stores of another CTA of the cluster (the waits above acquire at CTA
+// scope, which is what copies and MMAs that count on the barrier need).
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t a, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(a), "r"(parity)
+      : "memory");
+}
 // Bounded wait: false if another role aborted or the wait ran out (then the
 // error word gets bit `code` and every role is told to stop).
 __device__ __forceinline__ bool mbar_wait(uint32_t a, uint32_t parity, volatile int* abort_flag,

@@ -29,3 +29,13 @@ def test_programmatic_kernels_wait_for_the_launch_before():
             continue
         kernels = re.split(r"\b__global__\b", code)[1:]
         assert kernels and all("grid_wait()" in k for k in kernels), os.path.basename(f)
+
+
+def test_stores_handed_to_the_other_cta_are_acquired_there():
+    """The zeros behind a range's end are ordinary stores that the other CTA's MMAs
+    read: released at cluster scope, and acquired at cluster scope before them."""
+    code = _code(os.path.join(CSRC, "k_linear_tc.cu"))
+    assert "mbar_arrive_release_cluster(map_to(full(st), 0))" in code
+    issuer = code[code.index("umma_pair(d_tmem") - 1200:code.index("umma_pair(d_tmem")]
+    assert "mbar_acquire_cluster(full(s), ph)" in issuer
+    assert "acquire.cluster" in _code(os.path.join(CSRC, "mbarrier.cuh"))
