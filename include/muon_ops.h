@@ -9,12 +9,15 @@
  *   gate              the top-k experts of each token and their softmax weights
  *   dispatch          token rows copied into expert order
  *   combine           y[t] = sum_j weight[t, j] * ys[slot[t, j]] + r[t]
- * and the gradient of each.
+ *   layer norm        y = (x - mean) / sqrt(var + eps) * w + b, row by row
+ *   balance loss      the load of a router's experts and the loss that evens it out
+ * and the gradient of each; and for serving
+ *   mx weights        matrices in microscaled 4-bit numbers, and back
+ *   mx linear         linear with such weights, one matrix or an expert tensor
  *
  * Conventions, beyond those of muon.h (statuses, muon_last_error, streams):
  *  - Stateless calls.  Every buffer is the caller's; scratch is a caller
- *    buffer whose size muon_linear_workspace / muon_dispatch_workspace gives,
- *    256-byte aligned, free for reuse once the call's work on `stream` is
+ *    buffer whose size the operator's _workspace call gives, 256-byte aligned, free for reuse once the call's work on `stream` is
  *    done.  No call allocates device memory or synchronises, so every call can
  *    be captured in a CUDA graph (the first call of each operator on a device
  *    sets kernel attributes: host work, make it before a capture).
@@ -195,6 +198,126 @@ MUON_API muon_status_t muon_combine_backward(int32_t dtype, int64_t tokens, int6
                                              const int32_t* slot, const int32_t* offsets,
                                              const float* weights, void* dys, float* dweights,
                                              void* stream);
+
+/* Layer norm of each row: with mean and var (of width, not width - 1) of row t,
+ * rstd = 1 / sqrt(var + eps),
+ *   y[t] = (x[t] - mean[t]) * rstd[t] * w + bias.
+ * x: `dtype` [rows, width] with row stride x_stride; w and bias: w_dtype (dtype or
+ * F32) [width], nullable (ones, zeros); y: `dtype` [rows, width]; mean and rstd: fp32
+ * [rows], nullable, for the way back.  Errors: INVALID_ARG (NULL x or y with rows >
+ * 0; rows not in [0, 2^30], width not in [1, 2^30]; eps negative or not finite;
+ * stride; dtypes; stream), CUDA. */
+MUON_API muon_status_t muon_layer_norm(int32_t dtype, int32_t w_dtype, int64_t rows, int64_t width,
+                                       float eps, const void* x, int64_t x_stride, const void* w,
+                                       const void* bias, void* y, float* mean, float* rstd,
+                                       void* stream);
+
+/* Scratch bytes of muon_layer_norm_backward with dw or db. */
+MUON_API muon_status_t muon_layer_norm_workspace(int64_t rows, int64_t width, size_t* bytes);
+
+/* The gradient: with xh = (x - mean) * rstd and g = dy * w,
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + residual,
+ *   dw = sum over rows of dy * xh, db = sum over rows of dy.
+ * residual (nullable): the gradient that goes past the norm, added to dx.  Those of
+ * dx (`dtype`), dw and db (w_dtype) that are not NULL are written; the workspace is
+ * not needed for dx alone.  Errors: as muon_layer_norm; also INVALID_ARG where dx, dw
+ * and db all are NULL, or the workspace is too small or not 256-byte aligned. */
+MUON_API muon_status_t muon_layer_norm_backward(int32_t dtype, int32_t w_dtype, int64_t rows,
+                                                int64_t width, const void* dy, int64_t dy_stride,
+                                                const void* x, int64_t x_stride, const float* mean,
+                                                const float* rstd, const void* w,
+                                                const void* residual, int64_t residual_stride,
+                                                void* dx, void* dw, void* db, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* Scratch bytes of muon_balance_loss. */
+MUON_API muon_status_t muon_balance_loss_workspace(int64_t tokens, int32_t experts, size_t* bytes);
+
+/* The load of a router's experts and the loss that evens it out: with p the softmax
+ * of a token's logits over all experts,
+ *   counts[e] = assignments of indices to e,   live = tokens with a logit above -inf,
+ *   loss = coef * experts * sum_e (counts[e] / sum of counts) * (sum over tokens of p[e] / live),
+ * coef for a router that is even.  A logit of -inf masks its expert, and a token of
+ * which all are masked (padding) counts nowhere; an index outside [0, experts) is
+ * no assignment; without assignments or live tokens the loss is 0.  A NaN logit makes
+ * the loss NaN.  logits and indices as muon_gate takes and gives them; loss: fp32 [1];
+ * counts: int32 [experts]; live: int32 [1].  Errors: INVALID_ARG (as muon_gate; coef
+ * not finite; tokens * top_k > 2^31 - 1; workspace), CUDA. */
+MUON_API muon_status_t muon_balance_loss(int32_t dtype, int64_t tokens, int32_t experts, int32_t top_k,
+                                         float coef, const void* logits, int64_t logits_stride,
+                                         const int32_t* indices, float* loss, int32_t* counts,
+                                         int32_t* live, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/* Its gradient, the counts held fixed: with f = counts / sum of counts,
+ *   dlogits = dloss * coef * experts / live * p * (f - <p, f>) + residual.
+ * counts and live as muon_balance_loss gave them; dloss: fp32 [1] on the device;
+ * residual (nullable): `dtype` [tokens, experts], the logits' gradient through the gate's
+ * weights.  A masked expert gets the residual alone.  dlogits: `dtype`, contiguous.
+ * Errors: as muon_balance_loss. */
+MUON_API muon_status_t muon_balance_loss_backward(int32_t dtype, int64_t tokens, int32_t experts,
+                                                  float coef, const float* dloss, const void* logits,
+                                                  int64_t logits_stride, const int32_t* counts,
+                                                  const int32_t* live, const void* residual,
+                                                  int64_t residual_stride, void* dlogits,
+                                                  void* stream);
+
+/* Microscaled 4-bit weights.  A matrix [in, out] is held by rows of its transpose:
+ * values [out][B][16 bytes] and scales [out][B bytes], B = ceil(in / 32) blocks of 32
+ * steps along in.  A scale byte s is the factor 2^(s - 127), 255 is NaN; an element is
+ * four bits, sign, two of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6; element
+ * 2 i of a block is in the low half of its byte i.  experts >= 1: that many matrices,
+ * one behind the other; 0: one.  values start on 16 bytes.
+ *
+ * muon_mx_quantize rounds w (`dtype`, stored as muon_linear takes it): a block's scale
+ * is the power of two at or below its largest magnitude, over 4 (2^-127 at least), and
+ * w / scale goes to the nearest element, ties to the even mantissa, at most 6 (so that
+ * magnitudes above 6 of their scale, up to 8, come out as 6).  A block that holds an
+ * infinity or a NaN becomes NaN.  Elements past in are 0.  Errors: INVALID_ARG (NULL
+ * pointers, sizes, strides, enums, values not on 16 bytes, stream), UNSUPPORTED (more
+ * than 2^31 - 1025 blocks in a launch), CUDA. */
+MUON_API muon_status_t muon_mx_quantize(int32_t dtype, int32_t w_layout, int32_t experts, int64_t in,
+                                        int64_t out, const void* w, int64_t w_stride,
+                                        int64_t w_expert_stride, void* values, void* scales,
+                                        void* stream);
+
+/* The numbers that values and scales stand for, rounded to `dtype`: w [experts][out][in],
+ * contiguous (layout OUT_IN of muon_linear).  Errors: as muon_mx_quantize. */
+MUON_API muon_status_t muon_mx_dequantize(int32_t dtype, int32_t experts, int64_t in, int64_t out,
+                                          const void* values, const void* scales, void* w,
+                                          void* stream);
+
+/* y = act(x' W + bias) + residual for microscaled weights, x' the rows of x rounded as
+ * muon_mx_quantize rounds (blocks along in); experts and offsets as in
+ * muon_linear_args.  The products of 4-bit numbers and their scales are exact, sums are
+ * fp32.  x, bias, residual and y are of `dtype`.  Forward only. */
+typedef struct {
+  int32_t dtype;       /* muon_dtype_t                                        */
+  int32_t activation;  /* muon_activation_t                                   */
+  int32_t experts;     /* 0: one matrix; 1 .. MUON_MAX_EXPERTS                */
+  int32_t reserved;    /* 0                                                   */
+  int64_t rows, in, out;
+  int64_t x_stride;    /* row strides in elements                             */
+  int64_t residual_stride;
+  const void* x;
+  const void* w_values;
+  const void* w_scales;
+  const void* bias;    /* nullable: [out], or [experts, out]                  */
+  const void* residual;
+  const int32_t* offsets;
+  void* y;             /* contiguous [rows, out]                              */
+  void* workspace;     /* the rounded rows                                    */
+  size_t workspace_bytes;
+} muon_mx_linear_args;
+
+/* Scratch bytes of muon_mx_linear for this many rows. */
+MUON_API muon_status_t muon_mx_linear_workspace(int64_t rows, int64_t in, size_t* bytes);
+
+/* Errors, before any launch: INVALID_ARG (NULL args, weights, x or y with rows > 0,
+ * offsets NULL with experts > 0; a size, enum or stride out of range; w_values not on
+ * 16 bytes; workspace too small or not 256-byte aligned; a stream of another device),
+ * UNSUPPORTED (a launch of more than 2^31 - 1025 tiles or blocks), CUDA. */
+MUON_API muon_status_t muon_mx_linear(const muon_mx_linear_args* args, void* stream);
 
 /* Synchronises the current device and reads the operators' error word:
  * MUON_OK, or MUON_ERR_TIMEOUT if a kernel of an earlier call gave up a bounded

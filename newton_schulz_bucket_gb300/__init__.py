@@ -13,7 +13,9 @@ from . import _capi as _c
 from ._capi import MuonError  # noqa: F401
 
 _LAYERS = ("linear", "linear_backward", "expert_linear", "expert_linear_backward", "gate", "gate_backward",
-           "dispatch", "dispatch_backward", "combine", "combine_backward", "check_ops_error")
+           "dispatch", "dispatch_backward", "combine", "combine_backward", "layer_norm", "layer_norm_backward",
+           "balance_loss", "balance_loss_backward", "mx_quantize", "mx_dequantize", "mx_linear", "mx_expert_linear",
+           "check_ops_error")
 
 __all__ = ["MuonPlan", "describe", "assign_owners", "load_library", "MuonError", "QUINTIC", *_LAYERS]
 

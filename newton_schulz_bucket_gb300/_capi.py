@@ -81,6 +81,15 @@ class muon_linear_args(C.Structure):
                 ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
 
 
+class muon_mx_linear_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("activation", C.c_int32), ("experts", C.c_int32),
+                ("reserved", C.c_int32), ("rows", C.c_int64), ("in", C.c_int64), ("out", C.c_int64),
+                ("x_stride", C.c_int64), ("residual_stride", C.c_int64), ("x", C.c_void_p),
+                ("w_values", C.c_void_p), ("w_scales", C.c_void_p), ("bias", C.c_void_p),
+                ("residual", C.c_void_p), ("offsets", C.c_void_p), ("y", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
 # test hooks declared in include/muon_testing.h
 EXPORTED_TESTING = ["muon_testing_tc_gemm", "muon_testing_skinny_max_clusters",
                     "muon_testing_tile_walk", "muon_testing_tile_walk_pair",
@@ -99,6 +108,9 @@ EXPORTED = ["muon_default_options", "muon_plan_describe", "muon_plan_create", "m
 EXPORTED_OPS = ["muon_linear_workspace", "muon_linear", "muon_linear_backward", "muon_gate",
                 "muon_gate_backward", "muon_dispatch_workspace", "muon_dispatch",
                 "muon_dispatch_backward", "muon_combine", "muon_combine_backward",
+                "muon_layer_norm", "muon_layer_norm_workspace", "muon_layer_norm_backward",
+                "muon_balance_loss_workspace", "muon_balance_loss", "muon_balance_loss_backward",
+                "muon_mx_quantize", "muon_mx_dequantize", "muon_mx_linear_workspace", "muon_mx_linear",
                 "muon_ops_check_error"]
 
 _lib = None
@@ -169,6 +181,18 @@ def load() -> C.CDLL:
     L.muon_dispatch_backward.argtypes = [i32, i64, i64, i32, vp, i64, vp, vp, vp]
     L.muon_combine.argtypes = [i32, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp]
     L.muon_combine_backward.argtypes = [i32, i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+    size = C.POINTER(C.c_size_t)
+    L.muon_layer_norm.argtypes = [i32, i32, i64, i64, f32, vp, i64, vp, vp, vp, vp, vp, vp]
+    L.muon_layer_norm_workspace.argtypes = [i64, i64, size]
+    L.muon_layer_norm_backward.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp,
+                                           C.c_size_t, vp]
+    L.muon_balance_loss_workspace.argtypes = [i64, i32, size]
+    L.muon_balance_loss.argtypes = [i32, i64, i32, i32, f32, vp, i64, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    L.muon_balance_loss_backward.argtypes = [i32, i64, i32, f32, vp, vp, i64, vp, vp, vp, i64, vp, vp]
+    L.muon_mx_quantize.argtypes = [i32, i32, i32, i64, i64, vp, i64, i64, vp, vp, vp]
+    L.muon_mx_dequantize.argtypes = [i32, i32, i64, i64, vp, vp, vp, vp]
+    L.muon_mx_linear_workspace.argtypes = [i64, i64, size]
+    L.muon_mx_linear.argtypes = [C.POINTER(muon_mx_linear_args), vp]
     L.muon_ops_check_error.argtypes = []
     for name in EXPORTED_OPS:
         getattr(L, name).restype = C.c_int

@@ -1,0 +1,622 @@
+// Layer norm of rows, y = (x - mean) rstd w + b with rstd = (var + eps)^-1/2, and its
+// gradient: with xh = (x - mean) rstd and g = dy w,
+//   dx = rstd (g - mean(g) - xh mean(g xh)) + r,   dw = sum over rows of dy xh,   db = sum of dy.
+//
+// Every tensor crosses HBM once: a row stays in the registers of its threads (16
+// elements each) between the sums over it and its result, and the next row's loads
+// are in flight meanwhile.  Rows of up to 512 elements belong to 1 to 32 lanes of a
+// warp, longer ones to a block.  The variance is the sum of squares about the mean,
+// not a difference of two large sums.  Blocks stay for many rows, so that the
+// weights are read once a block and the sums over rows (dw, db) grow in registers
+// too; each part of rows leaves one partial sum, and a second kernel adds the
+// parts in a fixed order.  No atomics: the same bits every time.
+#include "common.cuh"
+#include "ops.h"
+
+namespace muon {
+
+namespace {
+
+constexpr int kEach = 16;        // elements of a row that a thread holds
+constexpr int kSmallBlock = 128; // threads of a block whose warps hold whole rows
+constexpr int kMostThreads = 512;
+constexpr int kPartRows = 512;   // most rows a thread adds up one after another
+
+// N neighbouring elements (16 bytes of them if N > 1) in the form they are loaded in.
+template <typename T, int N>
+struct Piece {
+  static constexpr int kLoads = N == 1 ? 1 : N * (int)sizeof(T) / 16;
+  uint4 u[kLoads];
+  T one;
+  __device__ __forceinline__ void fetch(const T* p) {
+    if constexpr (N == 1) {
+      one = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ void stream(const T* p) {  // read once
+    if constexpr (N == 1) {
+      one = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+  }
+  __device__ __forceinline__ void open(float* f) const {
+    if constexpr (N == 1) {
+      f[0] = to_f32(one);
+    } else {
+      const T* h = reinterpret_cast<const T*>(u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = to_f32(h[i]);
+    }
+  }
+};
+template <typename T, int N>
+__device__ __forceinline__ void put(T* p, const float* f) {
+  if constexpr (N == 1) {
+    *p = from_f32<T>(f[0]);
+  } else {
+    alignas(16) T h[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = from_f32<T>(f[i]);
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(T) / 16; ++i)
+      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(h)[i];
+  }
+}
+
+// Sums over the threads of a row: lanes of a warp (lanes of them, a power of two),
+// or the block.  A block's sums alternate between two buffers, so that one barrier
+// each is enough.
+template <bool kWarp>
+struct RowSum {
+  float (*red)[2][32];  // [buffer][value][warp]
+  int lanes, turn;
+  __device__ __forceinline__ void operator()(float& a, float& b) {
+    if constexpr (kWarp) {
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+    } else {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+      a = warp_sum(a);
+      b = warp_sum(b);
+      if (lane == 0) { red[turn][0][warp] = a; red[turn][1][warp] = b; }
+      __syncthreads();
+      a = warp_sum(lane < warps ? red[turn][0][lane] : 0.f);
+      b = warp_sum(lane < warps ? red[turn][1][lane] : 0.f);
+      turn ^= 1;
+    }
+  }
+  __device__ __forceinline__ void operator()(float& a) {
+    if constexpr (kWarp) {
+      for (int o = lanes >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    } else {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+      a = warp_sum(a);
+      if (lane == 0) red[turn][0][warp] = a;
+      __syncthreads();
+      a = warp_sum(lane < warps ? red[turn][0][lane] : 0.f);
+      turn ^= 1;
+    }
+  }
+};
+
+// Where a thread stands: its row within the block's round, and its first column of
+// each piece (col + p * step).
+struct Place {
+  int row, rows;   // of this round, rows a round
+  int col, step;
+};
+template <bool kWarp, int N>
+__device__ __forceinline__ Place place(int lanes) {
+  if constexpr (kWarp) {
+    const int t = threadIdx.x & (lanes - 1);
+    return {(int)threadIdx.x / lanes, (int)blockDim.x / lanes, t * N, lanes * N};
+  } else {
+    return {0, 1, (int)threadIdx.x * N, (int)blockDim.x * N};
+  }
+}
+
+template <typename W, int N>
+__device__ __forceinline__ void load_weights(const void* w, int col, bool live, float fill, float* f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = fill;
+  if (w && live) {
+    Piece<W, N> v;
+    v.fetch(static_cast<const W*>(w) + col);
+    v.open(f);
+  }
+}
+
+template <typename T, typename W, int N, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm(NormArgs a, int lanes) {
+  constexpr int P = kEach / N;
+  __shared__ float red[2][2][32];
+  grid_launch_next();
+  const Place at = place<kWarp, N>(lanes);
+  RowSum<kWarp> sum{red, lanes, 0};
+  const int h = (int)a.width;
+  bool live[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) live[p] = at.col + p * at.step < h;
+  grid_wait();
+  const T* x = static_cast<const T*>(a.x) + at.col;
+  T* y = static_cast<T*>(a.y) + at.col;
+  const int64_t by = (int64_t)gridDim.x * at.rows;
+  int64_t first = (int64_t)blockIdx.x * at.rows;  // the round's first row: the same for the block
+  Piece<T, N> v[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    if (live[p] && first + at.row < a.rows) v[p].stream(x + (first + at.row) * a.x_stride + p * at.step);
+  float w[kEach], b[kEach];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
+    load_weights<W, N>(a.bias, at.col + p * at.step, live[p], 0.f, b + p * N);
+  }
+  for (; first < a.rows; first += by) {
+    const int64_t row = first + at.row;
+    float f[kEach];
+    float s = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[p * N + i] = 0.f;
+      if (live[p] && row < a.rows) v[p].open(f + p * N);
+#pragma unroll
+      for (int i = 0; i < N; ++i) s += f[p * N + i];
+      if (live[p] && row + by < a.rows) v[p].stream(x + (row + by) * a.x_stride + p * at.step);
+    }
+    sum(s);
+    const float mean = s / (float)h;
+    float q = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        f[p * N + i] -= mean;
+        if (live[p]) q = fmaf(f[p * N + i], f[p * N + i], q);
+      }
+    }
+    sum(q);
+    const float rstd = 1.f / sqrtf(q / (float)h + a.eps);
+    if (row >= a.rows) continue;  // (after the sums, which every lane takes part in)
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (!live[p]) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[p * N + i] = fmaf(f[p * N + i] * rstd, w[p * N + i], b[p * N + i]);
+      put<T, N>(y + row * h + p * at.step, f + p * N);
+    }
+    if (at.col == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+// Rows first .. last - 1 of a part; its sums go to row `part` of a.part.
+template <typename T, typename W, int N, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_backward(NormArgs a, int lanes) {
+  constexpr int P = kEach / N;
+  __shared__ float red[2][2][32];
+  extern __shared__ float fold[];  // kWarp: [warps][2][width]
+  grid_launch_next();
+  const Place at = place<kWarp, N>(lanes);
+  RowSum<kWarp> sum{red, lanes, 0};
+  const int h = (int)a.width;
+  bool live[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) live[p] = at.col + p * at.step < h;
+  grid_wait();
+  const T* x = static_cast<const T*>(a.x) + at.col;
+  const T* dy = static_cast<const T*>(a.dy) + at.col;
+  const T* res = static_cast<const T*>(a.residual) + at.col;
+  T* dx = static_cast<T*>(a.dx) + at.col;
+  float w[kEach];
+#pragma unroll
+  for (int p = 0; p < P; ++p) load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
+  const float per = 1.f / (float)h;
+  for (int64_t part = blockIdx.x; part < a.parts; part += gridDim.x) {
+    const int64_t last = min(a.rows, (part + 1) * a.part_rows);
+    int64_t first = part * a.part_rows;
+    float sw[kEach] = {}, sb[kEach] = {};
+    Piece<T, N> vx[P], vd[P];
+    float mean = 0.f, rstd = 0.f;
+    if (first + at.row < last) {
+      const int64_t row = first + at.row;
+      mean = a.mean[row];
+      rstd = a.rstd[row];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (!live[p]) continue;
+        vx[p].stream(x + row * a.x_stride + p * at.step);
+        vd[p].stream(dy + row * a.dy_stride + p * at.step);
+      }
+    }
+    for (; first < last; first += at.rows) {
+      const int64_t row = first + at.row, next = row + at.rows;
+      const bool mine = row < last;
+      float xh[kEach], d[kEach];
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) xh[p * N + i] = mean, d[p * N + i] = 0.f;
+        if (mine && live[p]) {
+          vx[p].open(xh + p * N);
+          vd[p].open(d + p * N);
+        }
+        if (next < last && live[p]) {
+          vx[p].stream(x + next * a.x_stride + p * at.step);
+          vd[p].stream(dy + next * a.dy_stride + p * at.step);
+        }
+      }
+      const float r = rstd;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        xh[i] = (xh[i] - mean) * r;
+        const float g = d[i] * w[i];
+        s1 += g;
+        s2 = fmaf(g, xh[i], s2);
+        sw[i] = fmaf(d[i], xh[i], sw[i]);
+        sb[i] += d[i];
+      }
+      if (next < last) {
+        mean = a.mean[next];
+        rstd = a.rstd[next];
+      } else {
+        mean = rstd = 0.f;
+      }
+      if (!a.dx) continue;
+      Piece<T, N> vr[P];
+      if (a.residual && mine) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if (live[p]) vr[p].stream(res + row * a.r_stride + p * at.step);
+      }
+      sum(s1, s2);
+      s1 *= per;
+      s2 *= per;
+      if (!mine) continue;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (!live[p]) continue;
+        float o[N], add[N] = {};
+        if (a.residual) vr[p].open(add);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          o[i] = fmaf(r, d[p * N + i] * w[p * N + i] - s1 - xh[p * N + i] * s2, add[i]);
+        put<T, N>(dx + row * h + p * at.step, o);
+      }
+    }
+    if (!a.part) continue;
+    float* out = a.part + part * 2 * h + at.col;
+    if constexpr (kWarp) {  // the rows of a round, then the warps
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        for (int o = lanes; o < 32; o <<= 1) {
+          sw[i] += __shfl_xor_sync(0xffffffffu, sw[i], o);
+          sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
+        }
+      }
+      __syncthreads();
+      if (lane < lanes) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (!live[p]) continue;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            fold[warp * 2 * h + at.col + p * at.step + i] = sw[p * N + i];
+            fold[warp * 2 * h + h + at.col + p * at.step + i] = sb[p * N + i];
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * h; i += blockDim.x) {
+        float s = 0.f;
+        for (int k = 0; k < warps; ++k) s += fold[k * 2 * h + i];
+        a.part[part * 2 * h + i] = s;
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (!live[p]) continue;
+        if constexpr (N == 1) {
+          out[p * at.step] = sw[p];
+          out[h + p * at.step] = sb[p];
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            *reinterpret_cast<float4*>(out + p * at.step + i) =
+                make_float4(sw[p * N + i], sw[p * N + i + 1], sw[p * N + i + 2], sw[p * N + i + 3]);
+            *reinterpret_cast<float4*>(out + h + p * at.step + i) =
+                make_float4(sb[p * N + i], sb[p * N + i + 1], sb[p * N + i + 2], sb[p * N + i + 3]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Rows that no block holds: read again for each sum (from L2).  One block a row.
+template <typename T, typename W, int N>
+__global__ void __launch_bounds__(1024) k_norm_wide(NormArgs a) {
+  __shared__ float red[2][2][32];
+  grid_launch_next();
+  grid_wait();
+  RowSum<false> sum{red, 32, 0};
+  const int64_t h = a.width, step = (int64_t)blockDim.x * N, c0 = (int64_t)threadIdx.x * N;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    float s = 0.f, q = 0.f;
+    for (int64_t c = c0; c < h; c += step) {
+      Piece<T, N> v;
+      float f[N];
+      v.fetch(x + c);
+      v.open(f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) s += f[i];
+    }
+    sum(s);
+    const float mean = s / (float)h;
+    for (int64_t c = c0; c < h; c += step) {
+      Piece<T, N> v;
+      float f[N];
+      v.fetch(x + c);
+      v.open(f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) q = fmaf(f[i] - mean, f[i] - mean, q);
+    }
+    sum(q);
+    const float rstd = 1.f / sqrtf(q / (float)h + a.eps);
+    for (int64_t c = c0; c < h; c += step) {
+      Piece<T, N> v;
+      float f[N], w[N], b[N];
+      v.fetch(x + c);
+      v.open(f);
+      load_weights<W, N>(a.w, (int)c, true, 1.f, w);
+      load_weights<W, N>(a.bias, (int)c, true, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = fmaf((f[i] - mean) * rstd, w[i], b[i]);
+      put<T, N>(static_cast<T*>(a.y) + row * h + c, f);
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+template <typename T, typename W, int N>
+__global__ void __launch_bounds__(1024) k_norm_wide_dx(NormArgs a) {
+  __shared__ float red[2][2][32];
+  grid_launch_next();
+  grid_wait();
+  RowSum<false> sum{red, 32, 0};
+  const int64_t h = a.width, step = (int64_t)blockDim.x * N, c0 = (int64_t)threadIdx.x * N;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int64_t c = c0; c < h; c += step) {
+        Piece<T, N> v;
+        float f[N], d[N], w[N], add[N] = {};
+        v.fetch(x + c);
+        v.open(f);
+        v.fetch(dy + c);
+        v.open(d);
+        load_weights<W, N>(a.w, (int)c, true, 1.f, w);
+        if (pass && a.residual) {
+          v.fetch(static_cast<const T*>(a.residual) + row * a.r_stride + c);
+          v.open(add);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float xh = (f[i] - mean) * rstd, g = d[i] * w[i];
+          if (pass) {
+            f[i] = fmaf(rstd, g - s1 - xh * s2, add[i]);
+          } else {
+            s1 += g;
+            s2 = fmaf(g, xh, s2);
+          }
+        }
+        if (pass) put<T, N>(static_cast<T*>(a.dx) + row * h + c, f);
+      }
+      if (pass) break;
+      sum(s1, s2);
+      s1 /= (float)h;
+      s2 /= (float)h;
+    }
+  }
+}
+
+// Partial sums of dw and db for the same: a thread's columns over a part's rows.
+template <typename T, int N>
+__global__ void __launch_bounds__(256) k_norm_wide_dw(NormArgs a, int col_blocks) {
+  grid_launch_next();
+  grid_wait();
+  const int64_t h = a.width, c = ((int64_t)(blockIdx.x % col_blocks) * 256 + threadIdx.x) * N;
+  const int64_t part = blockIdx.x / col_blocks;
+  if (c >= h) return;
+  float sw[N] = {}, sb[N] = {};
+  const int64_t last = min(a.rows, (part + 1) * a.part_rows);
+#pragma unroll 4
+  for (int64_t row = part * a.part_rows; row < last; ++row) {
+    Piece<T, N> vx, vd;
+    float f[N], d[N];
+    vx.fetch(static_cast<const T*>(a.x) + row * a.x_stride + c);
+    vd.fetch(static_cast<const T*>(a.dy) + row * a.dy_stride + c);
+    vx.open(f);
+    vd.open(d);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      sw[i] = fmaf(d[i], (f[i] - mean) * rstd, sw[i]);
+      sb[i] += d[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a.part[part * 2 * h + c + i] = sw[i];
+    a.part[part * 2 * h + h + c + i] = sb[i];
+  }
+}
+
+// dw and db from the parts' sums: 32 columns a block, the parts shared out over 32
+// warps and added in order, then the warps'.
+template <typename W>
+__global__ void __launch_bounds__(1024) k_norm_join(NormArgs a) {
+  __shared__ float red[32][33];
+  grid_launch_next();
+  grid_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t h = a.width, c = (int64_t)blockIdx.x * 32 + lane;  // column of [dw, db]
+  float s = 0.f;
+  if (c < 2 * h) {
+#pragma unroll 8
+    for (int64_t p = warp; p < a.parts; p += 32) s += a.part[p * 2 * h + c];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  s = warp_sum(red[lane][warp]);  // column `warp` of the block
+  const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && mine < 2 * h) {
+    if (mine < h) {
+      if (a.dw) static_cast<W*>(a.dw)[mine] = from_f32<W>(s);
+    } else if (a.db) {
+      static_cast<W*>(a.db)[mine - h] = from_f32<W>(s);
+    }
+  }
+}
+
+// How rows of this width are held.
+struct Form {
+  bool warp, wide;
+  int lanes, threads;
+};
+Form form_of(int64_t width, int n) {
+  const int64_t pieces = (width + n - 1) / n, threads = (pieces * n + kEach - 1) / kEach;
+  Form f{false, false, 32, 0};
+  if (threads <= 32) {
+    f.warp = true;
+    f.lanes = 1;
+    while (f.lanes < threads) f.lanes *= 2;
+    f.threads = kSmallBlock;
+  } else if (threads <= kMostThreads) {
+    f.threads = (int)((threads + 31) / 32 * 32);
+  } else {
+    f.wide = true;
+    f.threads = 1024;
+  }
+  return f;
+}
+
+bool aligned(const void* p, int64_t stride, int64_t size) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * size % 16 == 0;
+}
+template <typename T, typename W>
+bool vector_rows(const NormArgs& a) {
+  constexpr int64_t b = sizeof(T);
+  return a.width * b % 16 == 0 && aligned(a.x, a.rows > 1 ? a.x_stride : 0, b) && aligned(a.y, 0, b) &&
+         aligned(a.dy, a.rows > 1 ? a.dy_stride : 0, b) && aligned(a.dx, 0, b) &&
+         aligned(a.residual, a.rows > 1 ? a.r_stride : 0, b) && aligned(a.w, 0, sizeof(W)) &&
+         aligned(a.bias, 0, sizeof(W));
+}
+
+// Parts of the sum over rows: one a resident block (about 512 threads an SM), and
+// no more than kPartRows rows one after another.
+void set_parts(NormArgs* a, int n) {
+  const Form f = form_of(a->width, n);
+  int64_t each, most;
+  if (f.wide) {
+    const int64_t col_blocks = (a->width + 256ll * n - 1) / (256ll * n);
+    most = (8ll * num_sms() + col_blocks - 1) / col_blocks;
+    each = 1;
+  } else {
+    most = (int64_t)num_sms() * (512 / f.threads);
+    each = f.warp ? f.threads / f.lanes : 1;  // rows a round
+  }
+  int64_t rows = (a->rows + most - 1) / most;
+  rows = (rows + each - 1) / each * each;
+  if (rows > kPartRows * each) rows = kPartRows * each;
+  a->part_rows = rows < 1 ? 1 : rows;
+  a->parts = (a->rows + a->part_rows - 1) / a->part_rows;
+}
+
+template <typename T, typename W, int N>
+cudaError_t forward(const NormArgs& a, cudaStream_t s) {
+  const Form f = form_of(a.width, N);
+  const int64_t each = f.warp ? f.threads / f.lanes : 1;
+  const int64_t rounds = (a.rows + each - 1) / each, most = (int64_t)num_sms() * (f.wide ? 2 : 1024 / f.threads);
+  const dim3 grid((unsigned)(rounds < most ? rounds : most)), block((unsigned)f.threads);
+  if (f.wide) return launch_early(k_norm_wide<T, W, N>, grid, block, 0, s, a);
+  if (f.warp) return launch_early(k_norm<T, W, N, true>, grid, block, 0, s, a, f.lanes);
+  return launch_early(k_norm<T, W, N, false>, grid, block, 0, s, a, f.lanes);
+}
+
+template <typename T, typename W, int N>
+cudaError_t backward(NormArgs a, cudaStream_t s) {
+  set_parts(&a, N);
+  const Form f = form_of(a.width, N);
+  cudaError_t e = cudaSuccess;
+  if (f.wide) {
+    const int64_t most = (int64_t)num_sms() * 2;
+    if (a.dx)
+      e = launch_early(k_norm_wide_dx<T, W, N>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(1024), 0, s, a);
+    const int col_blocks = (int)((a.width + 256ll * N - 1) / (256ll * N));
+    if (e == cudaSuccess && a.part)
+      e = launch_early(k_norm_wide_dw<T, N>, dim3((unsigned)(col_blocks * a.parts)), dim3(256), 0, s, a, col_blocks);
+  } else {
+    const int64_t most = (int64_t)num_sms() * (512 / f.threads);
+    const dim3 grid((unsigned)(a.parts < most ? a.parts : most)), block((unsigned)f.threads);
+    const size_t smem = f.warp ? sizeof(float) * 2 * a.width * (f.threads / 32) : 0;
+    e = f.warp ? launch_early(k_norm_backward<T, W, N, true>, grid, block, smem, s, a, f.lanes)
+               : launch_early(k_norm_backward<T, W, N, false>, grid, block, smem, s, a, f.lanes);
+  }
+  if (e == cudaSuccess && a.part)
+    e = launch_early(k_norm_join<W>, dim3((unsigned)((2 * a.width + 31) / 32)), dim3(1024), 0, s, a);
+  return e;
+}
+
+template <typename T, typename W>
+cudaError_t run(const NormArgs& a, bool back, cudaStream_t s) {
+  constexpr int N = 16 / (int)sizeof(T);
+  if (vector_rows<T, W>(a)) return back ? backward<T, W, N>(a, s) : forward<T, W, N>(a, s);
+  return back ? backward<T, W, 1>(a, s) : forward<T, W, 1>(a, s);
+}
+
+cudaError_t dispatch(const NormArgs& a, bool back, cudaStream_t s) {
+  const bool wide_w = a.w_dtype == DT_F32;
+  switch (a.dtype) {
+    case DT_F16: return wide_w ? run<__half, float>(a, back, s) : run<__half, __half>(a, back, s);
+    case DT_BF16: return wide_w ? run<__nv_bfloat16, float>(a, back, s) : run<__nv_bfloat16, __nv_bfloat16>(a, back, s);
+    default: return run<float, float>(a, back, s);
+  }
+}
+
+}  // namespace
+
+int64_t norm_part_rows(int64_t rows, int64_t width) {
+  int64_t most = 0;
+  for (const int n : {1, 4, 8}) {  // (whichever the pointers' alignment will allow)
+    NormArgs a{};
+    a.rows = rows;
+    a.width = width;
+    set_parts(&a, n);
+    if (a.parts > most) most = a.parts;
+  }
+  return most;
+}
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) { return dispatch(a, false, s); }
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s) { return dispatch(a, true, s); }
+
+}  // namespace muon

@@ -1,57 +1,10 @@
 // The layer operators behind the C ABI (include/muon_ops.h): argument checks,
 // the products a call is made of, and their launches.
-#include <cstdarg>
-#include <cstdio>
-#include <mutex>
-
-#include <cuda_runtime.h>
-
-#include "../../include/muon_ops.h"
-#include "internal.h"
-#include "ops.h"
+#include "ops_checks.h"
 
 using namespace muon;
 
 namespace {
-
-muon_status_t fail(muon_status_t st, const char* fmt, ...) {
-  char buf[320];
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  set_last_error(buf);
-  return st;
-}
-
-muon_status_t cuda_status(const char* what, cudaError_t e) {
-  return e == cudaSuccess ? MUON_OK : fail(MUON_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool dtype_ok(int32_t t) { return t == DT_F32 || t == DT_F16 || t == DT_BF16; }
-int64_t dtype_size(int32_t t) { return t == DT_F32 ? 4 : 2; }
-
-constexpr int64_t kMaxDim = 1ll << 30;
-constexpr int64_t kMaxBlocks = 0x7fffffffll - 1024;  // (item counters run ahead by a grid's pairs)
-size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-
-// Launches go to the current device, so the stream has to be one of its own.
-// A capturing stream cannot be asked (the query would end the capture).
-muon_status_t check_stream(const char* what, void* stream) {
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (s == nullptr || s == cudaStreamLegacy || s == cudaStreamPerThread) return MUON_OK;
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &capturing) == cudaSuccess && capturing != cudaStreamCaptureStatusNone) return MUON_OK;
-  int dev = 0, sdev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MUON_ERR_CUDA, "%s: cudaGetDevice failed", what);
-  if (cudaStreamGetDevice(s, &sdev) != cudaSuccess) {
-    cudaGetLastError();  // not left for the next call to report
-    return fail(MUON_ERR_INVALID_ARG, "%s: stream is not a valid CUDA stream", what);
-  }
-  if (sdev != dev)
-    return fail(MUON_ERR_INVALID_ARG, "%s: stream belongs to another device than the current one", what);
-  return MUON_OK;
-}
 
 // ---- linear ----
 
@@ -282,9 +235,8 @@ muon_status_t linear_entry(const muon_linear_args* a, bool backward, void* strea
   Carve sizes{nullptr};
   st = run_linear(a, backward, sizes, false, nullptr);
   if (st != MUON_OK) return st;
-  if (sizes.used > 0 && (!a->workspace || a->workspace_bytes < sizes.used ||
-                         (reinterpret_cast<uintptr_t>(a->workspace) & 255) != 0))
-    return fail(MUON_ERR_INVALID_ARG, "%s: needs a 256-byte aligned workspace of %zu bytes", what, sizes.used);
+  st = check_workspace(what, a->workspace, a->workspace_bytes, sizes.used);
+  if (st != MUON_OK) return st;
   Carve c{static_cast<uint8_t*>(a->workspace)};
   return run_linear(a, backward, c, true, static_cast<cudaStream_t>(stream));
 }
@@ -397,9 +349,8 @@ muon_status_t muon_dispatch(int32_t dtype, int64_t tokens, int64_t hidden, int32
   if (xs && (st = check_row_stride(what, x_stride, hidden)) != MUON_OK) return st;
   if (!offsets || (tokens > 0 && (!indices || !slot || (xs && !x))))
     return fail(MUON_ERR_INVALID_ARG, "%s: NULL pointer", what);
-  const size_t need = dispatch_bytes(tokens, top_k, experts);
-  if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0))
-    return fail(MUON_ERR_INVALID_ARG, "%s: needs a 256-byte aligned workspace of %zu bytes", what, need);
+  st = check_workspace(what, workspace, workspace_bytes, dispatch_bytes(tokens, top_k, experts));
+  if (st != MUON_OK) return st;
   if ((st = check_stream(what, stream)) != MUON_OK) return st;
   SortArgs a{};
   a.dtype = dtype; a.top_k = top_k; a.experts = experts; a.index_bits = index_bits;

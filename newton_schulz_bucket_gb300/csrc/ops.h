@@ -129,4 +129,89 @@ cudaError_t launch_dispatch(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_combine_backward(const SortArgs& a, cudaStream_t s);
 
+
+// Layer norm and its gradient (w_dtype: of w, bias, dw and db).
+struct NormArgs {
+  int32_t dtype, w_dtype;
+  int64_t rows, width;
+  float eps;
+  const void* x;
+  int64_t x_stride;
+  const void* w;               // nullable: ones
+  const void* bias;            // nullable
+  void* y;                     // row pitch width
+  float* mean;                 // forward: nullable
+  float* rstd;
+  const void* dy;              // backward
+  int64_t dy_stride;
+  const void* residual;        // nullable
+  int64_t r_stride;
+  void* dx;                    // nullable, row pitch width
+  void* dw;                    // nullable
+  void* db;                    // nullable
+  float* part;                 // nullable: [parts][2][width] sums of dw and db
+  int64_t parts, part_rows;    // set by the launch
+};
+int64_t norm_part_rows(int64_t rows, int64_t width);  // most parts that launch_norm_backward uses
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s);
+
+// A router's balance loss and its gradient.
+struct BalanceArgs {
+  int32_t dtype, experts, top_k;
+  int64_t tokens, stride;
+  float coef;
+  const void* logits;
+  const int32_t* indices;
+  float* loss;
+  int32_t* counts;             // [experts]
+  int32_t* live;
+  float* part;                 // [blocks][experts] sums of probabilities, then
+  int32_t* part_counts;        // [blocks][experts + 1] assignments and tokens
+  int32_t blocks;
+  const float* dloss;          // backward
+  const void* residual;        // nullable
+  int64_t r_stride;
+  void* dlogits;
+};
+int balance_blocks(int64_t tokens, int32_t experts);
+cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs& a, cudaStream_t s);
+
+// Rows of numbers into microscaled 4-bit form and back: values [rows][blocks of 32]
+// [16 bytes], scales [rows][scale_pitch].
+struct MxRows {
+  const void* src;             // stored along the sum (rows x cols), or across it (cols x rows)
+  int64_t stride, batch_stride;
+  int64_t rows, mat_rows, cols;  // rows of all matrices, of one, steps of the sum
+  uint8_t* values;
+  uint8_t* scales;
+  int64_t scale_pitch;
+  void* dst;                   // back: [rows][cols]
+  int64_t col_blocks;          // set by the launch
+  int log_across;
+  bool vec;
+};
+enum MxOp : int32_t { MX_ALONG = 0, MX_ACROSS = 1, MX_BACK = 2 };
+int64_t mx_blocks(int64_t rows, int64_t mat_rows, int64_t cols);
+cudaError_t launch_mx_rows(int32_t dtype, MxOp op, const MxRows& q, cudaStream_t s);
+
+// y = act(x W + b) + r of microscaled operands, rows in expert order if experts > 0.
+struct MxProduct {
+  int32_t dtype, act, experts;
+  const int32_t* offsets;
+  int64_t rows, in, out;
+  const uint8_t* x_values;     // [rows][blocks][16]
+  const uint8_t* x_scales;     // [rows][x_pitch]
+  int64_t x_pitch;
+  const uint8_t* w_values;     // [experts][out][blocks][16]
+  const uint8_t* w_scales;     // [experts][out][blocks]
+  const void* bias;
+  const void* residual;
+  int64_t r_stride;
+  void* y;
+  int* err;
+};
+cudaError_t launch_mx_linear(const MxProduct& p, cudaStream_t s);
+
 }  // namespace muon

@@ -1,6 +1,7 @@
 """The layer operators next to the Muon update: a layer's product with its
-epilogue, the same over an expert tensor, the gate, and tokens into expert
-order and back, each with its gradient.
+epilogue, the same over an expert tensor, the gate, tokens into expert order and
+back, the layer norm and a router's balance loss, each with its gradient; and for
+serving, weights in microscaled 4-bit numbers and the products that read them.
 
 Like the plan's steps, these calls work on plain device tensors: no autograd
 graph is built, forward and backward are separate calls, and the gradients they
@@ -25,7 +26,9 @@ import torch
 from . import _capi as _c
 
 __all__ = ["linear", "linear_backward", "expert_linear", "expert_linear_backward", "gate", "gate_backward",
-           "dispatch", "dispatch_backward", "combine", "combine_backward", "check_ops_error", "ACTIVATIONS"]
+           "dispatch", "dispatch_backward", "combine", "combine_backward", "layer_norm", "layer_norm_backward",
+           "balance_loss", "balance_loss_backward", "mx_quantize", "mx_dequantize", "mx_linear", "mx_expert_linear",
+           "check_ops_error", "ACTIVATIONS"]
 
 ACTIVATIONS = {"none": _c.MUON_ACT_NONE, "relu": _c.MUON_ACT_RELU, "silu": _c.MUON_ACT_SILU,
                "gelu": _c.MUON_ACT_GELU, "gelu_tanh": _c.MUON_ACT_GELU_TANH}
@@ -432,6 +435,275 @@ def combine_backward(dy, ys, slot, offsets, weights):
     if st:
         _c.check(st, "muon_combine_backward")
     return dys, dwts
+
+
+# ---- layer norm ----
+
+
+@functools.lru_cache(maxsize=4096)
+def _scratch_size(call, *problem):
+    """Scratch bytes that the library's `call` gives for these sizes."""
+    n = C.c_size_t()
+    _c.check(getattr(_c.load(), call)(*problem, C.byref(n)), call)
+    return n.value
+
+
+def _norm_weight(w, what, dev, dtype, width, like=None):
+    """(address, dtype code) of a norm's weight, of x's type or float32."""
+    if w.dtype != dtype and w.dtype != _F32:
+        raise ValueError(f"{what} has dtype {w.dtype}, expected {dtype} or {_F32}")
+    return _contiguous(w, what, dev, w.dtype if like is None else like, (width,)), _DTYPES[w.dtype]
+
+
+@_operator
+def layer_norm(x, w=None, bias=None, eps=1e-5, keep_stats=False):
+    """y[t] = (x[t] - mean) / sqrt(var + eps) * w + bias over each row of x [rows,
+    width]; with keep_stats (y, mean, rstd), float32 [rows] each, for the way
+    back.
+
+    w and bias [width] are of x's type or float32, both alike; x may have any row
+    stride."""
+    dev, stream, code = _start(x, "x", 2)
+    rows, width = x.shape
+    wp = bp = None
+    w_code = code
+    if w is not None:
+        wp, w_code = _norm_weight(w, "w", dev, x.dtype, width)
+    if bias is not None:
+        bp, w_code = _norm_weight(bias, "bias", dev, x.dtype, width, None if w is None else w.dtype)
+    y = _empty((rows, width), dtype=x.dtype, device=dev)
+    mean = rstd = mp = sp = None
+    if keep_stats:
+        mean, rstd = _empty(rows, dtype=_F32, device=dev), _empty(rows, dtype=_F32, device=dev)
+        mp, sp = mean.data_ptr(), rstd.data_ptr()
+    st = _c.load().muon_layer_norm(code, w_code, rows, width, eps, x.data_ptr(), _rows(x, "x"), wp, bp, y.data_ptr(),
+                                   mp, sp, stream)
+    if st:
+        _c.check(st, "muon_layer_norm")
+    return (y, mean, rstd) if keep_stats else y
+
+
+@_operator
+def layer_norm_backward(dy, x, mean, rstd, w=None, residual=None, dx=True, dw=True, bias=False):
+    """(dx, dw, db) of layer_norm for the gradient dy of its result, with the
+    statistics that keep_stats gave; those not asked for are None.  residual, the
+    gradient that goes past the norm, is added to dx.  dw and db are of w's type
+    (x's without w)."""
+    dev, stream, code = _start(x, "x", 2)
+    rows, width = x.shape
+    dtype = x.dtype
+    _check(dy, "dy", dev, dtype, (rows, width))
+    mp, sp = _contiguous(mean, "mean", dev, _F32, (rows,)), _contiguous(rstd, "rstd", dev, _F32, (rows,))
+    wp, w_code, w_dtype = None, code, dtype
+    if w is not None:
+        wp, w_code = _norm_weight(w, "w", dev, dtype, width)
+        w_dtype = w.dtype
+    if not (dx or dw or bias):
+        raise ValueError("nothing to compute: dx, dw and bias are all False")
+    rp, r_stride = None, 0
+    if residual is not None:
+        if not dx:
+            raise ValueError("residual is added to dx, which is not asked for")
+        _check(residual, "residual", dev, dtype, (rows, width))
+        rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
+    gx = _empty((rows, width), dtype=dtype, device=dev) if dx else None
+    gw = _empty(width, dtype=w_dtype, device=dev) if dw else None
+    gb = _empty(width, dtype=w_dtype, device=dev) if bias else None
+    size = _scratch_size("muon_layer_norm_workspace", rows, width) if dw or bias else 0
+    ws = _empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = _c.load().muon_layer_norm_backward(
+        code, w_code, rows, width, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"), mp, sp, wp, rp, r_stride,
+        gx.data_ptr() if dx else None, gw.data_ptr() if dw else None, gb.data_ptr() if bias else None,
+        ws.data_ptr() if size else None, size, stream)
+    if st:
+        _c.check(st, "muon_layer_norm_backward")
+    return gx, gw, gb
+
+
+# ---- balance loss ----
+
+
+@_operator
+def balance_loss(logits, indices, coef=1.0):
+    """(loss, counts, live): coef * experts * sum over experts of the share of the
+    assignments that an expert got and its mean probability (softmax over all
+    experts), coef itself for an even router; the assignments of each expert
+    (int32 [experts]) and the tokens counted (int32 []).
+
+    logits [tokens, experts] and indices [tokens, top_k] as ``gate`` takes and gives
+    them.  A logit of -inf masks its expert; a token with none left (padding) counts
+    nowhere, an index outside [0, experts) is no assignment."""
+    dev, stream, code = _start(logits, "logits", 2)
+    tokens, experts = logits.shape
+    if indices.dim() != 2:
+        raise ValueError(f"indices must be [tokens, top_k], got {list(indices.shape)}")
+    top_k = indices.shape[1]
+    ip = _contiguous(indices, "indices", dev, _I32, (tokens, top_k))
+    size = _scratch_size("muon_balance_loss_workspace", tokens, _int32(experts))
+    ws = _empty(size, dtype=torch.uint8, device=dev)
+    loss, live = _empty((), dtype=_F32, device=dev), _empty((), dtype=_I32, device=dev)
+    counts = _empty(experts, dtype=_I32, device=dev)
+    st = _c.load().muon_balance_loss(code, tokens, experts, _int32(top_k), coef, logits.data_ptr(),
+                                     _rows(logits, "logits"), ip, loss.data_ptr(), counts.data_ptr(), live.data_ptr(),
+                                     ws.data_ptr(), size, stream)
+    if st:
+        _c.check(st, "muon_balance_loss")
+    return loss, counts, live
+
+
+@_operator
+def balance_loss_backward(dloss, logits, counts, live, coef=1.0, residual=None):
+    """The gradient of balance_loss's logits for that of its loss (float32, one
+    element on the device), the counts held fixed, plus residual (``gate_backward``'s
+    gradient of the same logits)."""
+    dev, stream, code = _start(logits, "logits", 2)
+    tokens, experts = logits.shape
+    dp = _one(dloss, "dloss", dev, _F32)
+    np_ = _one(live, "live", dev, _I32)
+    cp = _contiguous(counts, "counts", dev, _I32, (experts,))
+    rp, r_stride = None, 0
+    if residual is not None:
+        _check(residual, "residual", dev, logits.dtype, (tokens, experts))
+        rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
+    out = _empty((tokens, experts), dtype=logits.dtype, device=dev)
+    st = _c.load().muon_balance_loss_backward(code, tokens, _int32(experts), coef, dp, logits.data_ptr(),
+                                              _rows(logits, "logits"), cp, np_, rp, r_stride, out.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_balance_loss_backward")
+    return out
+
+
+def _one(t, what, dev, dtype):
+    """Address of a tensor of one element."""
+    if t.numel() != 1:
+        raise ValueError(f"{what} must have one element, got {list(t.shape)}")
+    _check(t, what, dev, dtype, t.shape)
+    return t.data_ptr()
+
+
+# ---- microscaled 4-bit weights ----
+
+_U8 = torch.uint8
+_MX_PACK = struct.Struct("=4i5q9Q").pack
+assert struct.calcsize("=4i5q9Q") == C.sizeof(_c.muon_mx_linear_args)
+
+
+@functools.lru_cache(maxsize=None)
+def _mx_call():
+    """muon_mx_linear taking the packed structure."""
+    return C.CFUNCTYPE(C.c_int, C.c_char_p, C.c_void_p)(("muon_mx_linear", _c.load()))
+
+
+@_operator
+def mx_quantize(w):
+    """(values, scales), uint8: w [in, out] or [experts, in, out] in microscaled 4-bit
+    numbers, in blocks of 32 along in.
+
+    values is [.., out, 16 * blocks], two numbers to a byte, scales [.., out, blocks],
+    with blocks = ceil(in / 32): the power of two 2^(scale - 127) at or below a block's
+    largest magnitude, over 4.  Each number of a block is rounded to the nearest of +-
+    0, 0.5, 1, 1.5, 2, 3, 4, 6 of its scale.  A block with an infinity or a NaN becomes
+    NaN.  w may be stored [.., out, in] and passed as its transposed view."""
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [in, out] or [experts, in, out], got {list(w.shape)}")
+    dev, stream, code = _start(w, "w", w.dim())
+    *lead, n_in, n_out = w.shape
+    if w.numel() == 0:
+        raise ValueError(f"w must have elements, got {list(w.shape)}")
+    layout, w_stride = _weight(w, n_in, n_out)
+    blocks = -(-n_in // 32)
+    values = _empty((*lead, n_out, 16 * blocks), dtype=_U8, device=dev)
+    scales = _empty((*lead, n_out, blocks), dtype=_U8, device=dev)
+    experts = lead[0] if lead else 0
+    st = _c.load().muon_mx_quantize(code, layout, _int32(experts), n_in, n_out, w.data_ptr(), w_stride,
+                                    w.stride(0) if experts > 1 else 0, values.data_ptr(), scales.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_mx_quantize")
+    return values, scales
+
+
+def _held(values, scales, dev, n_in=None):
+    """(addresses, experts, out) of microscaled weights of n_in steps (any, if None)."""
+    if values.dim() not in (2, 3):
+        raise ValueError(f"values must be [out, 16 * blocks] or [experts, out, 16 * blocks], got {list(values.shape)}")
+    *lead, out, width = values.shape
+    if lead and lead[0] == 0:
+        raise ValueError(f"values must have experts, got {list(values.shape)}")
+    blocks = width // 16 if n_in is None else -(-n_in // 32)
+    vp = _contiguous(values, "values", dev, _U8, (*lead, out, 16 * blocks))
+    sp = _contiguous(scales, "scales", dev, _U8, (*lead, out, blocks))
+    return vp, sp, lead[0] if lead else 0, out
+
+
+@_operator
+def mx_dequantize(values, scales, n_in, dtype=torch.bfloat16):
+    """The weights [in, out] or [experts, in, out] that mx_quantize's values and scales
+    stand for, rounded to dtype: the transposed view of a contiguous [.., out, in]."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    n_in = int(n_in)
+    if n_in < 1:
+        raise ValueError(f"n_in must be at least 1, got {n_in}")
+    dev, stream = _start_bytes(values)
+    vp, sp, experts, out = _held(values, scales, dev, n_in)
+    w = _empty((*values.shape[:-1], n_in), dtype=dtype, device=dev)
+    st = _c.load().muon_mx_dequantize(_DTYPES[dtype], _int32(experts), n_in, out, vp, sp, w.data_ptr(), stream)
+    if st:
+        _c.check(st, "muon_mx_dequantize")
+    return w.transpose(-1, -2)
+
+
+def _start_bytes(values):
+    """(device index, current stream) of packed values."""
+    dev = values.get_device()
+    if dev < 0:
+        raise ValueError("values must live on a CUDA device")
+    if dev != _current_device():
+        raise ValueError(f"values is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev, _raw_stream(dev)
+
+
+def _mx_forward(x, offsets, values, scales, bias, activation, residual):
+    dev, stream, code = _start(x, "x", 2)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    rows, n_in = x.shape
+    vp, sp, experts, out = _held(values, scales, dev, n_in)
+    if (values.dim() == 3) != (offsets is not None):
+        raise ValueError(f"values must be [{'experts, ' if offsets is not None else ''}out, 16 * blocks], got "
+                         f"{list(values.shape)}")
+    off = bp = rp = r_stride = 0
+    if offsets is not None:
+        off = _contiguous(offsets, "offsets", dev, _I32, (experts + 1,))
+    if bias is not None:
+        bp = _contiguous(bias, "bias", dev, x.dtype, (out,) if offsets is None else (experts, out))
+    if residual is not None:
+        _check(residual, "residual", dev, x.dtype, (rows, out))
+        rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
+    y = _empty((rows, out), dtype=x.dtype, device=dev)
+    size = _scratch_size("muon_mx_linear_workspace", rows, n_in)
+    ws = _empty(size, dtype=_U8, device=dev) if size else None
+    st = _mx_call()(_MX_PACK(code, act, _int32(experts), 0, rows, n_in, out, _rows(x, "x"), r_stride, x.data_ptr(), vp, sp,
+                             bp, rp, off, y.data_ptr(), ws.data_ptr() if size else 0, size), stream)
+    if st:
+        _c.check(st, "muon_mx_linear")
+    return y
+
+
+@_operator
+def mx_linear(x, values, scales, bias=None, activation="none", residual=None):
+    """act(x' @ w + bias) + residual for weights that mx_quantize packed: x' is x
+    [rows, in] rounded to microscaled 4-bit numbers in the same way, row by row.  Sums
+    are fp32; bias, residual and the result are of x's type.  Forward only."""
+    return _mx_forward(x, None, values, scales, bias, activation, residual)
+
+
+@_operator
+def mx_expert_linear(x, offsets, values, scales, bias=None, activation="none", residual=None):
+    """mx_linear over an expert tensor: rows offsets[e] .. offsets[e + 1] - 1 of x go
+    through values[e], scales[e] and bias[e]; rows of no expert come out zero."""
+    return _mx_forward(x, _given(offsets), values, scales, bias, activation, residual)
 
 
 def check_ops_error() -> None:
