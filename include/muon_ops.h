@@ -306,12 +306,13 @@ typedef struct {
   const void* residual;
   const int32_t* offsets;
   void* y;             /* contiguous [rows, out]                              */
-  void* workspace;     /* the rounded rows                                    */
+  void* workspace;     /* the rounded rows, and scales in the order of the MMAs */
   size_t workspace_bytes;
 } muon_mx_linear_args;
 
-/* Scratch bytes of muon_mx_linear for this many rows. */
-MUON_API muon_status_t muon_mx_linear_workspace(int64_t rows, int64_t in, size_t* bytes);
+/* Scratch bytes muon_mx_linear needs for these sizes (pointers are not read).  Errors:
+ * INVALID_ARG and UNSUPPORTED as the call itself. */
+MUON_API muon_status_t muon_mx_linear_workspace(const muon_mx_linear_args* args, size_t* bytes);
 
 /* Errors, before any launch: INVALID_ARG (NULL args, weights, x or y with rows > 0,
  * offsets NULL with experts > 0; a size, enum or stride out of range; w_values not on

@@ -191,7 +191,7 @@ def load() -> C.CDLL:
     L.muon_balance_loss_backward.argtypes = [i32, i64, i32, f32, vp, vp, i64, vp, vp, vp, i64, vp, vp]
     L.muon_mx_quantize.argtypes = [i32, i32, i32, i64, i64, vp, i64, i64, vp, vp, vp]
     L.muon_mx_dequantize.argtypes = [i32, i32, i64, i64, vp, vp, vp, vp]
-    L.muon_mx_linear_workspace.argtypes = [i64, i64, size]
+    L.muon_mx_linear_workspace.argtypes = [C.POINTER(muon_mx_linear_args), size]
     L.muon_mx_linear.argtypes = [C.POINTER(muon_mx_linear_args), vp]
     L.muon_ops_check_error.argtypes = []
     for name in EXPORTED_OPS:

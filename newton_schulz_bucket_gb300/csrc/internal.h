@@ -150,6 +150,7 @@ struct TcMaps {
 // swizzle, zero fill outside the extents.
 cudaError_t tc_encode_map(CUtensorMap* m, const void* base, int ns_type, int64_t inner, int64_t rows,
                           int64_t B, int64_t pitch, int64_t batch, uint32_t box0, uint32_t box1);
+cudaError_t tc_encode_words(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t B, uint32_t box1);
 cudaError_t tc_make_maps(const KArgs& a, TcMaps* t);
 cudaError_t prepare_tc(int ns_type);  // function attributes
 cudaError_t launch_tc_gram(const KArgs& a, const TcMaps& t, int src, cudaStream_t s);

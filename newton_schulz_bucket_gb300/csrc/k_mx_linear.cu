@@ -1,15 +1,17 @@
 // A layer's product of microscaled 4-bit operands on the tensor cores: y =
 // act(x W + b) + r with the weights held in 4 bits and the token rows rounded to 4
-// bits before (k_mx_quantize.cu), fp32 sums.
+// bits before, fp32 sums.
 //
 // The block-scaled MMA (tcgen05.mma kind::mxf4) multiplies 64 steps of the sum at a
 // time and takes the operands' scales from TMEM: for every 128 steps a 32-bit word a row
 // (four scales), row r in lane r % 32, column r / 32, the same in all four quarters of
-// the lanes.  Scales are held by rows in memory, [rows][steps / 32]; four warps read
-// 16 of them a lane (512 steps), scatter the words into that order in shared
-// memory, and tcgen05.cp spreads them over TMEM just before the MMAs that use them.
+// the lanes.  The launch before (k_mx_quantize.cu) has put the scales of 128 rows x 128
+// steps into blocks of 512 bytes in that order, so that they come by TMA with the
+// operands, and tcgen05.cp spreads them over TMEM just before the MMAs that use them.
 // Each stage of the ring has scale columns of its own in TMEM, so the wait for the
-// stage covers them too.
+// stage covers them too.  (Put in order here, by warps that read them from memory and
+// handed them to the leader, they cost a release and an acquire at cluster scope a
+// stage: 1800 cycles a stage of 384 of MMAs.)
 //
 // Tiles are those of k_linear_tc.cu's rows form: a CTA pair computes 256 features x up
 // to 192 tokens (two accumulators of 192 columns and 5 x 24 columns of scales fill
@@ -29,10 +31,9 @@ namespace {
 
 constexpr int kStep = 256;                    // steps of the sum in a stage: 128 bytes a row
 constexpr uint32_t kRowBytes = 128;
-constexpr uint32_t kScaleA = 1024;            // a stage's scales: two words a row, 128 rows
-constexpr int kScaleWarps = 4;
-
-// ---- block-scaled MMA ----
+constexpr uint32_t kWeights = 128 * kRowBytes;
+constexpr uint32_t kScaleBlock = 512;         // scales of 128 rows x 128 steps
+constexpr uint32_t kScaleA = 2 * kScaleBlock;
 
 // Instruction descriptor, kind::mxf4: both operands e2m1 along the sum, scales of 8
 // exponent bits; `half`: which two of a word's four scales.
@@ -57,7 +58,7 @@ __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
   }
 }
-// 32 lanes x 16 bytes of shared memory to four TMEM columns, in all four quarters.
+// A block of scales, 32 lanes x 16 bytes, to four TMEM columns in all four quarters.
 template <bool kPair>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
   if constexpr (kPair)
@@ -70,82 +71,40 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
 
-// ---- scales ----
-
-struct MxScales {
-  const uint8_t* w;
-  const uint8_t* x;
-  int64_t w_pitch, x_pitch;
-  int64_t w_matrix;            // bytes between experts' scales
-  int blocks;                  // of a row
-};
-
-// Scales at .. at + 15 of a row, zero past the row's blocks.
-__device__ __forceinline__ uint4 fetch_scales(const uint8_t* row, int at, int blocks, bool vec) {
-  if (vec && at + 16 <= blocks) return *reinterpret_cast<const uint4*>(row + at);
-  uint32_t w[4];
+// The MMAs of one stage: its scales to TMEM (weights' at ta, tokens' behind), then
+// `steps` steps of the sum (256 at most), 64 an MMA; behind the sum's end there are only
+// zeros.  NB: blocks of scales of the tile's tokens.
+template <bool kPair, int NB>
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t ta, uint64_t da, uint64_t db, uint64_t dsa, uint64_t dsb,
+                                           uint32_t first, uint32_t second, int cols, int steps, uint32_t add) {
+  constexpr uint64_t kBlock = kScaleBlock >> 4;
+  const uint32_t tb = ta + 8;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + 4 * i + k < blocks) w[i] |= (uint32_t)row[at + 4 * i + k] << (8 * k);
+  for (int c = 0; c < 2; ++c) {
+    if (c && steps <= 128) break;
+    copy_scales<kPair>(ta + 4 * c, dsa + c * kBlock);
+    copy_scales<kPair>(tb + 4 * NB * c, dsb + c * NB * kBlock);
+    if (NB == 2 && cols > 128) copy_scales<kPair>(tb + 4 * NB * c + 4, dsb + (c * NB + 1) * kBlock);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Word i of a lane's 16 scales into a stage: row group j of block `base`.
-__device__ __forceinline__ void put_word(uint8_t* base, int lane, int j, uint32_t w) {
-  *reinterpret_cast<uint32_t*>(base + lane * 16 + j * 4) = w;
-}
-
-// 16 scales of the lane's row of weights and of its token rows (one in each group of
-// 128), on their way from memory to a stage.
-template <int G>
-struct ScaleSet {
-  uint4 a, b[G];
-  int stages;                  // of this set: 1 where the sum ends in its first half, 0: no set
-  // weight row m, token rows n, n + 128 ..: absent ones (>= their ends) are zero
-  __device__ __forceinline__ void fetch(const MxScales& q, int64_t mat, int m, int m_end, int n, int n_end, int k,
-                                        int K, bool vw, bool vx) {
-    const int at = k / kMxBlock;
-    a = make_uint4(0, 0, 0, 0);
-    if (m < m_end) a = fetch_scales(q.w + mat * q.w_matrix + m * q.w_pitch, at, q.blocks, vw);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      b[g] = make_uint4(0, 0, 0, 0);
-      if (n + 128 * g < n_end) b[g] = fetch_scales(q.x + (n + 128 * g) * q.x_pitch, at, q.blocks, vx);
-    }
-    stages = K - k > kStep ? 2 : 1;
+  for (int kk = 0; kk < 4; ++kk) {
+    if (kk * 64 >= steps) break;
+    umma_mx<kPair>(d, da + kk * 2, db + kk * 2, kk & 1 ? second : first, ta + 4 * (kk >> 1), tb + 4 * NB * (kk >> 1),
+                   kk ? 1 : add);
   }
-  // Half h (256 steps) into a stage's scales.
-  __device__ __forceinline__ void put(uint8_t* sa, uint8_t* sb, int lane, int j, int h) const {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      put_word(sa + c * 512, lane, j, h ? (c ? a.w : a.z) : (c ? a.y : a.x));
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        put_word(sb + (c * G + g) * 512, lane, j, h ? (c ? b[g].w : b[g].z) : (c ? b[g].y : b[g].x));
-    }
-  }
-};
-
-__device__ __forceinline__ bool row_vec(const uint8_t* p, int64_t pitch) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && pitch % 16 == 0;
 }
 
 // ---- tiles in CTA pairs ----
 
-constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
+constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kMaxStages = 9;
-constexpr uint32_t kWeights = 128 * kRowBytes;
-constexpr uint32_t kScaleB = 2048;
-constexpr int kScaleCols = 8 + 16;             // of a stage in TMEM
+constexpr uint32_t kRing = 212992;             // 8 stages of 128 tokens
 __host__ __device__ constexpr uint32_t stage_bytes_of(int tile_rows) {
-  return kWeights + (uint32_t)(tile_rows / 2) * kRowBytes + kScaleA + kScaleB;
+  return kWeights + (uint32_t)(tile_rows / 2) * kRowBytes + kScaleA + (uint32_t)mx_token_blocks(tile_rows) * kScaleA;
 }
-constexpr uint32_t kRing = 221184;             // 8 stages of 128 tokens
+__host__ __device__ constexpr int scale_cols_of(int tile_rows) { return 8 + 8 * mx_token_blocks(tile_rows); }
 __host__ __device__ constexpr int stages_of(int tile_rows) {
-  const int smem = (int)(kRing / stage_bytes_of(tile_rows)), tmem = (512 - 2 * tile_rows) / kScaleCols;
+  const int smem = (int)(kRing / stage_bytes_of(tile_rows)), tmem = (512 - 2 * tile_rows) / scale_cols_of(tile_rows);
   const int n = smem < tmem ? smem : tmem;
   return n < kMaxStages ? n : kMaxStages;
 }
@@ -155,9 +114,15 @@ static_assert(stage_bytes_of(192) % 1024 == 0 && stage_bytes_of(128) % 1024 == 0
 constexpr uint32_t kSmem = kRing + 512 + 1024;
 static_assert((2 * kMaxStages + 5) * 8 + 8 <= 512 && kSmem <= 227 * 1024, "shared memory layout");
 
+struct ScaleMaps {
+  CUtensorMap w, x;            // [block][128 steps][512 or 1024 bytes]
+};
+
+// NB: blocks of scales of a tile's tokens (2 for tiles of more than 128).
+template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx_tiles(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ NMaps mapsX,
-               const __grid_constant__ TcProduct p, const __grid_constant__ MxScales q) {
+               const __grid_constant__ ScaleMaps scales, const __grid_constant__ TcProduct p) {
   const int S = p.stages;
   const uint32_t stage_bytes = stage_bytes_of(p.tile_rows);
   extern __shared__ uint8_t smem_raw[];
@@ -178,10 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sa_at = kWeights + (uint32_t)(p.tile_rows / 2) * kRowBytes, sb_at = sa_at + kScaleA;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1 + 2 * kScaleWarps);  // the copies of both CTAs, and their scale warps
-      mbar_init(empty(s), 1);
-    }
+    for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), 2 * kEpiWarps); }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -215,7 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int box = 0;
       while (box_rows(box) < half) ++box;
       const CUtensorMap* mapX = &mapsX.box[box];
-      const uint32_t bytes = kWeights + (uint32_t)box_rows(box) * kRowBytes;
+      const uint32_t bytes = kWeights + (uint32_t)box_rows(box) * kRowBytes + kScaleA + NB * kScaleA;
+      const int wblock = it.e * p.tiles_n + wrow / 128;  // (tiles_n: blocks of 128 features)
+      const int xblock = mx_token_slot(walk.lo, it.e, p.tile_rows) + it.tile;
       for (int k = 0; k < p.K; k += kStep) {
         if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 512))) break;
         if (elect_lane()) {
@@ -223,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_expect_tx(full(s), 2 * bytes);
           tma_load_3d_pair(sw, &mapW, bar, k / 4, wrow, it.e);
           tma_load_3d_pair(sw + kWeights, mapX, bar, k / 4, xrow, 0);
+          tma_load_3d_pair(sw + sa_at, &scales.w, bar, 0, k / 128, wblock);
+          tma_load_3d_pair(sw + sb_at, &scales.x, bar, 0, k / 128, xblock);
         }
         __syncwarp();
         if (++s == S) { s = 0; ph ^= 1; }
@@ -236,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {  // ---- MMA issuer (leader only) ----
       const uint64_t da = smem_desc(saddr(smem), 16, 1024), db = smem_desc(saddr(smem) + kWeights, 16, 1024);
       const uint64_t dsa = scale_desc(saddr(smem) + sa_at), dsb = scale_desc(saddr(smem) + sb_at);
-      const uint32_t scales = tmem_base + 2 * acc_cols;
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 1;
       bool ok = true;
@@ -246,32 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d_tmem = tmem_base + (uint32_t)acc * acc_cols;
         const int cols = mma_cols(it);
         const uint32_t first = mx_desc(BM, cols, 0), second = mx_desc(BM, cols, 1);
-        uint32_t add = 0;  // the tile's first MMA overwrites
         for (int k = 0; k < p.K; k += kStep) {
           if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 2048))) break;
-          mbar_acquire_cluster(full(s), ph);  // the other CTA's scales
           tc_fence_after();
           const uint64_t at = s * (stage_bytes >> 4);
           if (elect_lane()) {
-            const uint32_t ta = scales + (uint32_t)(s * kScaleCols), tb = ta + 8;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c && p.K - k <= 128) break;
-              copy_scales<true>(ta + 4 * c, dsa + at + c * (512 >> 4));
-              copy_scales<true>(tb + 8 * c, dsb + at + c * (1024 >> 4));
-              if (cols > 128) copy_scales<true>(tb + 8 * c + 4, dsb + at + c * (1024 >> 4) + (512 >> 4));
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk * 64 >= p.K - k) break;
-              umma_mx<true>(d_tmem, da + at + kk * 2, db + at + kk * 2, kk & 1 ? second : first, ta + 4 * (kk >> 1),
-                            tb + 8 * (kk >> 1), add);
-              add = 1;
-            }
+            stage_mmas<true, NB>(d_tmem, tmem_base + 2 * acc_cols + (uint32_t)(s * (8 + 8 * NB)), da + at, db + at,
+                                 dsa + at, dsb + at, first, second, cols, p.K - k, k ? 1 : 0);
             umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
           }
           __syncwarp();
-          add = 1;
           if (++s == S) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
@@ -286,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int keep_waiting = 0;
       mbar_wait(done, 0, &keep_waiting, p.err, 16);
     }
-  } else if (warp < 2 + kEpiWarps) {  // ---- epilogue ----
+  } else {  // ---- epilogue ----
     const int quarter = warp & 3;     // TMEM lanes this warp may read
     const int half = (warp - 2) >> 2; // the warps of a quarter take turns at 32 tokens
     int acc = 0;
@@ -321,47 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       zero_span(p.D, 0, head, tid, n_threads);
       zero_span(p.D, from, to, tid, n_threads);
     }
-  } else {  // ---- scales (both CTAs) ----
-    constexpr int kSets = 2;  // sets in flight: one is stored while the others' loads are under way
-    const int j = warp - 2 - kEpiWarps;
-    const bool vw = row_vec(q.w, q.w_pitch) && q.w_matrix % 16 == 0, vx = row_vec(q.x, q.x_pitch);
-    ScaleSet<2> set[kSets];
-    int k = 0;
-    auto fetch = [&](ScaleSet<2>& t) {  // the next 512 steps of this tile, or of the next one
-      t.stages = 0;
-      if (!more) return;
-      const int cols = mma_cols(it);
-      t.fetch(q, it.e, it.m0 + (int)rank * 128 + 32 * j + lane, p.M, it.n0 + 32 * j + lane, min(it.n0 + cols, p.rows), k,
-              p.K, vw, vx);
-      k += 2 * kStep;
-      if (k >= p.K) {
-        k = 0;
-        more = walk.next(p, it);
-      }
-    };
-    const uint32_t full_leader = map_to(full(0), 0);
-    int s = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < kSets; ++i) fetch(set[i]);
-    while (ok && set[0].stages) {
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= set[i].stages) continue;
-          if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 4096))) continue;
-          uint8_t* stage = smem + s * stage_bytes;
-          set[i].put(stage + sa_at, stage + sb_at, lane, j, h);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive_release_cluster(full_leader + 8u * s);
-          if (++s == S) { s = 0; ph ^= 1; }
-        }
-        fetch(set[i]);
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -374,14 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- few rows ----
 
-constexpr int kFewThreads = 192;  // producer, MMA issuer, four warps for the scales and then the epilogue
-constexpr uint32_t kFewRing = 110592;  // 5 stages of 128 + 16 rows; two CTAs an SM
+constexpr int kFewThreads = 192;  // producer, MMA issuer, four epilogue warps
+constexpr uint32_t kFewRing = 112640;  // 5 stages of 128 + 16 rows, 4 of 128 + 64; two CTAs an SM
 constexpr uint32_t kFewSmem = kFewRing + 256 + 1024;
 constexpr int kFewStages = 5;
-constexpr uint32_t kFewScaleB = 1024;
-constexpr int kFewScaleCols = 16;
 constexpr int kFewTmem = 256;     // 64 of sums, 16 for each stage's scales
 constexpr int kMaxShares = 8;
+static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct FewArgs {
   int rows, M, K;           // token rows, features, length of the sum
@@ -409,7 +316,7 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 
 __global__ void __launch_bounds__(kFewThreads, 2)
     k_mx_few(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
-             const __grid_constant__ FewArgs p, const __grid_constant__ MxScales q) {
+             const __grid_constant__ ScaleMaps scales, const __grid_constant__ FewArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kFewRing);  // full, empty, all
@@ -425,7 +332,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t sa_at = kWeights + (uint32_t)p.cols * kRowBytes, sb_at = sa_at + kScaleA;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) { mbar_init(full(s), 1 + kScaleWarps); mbar_init(empty(s), 1); }
+    for (int s = 0; s < p.stages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
     mbar_init(all, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,22 +352,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   grid_launch_next();
   grid_wait();
 
-  // this CTA's share of the sum, in pieces of 512 steps (a lane's 16 scales)
-  const int pieces = (p.K + 2 * kStep - 1) / (2 * kStep);  // pieces * shares stays below 2^31
-  const int k0 = pieces * rank / shares * (2 * kStep);
-  const int k1 = rank + 1 == shares ? p.K : pieces * (rank + 1) / shares * (2 * kStep);
+  const int blocks = (p.K + kStep - 1) / kStep;  // blocks * shares stays below 2^31
+  const int k0 = blocks * rank / shares * kStep;
+  const int k1 = rank + 1 == shares ? p.K : blocks * (rank + 1) / shares * kStep;
   if (warp == 0) {  // ---- TMA producer ----
     const uint32_t ring = saddr(smem);
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
     for (int k = k0; k < k1; k += kStep) {
-      if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 8192))) break;
+      if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 4096))) break;
       if (elect_lane()) {
         const uint32_t sw = ring + s * p.stage_bytes;
-        mbar_expect_tx(full(s), kWeights + (uint32_t)p.cols * kRowBytes);
+        mbar_expect_tx(full(s), p.stage_bytes);
         tma_load_3d(sw, &mapW, full(s), k / 4, m0, 0);
         tma_load_3d(sw + kWeights, &mapX, full(s), k / 4, 0, 0);
+        tma_load_3d(sw + sa_at, &scales.w, full(s), 0, k / 128, m0 / 128);
+        tma_load_3d(sw + sb_at, &scales.x, full(s), 0, k / 128, 0);
       }
       __syncwarp();
       if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -474,70 +382,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const uint64_t dsa = scale_desc(saddr(smem) + sa_at), dsb = scale_desc(saddr(smem) + sb_at);
     const uint32_t first = mx_desc(128, p.cols, 0), second = mx_desc(128, p.cols, 1);
     int s = 0;
-    uint32_t ph = 0, add = 0;
+    uint32_t ph = 0;
     for (int k = k0; k < k1; k += kStep) {
-      if (!mbar_wait(full(s), ph, abort_flag, p.err, 16384)) break;
+      if (!mbar_wait(full(s), ph, abort_flag, p.err, 8192)) break;
       tc_fence_after();
       const uint64_t at = s * (p.stage_bytes >> 4);
       if (elect_lane()) {
-        const uint32_t ta = tmem + 64 + (uint32_t)(s * kFewScaleCols), tb = ta + 8;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c && k1 - k <= 128) break;
-          copy_scales<false>(ta + 4 * c, dsa + at + c * (512 >> 4));
-          copy_scales<false>(tb + 4 * c, dsb + at + c * (512 >> 4));
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kk * 64 >= k1 - k) break;
-          umma_mx<false>(tmem, da + at + kk * 2, db + at + kk * 2, kk & 1 ? second : first, ta + 4 * (kk >> 1),
-                         tb + 4 * (kk >> 1), add);
-          add = 1;
-        }
+        stage_mmas<false, 1>(tmem, tmem + 64 + (uint32_t)(s * 16), da + at, db + at, dsa + at, dsb + at, first, second,
+                             p.cols, k1 - k, k > k0 ? 1 : 0);
         umma_commit(empty(s));
       }
       __syncwarp();
-      add = 1;
       if (++s == p.stages) { s = 0; ph ^= 1; }
     }
     if (elect_lane()) umma_commit(all);
     __syncwarp();
     volatile int keep_waiting = 0;
     mbar_wait(all, 0, &keep_waiting, p.err, 256);  // every MMA is done before the ring is reused
-  } else {  // ---- scales ----
-    constexpr int kSets = 3;
-    const int j = warp - 2;
-    const bool vw = row_vec(q.w, q.w_pitch), vx = row_vec(q.x, q.x_pitch);
-    ScaleSet<1> set[kSets];
-    int next = k0;
-    auto fetch = [&](ScaleSet<1>& t) {
-      t.stages = 0;
-      if (next >= k1) return;
-      t.fetch(q, 0, m0 + 32 * j + lane, p.M, 32 * j + lane, p.rows, next, k1, vw, vx);
-      next += 2 * kStep;
-    };
-    int s = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < kSets; ++i) fetch(set[i]);
-    while (ok && set[0].stages) {
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= set[i].stages) continue;
-          if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 32768))) continue;
-          uint8_t* stage = smem + s * p.stage_bytes;
-          set[i].put(stage + sa_at, stage + sb_at, lane, j, h);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full(s));
-          if (++s == p.stages) { s = 0; ph ^= 1; }
-        }
-        fetch(set[i]);
-      }
-    }
   }
   // every copy has landed and been read, so the ring can take the partial sums:
   // [token][128 features]
@@ -611,72 +472,95 @@ cudaError_t launch_cluster(F fn, unsigned grid, unsigned threads, size_t smem, u
 cudaError_t encode(CUtensorMap* m, const uint8_t* values, int64_t blocks, int64_t rows, int64_t mats, uint32_t box) {
   return tc_encode_map(m, values, NS_F16, blocks * 8, rows, mats, blocks * 8, rows * blocks * 8, 64, box);
 }
+// Ordered scales as 32-bit words: two times 128 steps a stage.
+cudaError_t encode_scales(ScaleMaps* m, const MxProduct& p, int64_t w_blocks, int64_t x_slots, int nb) {
+  const int64_t parts = mx_parts(p.in);
+  cudaError_t e = tc_encode_words(&m->w, p.w_scales, 128, parts, w_blocks, 2);
+  if (e == cudaSuccess) e = tc_encode_words(&m->x, p.x_scales, 128 * nb, parts, x_slots, 2);
+  return e;
+}
 
-cudaError_t run_few(const MxProduct& p, const MxScales& q, cudaStream_t s) {
+cudaError_t run_few(const MxProduct& p, cudaStream_t s) {
   static bool ready[64] = {};
   static std::mutex mu;
   cudaError_t e = prepare(k_mx_few, kFewSmem, ready, mu);
   if (e != cudaSuccess) return e;
+  const int64_t kb = mx_blocks_of(p.in);
   FewArgs a{};
-  a.rows = (int)p.rows; a.M = (int)p.out; a.K = q.blocks * kMxBlock;
+  a.rows = (int)p.rows; a.M = (int)p.out; a.K = (int)kb * kMxBlock;
   a.cols = (a.rows + 15) / 16 * 16;
-  a.stage_bytes = kWeights + (uint32_t)a.cols * kRowBytes + kScaleA + kFewScaleB;
+  a.stage_bytes = kWeights + (uint32_t)a.cols * kRowBytes + 2 * kScaleA;
   a.stages = (int)(kFewRing / a.stage_bytes);
   if (a.stages > kFewStages) a.stages = kFewStages;
   a.type = p.dtype; a.act = p.act; a.D = p.y; a.bias = p.bias; a.residual = p.residual; a.r_m = p.r_stride;
   a.err = p.err;
+  const int tiles = (a.M + 127) / 128, blocks = (a.K + kStep - 1) / kStep, places = 2 * num_sms();
   CUtensorMap mw, mx;
-  e = encode(&mw, p.w_values, q.blocks, p.out, 1, 128);
-  if (e == cudaSuccess) e = encode(&mx, p.x_values, q.blocks, p.rows, 1, (uint32_t)a.cols);
+  ScaleMaps ms;
+  e = encode(&mw, p.w_values, kb, p.out, 1, 128);
+  if (e == cudaSuccess) e = encode(&mx, p.x_values, kb, p.rows, 1, (uint32_t)a.cols);
+  if (e == cudaSuccess) e = encode_scales(&ms, p, tiles, 1, 1);
   if (e != cudaSuccess) return e;
   // shares of the sum: as many as one wave of two CTAs an SM takes, as in k_linear_few.cu
-  const int tiles = (a.M + 127) / 128, pieces = (a.K + 2 * kStep - 1) / (2 * kStep), places = 2 * num_sms();
   int shares = places / tiles < kMaxShares ? places / tiles : kMaxShares;
-  if (shares > pieces) shares = pieces;
+  if (shares > blocks) shares = blocks;
   if (shares < 1) shares = 1;
-  return launch_cluster(k_mx_few, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, a, q);
+  return launch_cluster(k_mx_few, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, ms, a);
 }
 
-cudaError_t run_tiles(const MxProduct& p, const MxScales& q, cudaStream_t s) {
+template <int NB>
+cudaError_t run_tiles(const MxProduct& p, cudaStream_t s) {
   static bool ready[64] = {};
   static std::mutex mu;
-  cudaError_t e = prepare(k_mx_tiles, kSmem, ready, mu);
+  cudaError_t e = prepare(k_mx_tiles<NB>, kSmem, ready, mu);
   if (e != cudaSuccess) return e;
+  const int64_t kb = mx_blocks_of(p.in), mats = p.experts ? p.experts : 1;
   TcProduct a{};
   a.mode = p.experts ? GROUP_ROWS : GROUP_NONE;
   a.experts = p.experts; a.offsets = p.offsets; a.splits = 1;
-  a.rows = (int)p.rows; a.K = q.blocks * kMxBlock; a.M = (int)p.out;
+  a.rows = (int)p.rows; a.K = (int)kb * kMxBlock; a.M = (int)p.out;
   a.tiles_m = (a.M + BM - 1) / BM;
+  a.tiles_n = (a.M + 127) / 128;
   a.type = p.dtype; a.act = p.act; a.D = p.y; a.bias = p.bias; a.residual = p.residual; a.r_m = p.r_stride;
   a.err = p.err;
-  const int64_t pairs = num_sms() / 2;
-  const int64_t ranges = p.experts ? (p.rows < p.experts ? p.rows : p.experts) : 1;
-  const int64_t each = (p.rows + ranges - 1) / ranges;
-  const auto items = [&](int tile) { return ranges * ((each + tile - 1) / tile) * a.tiles_m; };
-  a.tile_rows = each <= 32 ? 64 : (each <= 64 ? 128 : 192);
-  if (!p.experts) a.tile_rows = items(192) >= pairs ? 192 : (items(128) >= pairs ? 128 : 64);
+  a.tile_rows = p.tile_rows;
   a.stages = stages_of(a.tile_rows);
   CUtensorMap mw;
   NMaps mx;
-  e = encode(&mw, p.w_values, q.blocks, p.out, p.experts ? p.experts : 1, 128);
+  ScaleMaps ms;
+  e = encode(&mw, p.w_values, kb, p.out, mats, 128);
   for (int b = 0; b < kBoxes && e == cudaSuccess; ++b)
-    e = encode(&mx.box[b], p.x_values, q.blocks, p.rows, 1, (uint32_t)box_rows(b));
+    e = encode(&mx.box[b], p.x_values, kb, p.rows, 1, (uint32_t)box_rows(b));
+  if (e == cudaSuccess) e = encode_scales(&ms, p, mats * a.tiles_n, mx_token_slots(p.rows, p.experts, a.tile_rows), NB);
   if (e != cudaSuccess) return e;
+  const int64_t pairs = num_sms() / 2;
   int64_t most = (p.rows + a.tile_rows - 1) / a.tile_rows;
-  if (p.experts) most = p.rows / a.tile_rows + ranges;  // at most
+  if (p.experts) most = p.rows / a.tile_rows + (p.rows < mats ? p.rows : mats);  // at most
   most *= a.tiles_m;
   const unsigned grid = (unsigned)(2 * (most < 1 ? 1 : (most < pairs ? most : pairs)));
-  return launch_cluster(k_mx_tiles, grid, kThreads, kSmem, 2, s, mw, mx, a, q);
+  return launch_cluster(k_mx_tiles<NB>, grid, kThreads, kSmem, 2, s, mw, mx, ms, a);
 }
 
 }  // namespace
 
+// Most token rows of a tile: as many as fill the tensor cores' columns, fewer where
+// that leaves pairs without a tile.  An expert often has more rows than the average,
+// which is all the host knows: not where that would need another tile.
+int mx_tile_rows(int64_t rows, int32_t experts, int64_t out) {
+  const int64_t pairs = num_sms() / 2, features = (out + BM - 1) / BM;
+  if (experts) {
+    const int64_t ranges = rows < experts ? rows : experts, each = ranges ? (rows + ranges - 1) / ranges : 0;
+    return each <= 32 ? 64 : (each <= 64 ? 128 : 192);
+  }
+  if (rows <= 64) return 64;
+  for (int t : {192, 128})
+    if (features * ((rows + t - 1) / t) >= pairs) return t;
+  return 64;
+}
+
 cudaError_t launch_mx_linear(const MxProduct& p, cudaStream_t s) {
-  MxScales q{};
-  q.blocks = (int)((p.in + kMxBlock - 1) / kMxBlock);
-  q.w = p.w_scales; q.w_pitch = q.blocks; q.w_matrix = p.out * q.blocks;
-  q.x = p.x_scales; q.x_pitch = p.x_pitch;
-  return !p.experts && p.rows <= 64 ? run_few(p, q, s) : run_tiles(p, q, s);
+  if (!p.experts && p.rows <= 64) return run_few(p, s);
+  return mx_token_blocks(p.tile_rows) == 2 ? run_tiles<2>(p, s) : run_tiles<1>(p, s);
 }
 
 }  // namespace muon

@@ -7,6 +7,7 @@
 // columns, so that it has a block to itself, and the packed rows meet in shared
 // memory.  Bound by HBM.
 #include "common.cuh"
+#include "linear_tiles.cuh"
 #include "mx.cuh"
 #include "ops.h"
 
@@ -38,18 +39,17 @@ struct Spot {
   int64_t piece, row;
   int by;                        // rows between a thread's rows
 };
-__device__ __forceinline__ Spot spot(const MxRows& q) {
+__device__ __forceinline__ Spot spot(const MxRows& q, int64_t block) {
   const int across = 1 << q.log_across, down = kThreads >> q.log_across;
-  const int64_t cb = blockIdx.x % q.col_blocks, rb = blockIdx.x / q.col_blocks;
+  const int64_t cb = block % q.col_blocks, rb = block / q.col_blocks;
   return {cb * across + (threadIdx.x & (across - 1)), rb * down * kRows + (threadIdx.x >> q.log_across), down};
 }
 
+// Loads and rounds a thread's rows, (packed numbers, scale) of each to `give`.
 // (rows counts those of all matrices; one row after the other in the outputs)
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
-  grid_launch_next();
-  grid_wait();
-  const Spot at = spot(q);
+template <typename T, typename F>
+__device__ __forceinline__ void quantize_rows(const MxRows& q, int64_t block, F give) {
+  const Spot at = spot(q, block);
   const int64_t col = at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   const bool there = at.piece < 4 * kb;
   float f[kRows][8];
@@ -70,7 +70,99 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
     const int64_t row = at.row + k * at.by;
     if (!there || row >= q.rows) continue;
     *reinterpret_cast<uint32_t*>(q.values + (row * kb * 4 + at.piece) * 4) = v;
-    if ((at.piece & 3) == 0) q.scales[row * q.scale_pitch + at.piece / 4] = (uint8_t)s;
+    if ((at.piece & 3) == 0) give(row, at.piece / 4, s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
+  grid_launch_next();
+  grid_wait();
+  const int64_t kb = (q.cols + kMxBlock - 1) / kMxBlock;
+  quantize_rows<T>(q, blockIdx.x, [&](int64_t row, int64_t b, uint32_t s) { q.scales[row * kb + b] = (uint8_t)s; });
+}
+
+__device__ __forceinline__ int clamped(const MxPrepare& q, int e) {
+  const int v = q.offsets[e], rows = (int)q.x.rows;
+  return v < 0 ? 0 : (v > rows ? rows : v);
+}
+
+// Byte of a token row's first scale: the slot of its tile (as Walk cuts ranges into
+// tiles), its row there; -1 for a row of no range.
+__device__ __forceinline__ int64_t token_scales(const MxPrepare& q, int row, int64_t part_bytes, int64_t slot_bytes) {
+  int e = 0, lo = 0, hi = (int)q.x.rows;
+  if (q.experts) {  // the range that holds the row: the first that ends behind it
+    int end = q.experts;
+    while (e < end) {
+      const int m = (e + end) / 2;
+      if (clamped(q, m + 1) > row) end = m;
+      else e = m + 1;
+    }
+    if (e == q.experts) return -1;
+    lo = clamped(q, e);
+    hi = clamped(q, e + 1);
+    if (row < lo) return -1;
+  }
+  const int n = hi - lo, tiles = (n + q.tile_rows - 1) / q.tile_rows;
+  const int units = (n + 31) / 32, each = units / tiles, more = units - each * tiles, u = (row - lo) / 32;
+  const int tile = u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
+  const int r = row - lo - token_start(n, tiles, tile);
+  return (int64_t)(mx_token_slot(lo, e, q.tile_rows) + tile) * slot_bytes + (r >> 7) * 512 + mx_scale_byte(r, 0);
+}
+
+// What a product starts from, in one launch: the token rows, then the weights' scales
+// (of the matrices that any row reaches) through shared memory, 128 rows x 64 words.
+constexpr int kWords = 64;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
+  __shared__ uint32_t words[128][kWords + 1];
+  grid_launch_next();
+  grid_wait();
+  const int64_t kb = (q.x.cols + kMxBlock - 1) / kMxBlock, parts = (kb + 3) / 4;
+  if (blockIdx.x < q.x_blocks) {
+    const int64_t part_bytes = 512 * mx_token_blocks(q.tile_rows), slot_bytes = parts * part_bytes;
+    quantize_rows<T>(q.x, blockIdx.x, [&](int64_t row, int64_t b, uint32_t s) {
+      const int64_t at = token_scales(q, (int)row, part_bytes, slot_bytes);
+      if (at >= 0) {
+        q.x.scales[at + (b >> 2) * part_bytes + (b & 3)] = (uint8_t)s;
+        // the part's blocks behind the row's end
+        if (b + 1 == kb)
+          for (int64_t z = b + 1; z < parts * 4; ++z) q.x.scales[at + (z >> 2) * part_bytes + (z & 3)] = 0;
+      }
+    });
+    return;
+  }
+  int64_t j = blockIdx.x - q.x_blocks;
+  const int64_t run = j % q.w_parts, tiles = (q.out + 127) / 128;
+  j /= q.w_parts;
+  const int64_t mat = j / tiles, row0 = j % tiles * 128;
+  if (q.experts && clamped(q, (int)mat) >= clamped(q, (int)mat + 1)) return;
+  const uint8_t* src = q.w_scales + (mat * q.out + row0) * kb;
+  const int rows = (int)min((int64_t)128, q.out - row0);
+  const int64_t w0 = run * kWords;
+  const int n = (int)min((int64_t)kWords, parts - w0);
+  const bool vec = kb % 4 == 0 && (reinterpret_cast<uintptr_t>(q.w_scales) & 3) == 0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < 128 * kWords; i += kThreads) {
+    const int r = i / kWords, w = i % kWords;
+    uint32_t v = 0;
+    if (r < rows && w < n) {
+      const uint8_t* p = src + r * kb + (w0 + w) * 4;
+      if (vec) {
+        v = *reinterpret_cast<const uint32_t*>(p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((w0 + w) * 4 + k < kb) v |= (uint32_t)p[k] << (8 * k);
+      }
+    }
+    words[r][w] = v;
+  }
+  __syncthreads();
+  uint4* out = reinterpret_cast<uint4*>(q.w_ordered + ((mat * tiles + row0 / 128) * parts + w0) * 512);
+  for (int i = threadIdx.x; i < n * 32; i += kThreads) {
+    const int w = i >> 5, lane = i & 31;
+    out[i] = make_uint4(words[lane][w], words[32 + lane][w], words[64 + lane][w], words[96 + lane][w]);
   }
 }
 
@@ -132,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_across(MxRows q, int i
     if (o0 + col >= q.mat_rows || b0 + blk >= kb) continue;
     const int64_t row = mat * q.mat_rows + o0 + col;
     *reinterpret_cast<uint4*>(q.values + (row * kb + b0 + blk) * 16) = vals[col][blk ^ (col >> 1 & 7)];
-    q.scales[row * q.scale_pitch + b0 + blk] = scale[col][blk];
+    q.scales[row * kb + b0 + blk] = scale[col][blk];
   }
 }
 
@@ -140,7 +232,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
   grid_launch_next();
   grid_wait();
-  const Spot at = spot(q);
+  const Spot at = spot(q, blockIdx.x);
   const int64_t col = at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   if (col >= q.cols) return;
   uint32_t v[kRows], s[kRows];
@@ -149,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
     const int64_t row = at.row + k * at.by;
     if (row >= q.rows) break;
     v[k] = *reinterpret_cast<const uint32_t*>(q.values + (row * kb * 4 + at.piece) * 4);
-    s[k] = q.scales[row * q.scale_pitch + at.piece / 4];
+    s[k] = q.scales[row * kb + at.piece / 4];
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -173,27 +265,47 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
   }
 }
 
+// How blocks cover rows of pieces of eight columns; their number.
+int64_t shape_rows(MxRows* q) {
+  const int64_t pieces = 4 * mx_blocks_of(q->cols);
+  q->log_across = 2;
+  while (q->log_across < 8 && (1 << q->log_across) < pieces) ++q->log_across;
+  q->col_blocks = (pieces + (1 << q->log_across) - 1) >> q->log_across;
+  const int64_t down = (int64_t)(kThreads >> q->log_across) * kRows;
+  return (q->rows + down - 1) / down * q->col_blocks;
+}
+// 16-byte loads: every row starts on 16 bytes.
+template <typename T>
+bool vector_rows(const MxRows& q) {
+  constexpr int64_t b = sizeof(T);
+  return reinterpret_cast<uintptr_t>(q.src) % 16 == 0 && (q.mat_rows == 1 || q.stride * b % 16 == 0) &&
+         q.batch_stride * b % 16 == 0;
+}
+
 template <typename T>
 cudaError_t run(MxRows q, MxOp op, cudaStream_t s) {
-  constexpr int64_t b = sizeof(T);
   if (op == MX_ACROSS) {
     const int64_t ti = ((q.cols + kMxBlock - 1) / kMxBlock + 7) / 8, to = (q.mat_rows + 63) / 64;
-    q.vec = reinterpret_cast<uintptr_t>(q.src) % (2 * b) == 0 && q.stride % 2 == 0 && q.batch_stride % 2 == 0;
+    q.vec = reinterpret_cast<uintptr_t>(q.src) % (2 * sizeof(T)) == 0 && q.stride % 2 == 0 && q.batch_stride % 2 == 0;
     return launch_early(k_mx_quantize_across<T>, dim3((unsigned)(ti * to * (q.rows / q.mat_rows))), dim3(kThreads), 0, s,
                         q, (int)ti, (int)to);
   }
-  const int64_t pieces = 4 * ((q.cols + kMxBlock - 1) / kMxBlock);
-  q.log_across = 2;
-  while (q.log_across < 8 && (1 << q.log_across) < pieces) ++q.log_across;
-  q.col_blocks = (pieces + (1 << q.log_across) - 1) >> q.log_across;
-  const int64_t down = (int64_t)(kThreads >> q.log_across) * kRows;
-  const dim3 grid((unsigned)((q.rows + down - 1) / down * q.col_blocks));
+  const dim3 grid((unsigned)shape_rows(&q));
   if (op == MX_BACK) {
     q.vec = reinterpret_cast<uintptr_t>(q.dst) % 16 == 0 && q.cols % 8 == 0;
     return launch_early(k_mx_dequantize<T>, grid, dim3(kThreads), 0, s, q);
   }
-  q.vec = reinterpret_cast<uintptr_t>(q.src) % 16 == 0 && q.stride * b % 16 == 0 && q.batch_stride * b % 16 == 0;
+  q.vec = vector_rows<T>(q);
   return launch_early(k_mx_quantize_rows<T>, grid, dim3(kThreads), 0, s, q);
+}
+
+template <typename T>
+cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
+  q.x_blocks = shape_rows(&q.x);
+  q.x.vec = vector_rows<T>(q.x);
+  q.w_parts = (mx_parts(q.x.cols) + kWords - 1) / kWords;
+  const int64_t grid = q.x_blocks + q.w_parts * ((q.out + 127) / 128) * q.mats;
+  return launch_early(k_mx_prepare<T>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
 }
 
 }  // namespace
@@ -211,6 +323,18 @@ cudaError_t launch_mx_rows(int32_t dtype, MxOp op, const MxRows& q, cudaStream_t
     case DT_F16: return run<__half>(q, op, s);
     case DT_BF16: return run<__nv_bfloat16>(q, op, s);
     default: return run<float>(q, op, s);
+  }
+}
+
+int64_t mx_prepare_blocks(int64_t rows, int64_t in, int64_t out, int64_t mats) {
+  return mx_blocks(rows, rows, in) + (mx_parts(in) + kWords - 1) / kWords * ((out + 127) / 128) * mats;
+}
+
+cudaError_t launch_mx_prepare(int32_t dtype, const MxPrepare& q, cudaStream_t s) {
+  switch (dtype) {
+    case DT_F16: return run_prepare<__half>(q, s);
+    case DT_BF16: return run_prepare<__nv_bfloat16>(q, s);
+    default: return run_prepare<float>(q, s);
   }
 }
 

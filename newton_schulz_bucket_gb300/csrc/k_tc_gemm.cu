@@ -747,6 +747,21 @@ cudaError_t tc_encode_map(CUtensorMap* m, const void* base, int ns_type, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// 32-bit words [B][rows][inner] one behind the other, not swizzled, in boxes of box1 whole
+// rows.
+cudaError_t tc_encode_words(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t B, uint32_t box1) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)B};
+  const cuuint64_t strides[2] = {(cuuint64_t)(inner * 4), (cuuint64_t)(rows * inner * 4)};
+  const cuuint32_t box[3] = {(cuuint32_t)inner, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int32_t tc_tile_walk(int32_t op, int64_t m, int64_t n, int32_t bm, int32_t bn, int32_t* tm,
                      int32_t* tn, int32_t cap) {
   const bool sym = op == TC_GRAM || op == TC_POLY;

@@ -45,12 +45,13 @@ __device__ __forceinline__ int range_at(const TcProduct& p, int e, int hi) {
 // at most).  Sum form: output rows m0 .., columns n0 ...  Sum over k0 .. k1 - 1.
 struct Item {
   int e, m0, n0, n_end, k0, k1, split;
+  int tile;                   // rows form: the token tile within its range
 };
 
 // Token tiles of a range of n rows: as few as tile_rows allows, in steps of 32
 // rows shared out evenly (the first ones take one more).  Tile i of tiles starts
 // at token_start(i); none is empty, as tiles - 1 full ones do not hold n.
-__device__ __forceinline__ int token_start(int n, int tiles, int i) {
+__host__ __device__ __forceinline__ int token_start(int n, int tiles, int i) {
   const int units = (n + 31) / 32, each = units / tiles;
   return 32 * (i * each + min(i, units - each * tiles));
 }
@@ -121,6 +122,7 @@ struct Walk {
       raster(q, p.tiles_m, tt, tm, tn);
       it.e = e;
       it.m0 = tm * BM;
+      it.tile = tn;
       it.n0 = lo + token_start(hi - lo, tt, tn);
       it.n_end = min(hi, lo + token_start(hi - lo, tt, tn + 1));
       part_of_sum(p, split, it);

@@ -179,14 +179,13 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs& a, cudaStream_t s);
 
 // Rows of numbers into microscaled 4-bit form and back: values [rows][blocks of 32]
-// [16 bytes], scales [rows][scale_pitch].
+// [16 bytes], scales [rows][blocks], or for a product in the MMA's order (below).
 struct MxRows {
   const void* src;             // stored along the sum (rows x cols), or across it (cols x rows)
   int64_t stride, batch_stride;
   int64_t rows, mat_rows, cols;  // rows of all matrices, of one, steps of the sum
   uint8_t* values;
   uint8_t* scales;
-  int64_t scale_pitch;
   void* dst;                   // back: [rows][cols]
   int64_t col_blocks;          // set by the launch
   int log_across;
@@ -196,16 +195,48 @@ enum MxOp : int32_t { MX_ALONG = 0, MX_ACROSS = 1, MX_BACK = 2 };
 int64_t mx_blocks(int64_t rows, int64_t mat_rows, int64_t cols);
 cudaError_t launch_mx_rows(int32_t dtype, MxOp op, const MxRows& q, cudaStream_t s);
 
+// Scales in the MMA's order, for a product: a block of 512 bytes holds those of 128 rows
+// x 128 steps of the sum (a part), byte (r % 32) * 16 + r / 32 * 4 + block of 32 steps.
+// Weights: [matrix][128 features][part][512].  Token rows: a slot for every tile of the
+// product, [slot][part][1 or 2 blocks][512], row 0 of a tile at its start.  A range's
+// slots start at mx_token_slot, which leaves as many as its tiles can be.
+__host__ __device__ constexpr int mx_token_blocks(int tile_rows) { return tile_rows > 128 ? 2 : 1; }
+__host__ __device__ constexpr int mx_token_slot(int first_row, int range, int tile_rows) {
+  return first_row / tile_rows + range;
+}
+__host__ __device__ constexpr uint32_t mx_scale_byte(int r, int block) {
+  return (uint32_t)((r & 31) * 16 + (r >> 5 & 3) * 4 + (block & 3));
+}
+inline int64_t mx_blocks_of(int64_t n) { return (n + 31) / 32; }
+inline int64_t mx_parts(int64_t n) { return (n + 127) / 128; }
+inline int64_t mx_token_slots(int64_t rows, int32_t experts, int tile_rows) {
+  return rows / tile_rows + (experts ? experts : 1);
+}
+int mx_tile_rows(int64_t rows, int32_t experts, int64_t out);
+
+// What a product starts from: the token rows rounded, and both operands' scales in order.
+struct MxPrepare {
+  MxRows x;                    // scales: [slots]
+  int32_t experts;
+  const int32_t* offsets;
+  int32_t tile_rows;
+  const uint8_t* w_scales;     // [matrices][out][blocks]
+  int64_t out, mats;
+  uint8_t* w_ordered;
+  int64_t x_blocks, w_parts;   // set by the launch: blocks of the first job, runs of parts
+};
+int64_t mx_prepare_blocks(int64_t rows, int64_t in, int64_t out, int64_t mats);
+cudaError_t launch_mx_prepare(int32_t dtype, const MxPrepare& q, cudaStream_t s);
+
 // y = act(x W + b) + r of microscaled operands, rows in expert order if experts > 0.
 struct MxProduct {
-  int32_t dtype, act, experts;
+  int32_t dtype, act, experts, tile_rows;
   const int32_t* offsets;
   int64_t rows, in, out;
   const uint8_t* x_values;     // [rows][blocks][16]
-  const uint8_t* x_scales;     // [rows][x_pitch]
-  int64_t x_pitch;
-  const uint8_t* w_values;     // [experts][out][blocks][16]
-  const uint8_t* w_scales;     // [experts][out][blocks]
+  const uint8_t* x_scales;     // in order
+  const uint8_t* w_values;     // [matrices][out][blocks][16]
+  const uint8_t* w_scales;     // in order
   const void* bias;
   const void* residual;
   int64_t r_stride;

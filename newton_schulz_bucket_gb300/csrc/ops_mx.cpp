@@ -28,16 +28,20 @@ muon_status_t check_blocks(const char* what, int64_t rows, int64_t mat_rows, int
   return MUON_OK;
 }
 
-// The rounded token rows in the workspace.
+// The rounded token rows and both operands' ordered scales in the workspace.
 struct Scratch {
-  size_t values, total;
-  int64_t pitch;               // of a row's scales: whole 16 bytes
+  size_t x_scales, w_scales, total;
+  int tile_rows;
 };
-Scratch scratch_of(int64_t rows, int64_t in) {
+Scratch scratch_of(const muon_mx_linear_args* a) {
   Scratch c{};
-  c.pitch = (blocks_of(in) + 15) / 16 * 16;
-  c.values = align256((size_t)(rows * blocks_of(in) * 16));
-  c.total = c.values + align256((size_t)(rows * c.pitch));
+  const int64_t parts = mx_parts(a->in), mats = a->experts ? a->experts : 1;
+  c.tile_rows = mx_tile_rows(a->rows, a->experts, a->out);
+  if (a->rows == 0) return c;
+  c.x_scales = align256((size_t)(a->rows * blocks_of(a->in) * 16));
+  c.w_scales = c.x_scales + align256((size_t)(mx_token_slots(a->rows, a->experts, c.tile_rows) * parts * 512 *
+                                              mx_token_blocks(c.tile_rows)));
+  c.total = c.w_scales + align256((size_t)(mats * ((a->out + 127) / 128) * parts * 512));
   return c;
 }
 
@@ -55,7 +59,9 @@ muon_status_t check_product(const char* what, const muon_mx_linear_args* a) {
   const int64_t mats = a->experts ? a->experts : 1;
   if ((a->rows / 64 + mats) * ((a->out + 255) / 256) > kMaxBlocks)
     return fail(MUON_ERR_UNSUPPORTED, "%s: too many tiles for one launch", what);
-  return check_blocks(what, a->rows, a->rows, a->in);
+  if (mx_prepare_blocks(a->rows, a->in, a->out, mats) > kMaxBlocks)
+    return fail(MUON_ERR_UNSUPPORTED, "%s: too many blocks for one launch", what);
+  return MUON_OK;
 }
 
 }  // namespace
@@ -86,7 +92,6 @@ muon_status_t muon_mx_quantize(int32_t dtype, int32_t w_layout, int32_t experts,
   q.cols = in;
   q.values = static_cast<uint8_t*>(values);
   q.scales = static_cast<uint8_t*>(scales);
-  q.scale_pitch = blocks_of(in);
   st = check_held(what, values, scales);
   if (st == MUON_OK) st = check_blocks(what, q.rows, q.mat_rows, in);
   if (st == MUON_OK) st = check_stream(what, stream);
@@ -108,7 +113,6 @@ muon_status_t muon_mx_dequantize(int32_t dtype, int32_t experts, int64_t in, int
   q.cols = in;
   q.values = static_cast<uint8_t*>(const_cast<void*>(values));
   q.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
-  q.scale_pitch = blocks_of(in);
   q.dst = w;
   st = check_blocks(what, q.rows, q.rows, in);
   if (st == MUON_OK) st = check_stream(what, stream);
@@ -116,13 +120,12 @@ muon_status_t muon_mx_dequantize(int32_t dtype, int32_t experts, int64_t in, int
   return cuda_status(what, launch_mx_rows(dtype, MX_BACK, q, static_cast<cudaStream_t>(stream)));
 }
 
-muon_status_t muon_mx_linear_workspace(int64_t rows, int64_t in, size_t* bytes) {
+muon_status_t muon_mx_linear_workspace(const muon_mx_linear_args* args, size_t* bytes) {
   const char* what = "muon_mx_linear_workspace";
   if (!bytes) return fail(MUON_ERR_INVALID_ARG, "%s: bytes is NULL", what);
-  if (rows < 0 || rows > kMaxDim || in < 1 || in > kMaxDim)
-    return fail(MUON_ERR_INVALID_ARG, "%s: rows must be in [0, 2^30], in in [1, 2^30]", what);
-  *bytes = scratch_of(rows, in).total;
-  return MUON_OK;
+  const muon_status_t st = check_product(what, args);
+  if (st == MUON_OK) *bytes = scratch_of(args).total;
+  return st;
 }
 
 muon_status_t muon_mx_linear(const muon_mx_linear_args* args, void* stream) {
@@ -134,29 +137,33 @@ muon_status_t muon_mx_linear(const muon_mx_linear_args* args, void* stream) {
   if (st != MUON_OK) return st;
   if (a.experts > 0 && !a.offsets) return fail(MUON_ERR_INVALID_ARG, "%s: offsets is NULL with experts > 0", what);
   if (a.rows > 0 && (!a.x || !a.y)) return fail(MUON_ERR_INVALID_ARG, "%s: NULL pointer", what);
-  const Scratch c = scratch_of(a.rows, a.in);
+  const Scratch c = scratch_of(args);
   st = check_workspace(what, a.workspace, a.workspace_bytes, c.total);
   if (st == MUON_OK) st = check_stream(what, stream);
   if (st != MUON_OK || a.rows == 0) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  MxRows q{};
-  q.src = a.x;
-  q.stride = a.x_stride;
-  q.rows = q.mat_rows = a.rows;
-  q.cols = a.in;
-  q.values = ws;
-  q.scales = ws + c.values;
-  q.scale_pitch = c.pitch;
+  MxPrepare q{};
+  q.x.src = a.x;
+  q.x.stride = a.x_stride;
+  q.x.rows = q.x.mat_rows = a.rows;
+  q.x.cols = a.in;
+  q.x.values = ws;
+  q.x.scales = ws + c.x_scales;
+  q.experts = a.experts; q.offsets = a.offsets; q.tile_rows = c.tile_rows;
+  q.w_scales = static_cast<const uint8_t*>(a.w_scales);
+  q.w_ordered = ws + c.w_scales;
+  q.out = a.out;
+  q.mats = a.experts ? a.experts : 1;
   MxProduct p{};
-  p.dtype = a.dtype; p.act = a.activation; p.experts = a.experts; p.offsets = a.offsets;
+  p.dtype = a.dtype; p.act = a.activation; p.experts = a.experts; p.offsets = a.offsets; p.tile_rows = c.tile_rows;
   p.rows = a.rows; p.in = a.in; p.out = a.out;
-  p.x_values = q.values; p.x_scales = q.scales; p.x_pitch = c.pitch;
+  p.x_values = q.x.values; p.x_scales = q.x.scales;
   p.w_values = static_cast<const uint8_t*>(a.w_values);
-  p.w_scales = static_cast<const uint8_t*>(a.w_scales);
+  p.w_scales = q.w_ordered;
   p.bias = a.bias; p.residual = a.residual; p.r_stride = a.residual ? a.residual_stride : 0; p.y = a.y;
   cudaError_t e = ops_error_word(&p.err);
-  if (e == cudaSuccess) e = launch_mx_rows(a.dtype, MX_ALONG, q, s);
+  if (e == cudaSuccess) e = launch_mx_prepare(a.dtype, q, s);
   if (e == cudaSuccess) e = launch_mx_linear(p, s);
   return cuda_status(what, e);
 }

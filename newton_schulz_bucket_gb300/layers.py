@@ -594,6 +594,15 @@ def _mx_call():
     return C.CFUNCTYPE(C.c_int, C.c_char_p, C.c_void_p)(("muon_mx_linear", _c.load()))
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx_scratch_size(code, experts, rows, n_in, out):
+    n = C.c_size_t()
+    a = _c.muon_mx_linear_args.from_buffer_copy(
+        _MX_PACK(code, 0, _int32(experts), 0, rows, n_in, out, n_in, 0, *(0,) * 9))
+    _c.check(_c.load().muon_mx_linear_workspace(C.byref(a), C.byref(n)), "muon_mx_linear_workspace")
+    return n.value
+
+
 @_operator
 def mx_quantize(w):
     """(values, scales), uint8: w [in, out] or [experts, in, out] in microscaled 4-bit
@@ -682,7 +691,7 @@ def _mx_forward(x, offsets, values, scales, bias, activation, residual):
         _check(residual, "residual", dev, x.dtype, (rows, out))
         rp, r_stride = residual.data_ptr(), _rows(residual, "residual")
     y = _empty((rows, out), dtype=x.dtype, device=dev)
-    size = _scratch_size("muon_mx_linear_workspace", rows, n_in)
+    size = _mx_scratch_size(code, experts, rows, n_in, out)
     ws = _empty(size, dtype=_U8, device=dev) if size else None
     st = _mx_call()(_MX_PACK(code, act, _int32(experts), 0, rows, n_in, out, _rows(x, "x"), r_stride, x.data_ptr(), vp, sp,
                              bp, rp, off, y.data_ptr(), ws.data_ptr() if size else 0, size), stream)
