@@ -41,7 +41,9 @@ __device__ __forceinline__ bool aligned16(const void* p) {
 // block, so that completion carries over from launch to launch.  Non-coherent
 // loads (__ldg, ld.global.nc, const __restrict__) are not for these kernels: they
 // are defined for memory that nobody writes while the kernel is resident, and the
-// launch before may still be writing then.
+// launch before may still be writing then.  (A kernel that lets the next one start only
+// after its own grid_wait, as k_mx_prepare does, vouches for all that came before
+// itself: that much the next one may read before it waits.)
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>

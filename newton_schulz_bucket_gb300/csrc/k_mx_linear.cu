@@ -8,15 +8,15 @@
 // the lanes.  The launch before (k_mx_quantize.cu) has put the scales of 128 rows x 128
 // steps into blocks of 512 bytes in that order, so that they come by TMA with the
 // operands, and tcgen05.cp spreads them over TMEM just before the MMAs that use them.
-// Each stage of the ring has scale columns of its own in TMEM, so the wait for the
-// stage covers them too.  (Put in order here, by warps that read them from memory and
+// Sets of scale columns are used in turn, each once the MMAs that read it are done.  (Put in order here, by warps that read them from memory and
 // handed them to the leader, they cost a release and an acquire at cluster scope a
 // stage: 1800 cycles a stage of 384 of MMAs.)
 //
 // Tiles are those of k_linear_tc.cu's rows form: a CTA pair computes 256 features x up
 // to 192 tokens (two accumulators of 192 columns and 5 x 24 columns of scales fill
 // TMEM), each CTA stages its 128 rows of weights and its half of the tokens, 256 steps a
-// stage.  Up to 64 rows of one matrix take the form of k_linear_few.cu: 128 features a
+// stage.  The bytes in flight set the pace: about 3900 cycles pass from a stage's release to
+// its next use, so that 5 stages gave 790 cycles each.  Up to 64 rows of one matrix take the form of k_linear_few.cu: 128 features a
 // cluster of up to eight CTAs that share the sum.
 #include <cuda.h>
 
@@ -66,53 +66,61 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
   else
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+// Arrives on the leader's barrier alone when what this thread issued has completed.
+__device__ __forceinline__ void commit_leader(uint32_t mbar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
+}
 // Descriptor of such a block: no swizzle, groups of eight 16-byte rows 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
 
-// The MMAs of one stage: its scales to TMEM (weights' at ta, tokens' behind), then
-// `steps` steps of the sum (256 at most), 64 an MMA; behind the sum's end there are only
-// zeros.  NB: blocks of scales of the tile's tokens.
+// A stage's scales to TMEM, the weights' at ta and the tokens' behind, for `steps` steps of
+// the sum (256 at most).  NB: blocks of scales of the tile's tokens.
 template <bool kPair, int NB>
-__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t ta, uint64_t da, uint64_t db, uint64_t dsa, uint64_t dsb,
-                                           uint32_t first, uint32_t second, int cols, int steps, uint32_t add) {
+__device__ __forceinline__ void stage_scales(uint32_t ta, uint64_t dsa, uint64_t dsb, int steps) {
   constexpr uint64_t kBlock = kScaleBlock >> 4;
   const uint32_t tb = ta + 8;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if (c && steps <= 128) break;
-    copy_scales<kPair>(ta + 4 * c, dsa + c * kBlock);
-    copy_scales<kPair>(tb + 4 * NB * c, dsb + c * NB * kBlock);
-    if (NB == 2 && cols > 128) copy_scales<kPair>(tb + 4 * NB * c + 4, dsb + (c * NB + 1) * kBlock);
+  copy_scales<kPair>(ta, dsa);
+  copy_scales<kPair>(tb, dsb);
+  if (NB == 2) copy_scales<kPair>(tb + 4, dsb + kBlock);
+  if (steps > 128) {
+    copy_scales<kPair>(ta + 4, dsa + kBlock);
+    copy_scales<kPair>(tb + 4 * NB, dsb + NB * kBlock);
+    if (NB == 2) copy_scales<kPair>(tb + 12, dsb + 3 * kBlock);
   }
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    if (kk * 64 >= steps) break;
-    umma_mx<kPair>(d, da + kk * 2, db + kk * 2, kk & 1 ? second : first, ta + 4 * (kk >> 1), tb + 4 * NB * (kk >> 1),
-                   kk ? 1 : add);
+}
+// Its MMAs, 64 steps each; behind the sum's end there are only zeros.
+template <bool kPair, int NB>
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t ta, uint64_t da, uint64_t db, uint32_t first,
+                                           uint32_t second, int steps, uint32_t add) {
+  const uint32_t tb = ta + 8;
+  umma_mx<kPair>(d, da, db, first, ta, tb, add);
+  if (steps > 192) {
+    umma_mx<kPair>(d, da + 2, db + 2, second, ta, tb, 1);
+    umma_mx<kPair>(d, da + 4, db + 4, first, ta + 4, tb + 4 * NB, 1);
+    umma_mx<kPair>(d, da + 6, db + 6, second, ta + 4, tb + 4 * NB, 1);
+  } else {
+    if (steps > 64) umma_mx<kPair>(d, da + 2, db + 2, second, ta, tb, 1);
+    if (steps > 128) umma_mx<kPair>(d, da + 4, db + 4, first, ta + 4, tb + 4 * NB, 1);
   }
 }
 
 // ---- tiles in CTA pairs ----
 
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (4 + kEpiWarps);  // producer, MMA issuer, epilogue, two that copy scales
 constexpr int kMaxStages = 9;
-constexpr uint32_t kRing = 212992;             // 8 stages of 128 tokens
+constexpr uint32_t kRing = 222208;             // 7 stages of 192 tokens, 8 of 128, 9 of 64
 __host__ __device__ constexpr uint32_t stage_bytes_of(int tile_rows) {
   return kWeights + (uint32_t)(tile_rows / 2) * kRowBytes + kScaleA + (uint32_t)mx_token_blocks(tile_rows) * kScaleA;
 }
-__host__ __device__ constexpr int scale_cols_of(int tile_rows) { return 8 + 8 * mx_token_blocks(tile_rows); }
-__host__ __device__ constexpr int stages_of(int tile_rows) {
-  const int smem = (int)(kRing / stage_bytes_of(tile_rows)), tmem = (512 - 2 * tile_rows) / scale_cols_of(tile_rows);
-  const int n = smem < tmem ? smem : tmem;
-  return n < kMaxStages ? n : kMaxStages;
-}
-static_assert(stages_of(192) == 5 && stages_of(128) == 8 && stages_of(64) == kMaxStages, "ring depths");
+__host__ __device__ constexpr int stages_of(int tile_rows) { return (int)(kRing / stage_bytes_of(tile_rows)); }
+static_assert(stages_of(192) == 7 && stages_of(128) == 8 && stages_of(64) == kMaxStages, "ring depths");
+static_assert(2 * 192 + 5 * 24 <= 512 && 2 * 128 + kMaxStages * 16 <= 512, "accumulators and scales in TMEM");
 static_assert(stage_bytes_of(192) % 1024 == 0 && stage_bytes_of(128) % 1024 == 0 && stage_bytes_of(64) % 1024 == 0,
               "stages start where the swizzle does");
 constexpr uint32_t kSmem = kRing + 512 + 1024;
-static_assert((2 * kMaxStages + 5) * 8 + 8 <= 512 && kSmem <= 227 * 1024, "shared memory layout");
+static_assert((3 * kMaxStages + 5) * 8 + 8 <= 512 && kSmem <= 227 * 1024, "shared memory layout");
 
 struct ScaleMaps {
   CUtensorMap w, x;            // [block][128 steps][512 or 1024 bytes]
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -138,12 +146,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
   auto tempty = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
   const uint32_t done = bar0 + 8u * (2 * kMaxStages + 4);
+  auto ready = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 5 + s); };
   const uint32_t acc_cols = (uint32_t)p.tile_rows;
+  constexpr int kScaleCols = 8 + 8 * NB, kSets = NB == 2 ? 5 : kMaxStages;  // sets of scale columns
   // the scales' place in a stage
   const uint32_t sa_at = kWeights + (uint32_t)(p.tile_rows / 2) * kRowBytes, sb_at = sa_at + kScaleA;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(full(s), 1); mbar_init(ready(s), 1); mbar_init(empty(s), 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(tfull(a), 1); mbar_init(tempty(a), 2 * kEpiWarps); }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -161,36 +171,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   grid_launch_next();
-  grid_wait();  // all that runs before this launch is done: its results may be read, its inputs overwritten
+  // The launch before (k_mx_prepare) lets this one start only once all that ran before
+  // it is done, so that offsets and weights may be read here; what it writes itself, and
+  // what y takes the place of, waits.
   Walk<0> walk(p);
   Item it;
   bool more = walk.next(p, it);
+  if (warp != 0) grid_wait();
 
   if (warp == 0) {  // ---- TMA producer (both CTAs) ----
     const uint32_t ring = saddr(smem), full_leader = map_to(full(0), 0);
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
+    const int ahead = min(S, (p.K + kStep - 1) / kStep);  // stages of the first tile whose weights come early
+    if (more && elect_lane()) {
+      for (int i = 0; i < ahead; ++i)
+        tma_load_3d_pair(ring + i * stage_bytes, &mapW, full_leader + 8u * i, i * (kStep / 4), it.m0 + (int)rank * 128,
+                         it.e);
+    }
+    __syncwarp();
+    grid_wait();
+    int early = ahead;
     for (; ok && more; more = walk.next(p, it)) {
-      const int wrow = it.m0 + (int)rank * 128;
+      const int wrow = it.m0 + (int)rank * 128, e = it.e;
       const int half = mma_cols(it) / 2, xrow = it.n0 + (int)rank * half;
       int box = 0;
       while (box_rows(box) < half) ++box;
       const CUtensorMap* mapX = &mapsX.box[box];
       const uint32_t bytes = kWeights + (uint32_t)box_rows(box) * kRowBytes + kScaleA + NB * kScaleA;
-      const int wblock = it.e * p.tiles_n + wrow / 128;  // (tiles_n: blocks of 128 features)
+      const int wblock = e * p.tiles_n + wrow / 128;  // (tiles_n: blocks of 128 features)
       const int xblock = mx_token_slot(walk.lo, it.e, p.tile_rows) + it.tile;
       for (int k = 0; k < p.K; k += kStep) {
         if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 512))) break;
         if (elect_lane()) {
           const uint32_t sw = ring + s * stage_bytes, bar = full_leader + 8u * s;
           if (rank == 0) mbar_expect_tx(full(s), 2 * bytes);
-          tma_load_3d_pair(sw, &mapW, bar, k / 4, wrow, it.e);
+          if (early == 0) tma_load_3d_pair(sw, &mapW, bar, k / 4, wrow, e);
           tma_load_3d_pair(sw + kWeights, mapX, bar, k / 4, xrow, 0);
           tma_load_3d_pair(sw + sa_at, &scales.w, bar, 0, k / 128, wblock);
           tma_load_3d_pair(sw + sb_at, &scales.x, bar, 0, k / 128, xblock);
         }
         __syncwarp();
+        if (early) --early;
         if (++s == S) { s = 0; ph ^= 1; }
       }
     }
@@ -201,27 +224,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {  // ---- MMA issuer (leader only) ----
       const uint64_t da = smem_desc(saddr(smem), 16, 1024), db = smem_desc(saddr(smem) + kWeights, 16, 1024);
-      const uint64_t dsa = scale_desc(saddr(smem) + sa_at), dsb = scale_desc(saddr(smem) + sb_at);
+      const uint32_t apart = stage_bytes >> 4;
+      const int whole = p.K / kStep, rest = p.K % kStep;
       int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 1;
+      uint32_t ph = 0, aph = 1, at = 0, ta = 2 * acc_cols;  // (all of TMEM is this CTA's: it starts at 0)
+      const uint32_t ta_end = ta + kSets * kScaleCols;
       bool ok = true;
+      const auto next_stage = [&] {
+        at += apart;
+        ta += kScaleCols;
+        if (ta == ta_end) ta = 2 * acc_cols;
+        if (++s == S) { s = 0; at = 0; ph ^= 1; }
+      };
       for (; more; more = walk.next(p, it)) {
         if (!(ok = mbar_wait(tempty(acc), aph, abort_flag, p.err, 1024))) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)acc * acc_cols;
+        const uint32_t d_tmem = (uint32_t)acc * acc_cols;
         const int cols = mma_cols(it);
         const uint32_t first = mx_desc(BM, cols, 0), second = mx_desc(BM, cols, 1);
-        for (int k = 0; k < p.K; k += kStep) {
-          if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 2048))) break;
+        uint32_t add = 0;
+        for (int i = 0; i < whole; ++i) {
+          if (!(ok = mbar_wait(ready(s), ph, abort_flag, p.err, 2048))) break;
           tc_fence_after();
-          const uint64_t at = s * (stage_bytes >> 4);
           if (elect_lane()) {
-            stage_mmas<true, NB>(d_tmem, tmem_base + 2 * acc_cols + (uint32_t)(s * (8 + 8 * NB)), da + at, db + at,
-                                 dsa + at, dsb + at, first, second, cols, p.K - k, k ? 1 : 0);
+            stage_mmas<true, NB>(d_tmem, ta, da + at, db + at, first, second, kStep, add);
             umma_commit_pair(empty(s), 3);  // frees the stage in both CTAs once these MMAs retire
           }
           __syncwarp();
-          if (++s == S) { s = 0; ph ^= 1; }
+          add = 1;
+          next_stage();
+        }
+        if (ok && rest) {
+          if (!(ok = mbar_wait(ready(s), ph, abort_flag, p.err, 2048))) break;
+          tc_fence_after();
+          if (elect_lane()) {
+            stage_mmas<true, NB>(d_tmem, ta, da + at, db + at, first, second, rest, add);
+            umma_commit_pair(empty(s), 3);
+          }
+          __syncwarp();
+          next_stage();
         }
         if (!ok) break;
         if (elect_lane()) umma_commit_pair(tfull(acc), 3);
@@ -234,6 +275,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       volatile int keep_waiting = 0;
       mbar_wait(done, 0, &keep_waiting, p.err, 16);
+    }
+  } else if (warp >= 2 + kEpiWarps) {
+    if (rank == 0) {  // ---- scales from shared memory to TMEM, of both CTAs (leader only) ----
+      // Two warps, one for the even stages and one for the odd: one alone needs 540 cycles a
+      // stage for its waits and copies, the MMAs 384.  (Not in turns: a barrier's phases
+      // are told apart by their parity, so that whoever waits on a stage has to wait for
+      // each of its phases.)
+      const uint64_t dsa = scale_desc(saddr(smem) + sa_at), dsb = scale_desc(saddr(smem) + sb_at);
+      const uint32_t apart = stage_bytes >> 4;
+      int s = 0, used = 0, old = 0;  // sets in use; the stage whose MMAs read the next set before
+      const int which = warp - 2 - kEpiWarps;
+      uint32_t ph = 0, oph = 0, at = 0, ta = 2 * acc_cols;
+      const uint32_t ta_end = ta + kSets * kScaleCols;
+      bool ok = true;
+      for (; ok && more; more = walk.next(p, it)) {
+        for (int k = 0; k < p.K; k += kStep) {
+          if ((s & 1) == which) {
+            // (as many sets as stages: the stage's own wait will do)
+            if (NB == 2 && used == kSets && !(ok = mbar_wait(empty(old), oph, abort_flag, p.err, 4096))) break;
+            if (!(ok = mbar_wait(full(s), ph, abort_flag, p.err, 8192))) break;
+            tc_fence_after();
+            if (elect_lane()) {
+              stage_scales<true, NB>(ta, dsa + at, dsb + at, p.K - k);
+              commit_leader(ready(s));
+            }
+            __syncwarp();
+          }
+          if (used < kSets) ++used;
+          else if (++old == S) { old = 0; oph ^= 1; }
+          at += apart;
+          ta += kScaleCols;
+          if (ta == ta_end) ta = 2 * acc_cols;
+          if (++s == S) { s = 0; at = 0; ph ^= 1; }
+        }
+      }
+      // (the last copies are done when the MMAs that wait for them are; after an abort they
+      // are waited for here)
+      if (!ok) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 21)) {}
+      }
     }
   } else {  // ---- epilogue ----
     const int quarter = warp & 3;     // TMEM lanes this warp may read
@@ -303,9 +385,12 @@ struct FewArgs {
   int* err;
 };
 
-__device__ __forceinline__ float ld_shared_of(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to(addr, rank)) : "memory");
+__device__ __forceinline__ float4 ld_shared_of(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(map_to(addr, rank))
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t cluster_ctas() {
@@ -350,7 +435,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_launch_next();
-  grid_wait();
+  if (warp != 0) grid_wait();  // (the producer's weights come early, as in k_mx_tiles)
 
   const int blocks = (p.K + kStep - 1) / kStep;  // blocks * shares stays below 2^31
   const int k0 = blocks * rank / shares * kStep;
@@ -360,17 +445,24 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
+    int early = min(p.stages, (k1 - k0 + kStep - 1) / kStep);
+    if (elect_lane())
+      for (int i = 0; i < early; ++i)
+        tma_load_3d(ring + i * p.stage_bytes, &mapW, full(i), (k0 + i * kStep) / 4, m0, 0);
+    __syncwarp();
+    grid_wait();
     for (int k = k0; k < k1; k += kStep) {
       if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 4096))) break;
       if (elect_lane()) {
         const uint32_t sw = ring + s * p.stage_bytes;
         mbar_expect_tx(full(s), p.stage_bytes);
-        tma_load_3d(sw, &mapW, full(s), k / 4, m0, 0);
+        if (early == 0) tma_load_3d(sw, &mapW, full(s), k / 4, m0, 0);
         tma_load_3d(sw + kWeights, &mapX, full(s), k / 4, 0, 0);
         tma_load_3d(sw + sa_at, &scales.w, full(s), 0, k / 128, m0 / 128);
         tma_load_3d(sw + sb_at, &scales.x, full(s), 0, k / 128, 0);
       }
       __syncwarp();
+      if (early) --early;
       if (++s == p.stages) { s = 0; ph ^= 1; }
     }
     if (!ok) {  // gave up: let the copies in flight land before the block leaves
@@ -387,9 +479,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if (!mbar_wait(full(s), ph, abort_flag, p.err, 8192)) break;
       tc_fence_after();
       const uint64_t at = s * (p.stage_bytes >> 4);
+      const uint32_t ta = tmem + 64 + (uint32_t)(s * 16);
       if (elect_lane()) {
-        stage_mmas<false, 1>(tmem, tmem + 64 + (uint32_t)(s * 16), da + at, db + at, dsa + at, dsb + at, first, second,
-                             p.cols, k1 - k, k > k0 ? 1 : 0);
+        stage_scales<false, 1>(ta, dsa + at, dsb + at, k1 - k);
+        stage_mmas<false, 1>(tmem, ta, da + at, db + at, first, second, k1 - k, k > k0 ? 1 : 0);
         umma_commit(empty(s));
       }
       __syncwarp();
@@ -418,15 +511,26 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     tc_fence_before();
   }
   cluster_barrier();  // the partial sums of every share are in place
-  for (int i = (int)threadIdx.x + rank * kFewThreads; i < p.rows * 128; i += kFewThreads * shares) {
-    const int64_t t = i >> 7, f = m0 + (i & 127);
+  // four features a thread, every share's sums in flight together
+  for (int i = (int)threadIdx.x + rank * kFewThreads; i < p.rows * 32; i += kFewThreads * shares) {
+    const int64_t t = i >> 5, f = m0 + (i & 31) * 4;
     if (f >= p.M) continue;
-    float z = 0.f;
-    for (int r = 0; r < shares; ++r) z += ld_shared_of(saddr(part + i), (uint32_t)r);
-    if (p.bias) z += ld_el(p.bias, f, p.type);
-    z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
-    if (p.residual) z += ld_el(p.residual, t * p.r_m + f, p.type);
-    st_el(p.D, t * p.M + f, z, p.type);
+    float4 v[kMaxShares];
+#pragma unroll
+    for (int r = 0; r < kMaxShares; ++r)
+      if (r < shares) v[r] = ld_shared_of(saddr(part + 4 * i), (uint32_t)r);
+    float z[4] = {};
+#pragma unroll
+    for (int r = 0; r < kMaxShares; ++r)
+      if (r < shares) { z[0] += v[r].x; z[1] += v[r].y; z[2] += v[r].z; z[3] += v[r].w; }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (f + c >= p.M) break;
+      if (p.bias) z[c] += ld_el(p.bias, f + c, p.type);
+      z[c] = p.type == DT_F32 ? activate<false>(z[c], p.act) : activate<true>(z[c], p.act);
+      if (p.residual) z[c] += ld_el(p.residual, t * p.r_m + f + c, p.type);
+      st_el(p.D, t * p.M + f + c, z[c], p.type);
+    }
   }
   cluster_barrier();  // no CTA leaves while another reads its sums
   if (warp == 1) {

@@ -6,6 +6,8 @@
 // a tile of 256 steps of it by 64 columns: a lane takes 32 steps of two neighbouring
 // columns, so that it has a block to itself, and the packed rows meet in shared
 // memory.  Bound by HBM.
+#include <type_traits>
+
 #include "common.cuh"
 #include "linear_tiles.cuh"
 #include "mx.cuh"
@@ -18,21 +20,54 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 4;         // rows of a thread, in flight together
 
+// Eight neighbouring numbers of a row.
 template <typename T>
-__device__ __forceinline__ void fetch8(const T* p, int64_t n, bool vec, float* f) {
-  if (vec && n >= 8) {
+struct Eight {
+  static constexpr int kWords = 2 * (int)sizeof(T);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + c);  // read once
-      const T* h = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int i = 0; i < 16 / (int)sizeof(T); ++i) f[c * (16 / sizeof(T)) + i] = to_f32(h[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-}
+  __device__ __forceinline__ void fetch(const T* p) {  // 16-byte loads; read once
+#pragma unroll
+    for (int c = 0; c < kWords / 4; ++c)
+      *reinterpret_cast<uint4*>(w + 4 * c) = __ldcs(reinterpret_cast<const uint4*>(p) + c);
+  }
+  __device__ __forceinline__ void fetch_some(const T* p, int64_t n) {  // the first n, zeros behind
+    T* h = reinterpret_cast<T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = i < n ? p[i] : from_f32<T>(0.f);
+  }
+  // The largest magnitude, as bits of fp32 (magnitudes compare as integers, a NaN above
+  // all).
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    } else {
+      uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+      m = max(m & 0xffffu, m >> 16);
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+      else return __float_as_uint(__half2float(__ushort_as_half((uint16_t)m)));
+    }
+  }
+  __device__ __forceinline__ uint32_t packed(float inverse) const {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+      else if constexpr (std::is_same<T, __nv_bfloat16>::value) f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      else f[i] = __half2float(__ushort_as_half((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu)));
+      f[i] *= inverse;
+    }
+    return mx_pack8(f);
+  }
+};
 
 // Where a thread of the row kernels works: its piece of eight columns, its first row.
 struct Spot {
@@ -45,32 +80,41 @@ __device__ __forceinline__ Spot spot(const MxRows& q, int64_t block) {
   return {cb * across + (threadIdx.x & (across - 1)), rb * down * kRows + (threadIdx.x >> q.log_across), down};
 }
 
-// Loads and rounds a thread's rows, (packed numbers, scale) of each to `give`.
+// Loads and rounds a thread's rows; each row's block of 32 and its scale go to `give`,
+// which all lanes of a warp call together.
 // (rows counts those of all matrices; one row after the other in the outputs)
-template <typename T, typename F>
-__device__ __forceinline__ void quantize_rows(const MxRows& q, int64_t block, F give) {
+template <typename T, typename M, typename F>
+__device__ __forceinline__ void quantize_rows(const MxRows& q, int64_t block, M meanwhile, F give) {
   const Spot at = spot(q, block);
   const int64_t col = at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   const bool there = at.piece < 4 * kb;
-  float f[kRows][8];
+  const T* src = static_cast<const T*>(q.src) + at.row * q.stride + col;  // (of one matrix)
+  Eight<T> v[kRows];
+  const bool whole = q.vec && col + 8 <= q.cols;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = at.row + k * at.by;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[k][i] = 0.f;
+    v[k].zero();
     if (!there || row >= q.rows) continue;
-    const int64_t mat = q.mat_rows == q.rows ? 0 : row / q.mat_rows;
-    fetch8(static_cast<const T*>(q.src) + mat * q.batch_stride + (row - mat * q.mat_rows) * q.stride + col, q.cols - col,
-           q.vec, f[k]);
+    const T* p = src + k * at.by * q.stride;
+    if (q.mat_rows != q.rows) {
+      const int64_t mat = row / q.mat_rows;
+      p = static_cast<const T*>(q.src) + mat * q.batch_stride + (row - mat * q.mat_rows) * q.stride + col;
+    }
+    if (whole) v[k].fetch(p);
+    else v[k].fetch_some(p, q.cols - col);
   }
+  meanwhile();
+  uint32_t* out = reinterpret_cast<uint32_t*>(q.values) + at.row * kb * 4 + at.piece;
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    uint32_t s;
-    const uint32_t v = mx_quantize8(f[k], &s);
+  for (int k = 0; k < kRows; ++k) {  // four lanes share a block
+    uint32_t top = v[k].top();
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t s = mx_scale(top);
     const int64_t row = at.row + k * at.by;
-    if (!there || row >= q.rows) continue;
-    *reinterpret_cast<uint32_t*>(q.values + (row * kb * 4 + at.piece) * 4) = v;
-    if ((at.piece & 3) == 0) give(row, at.piece / 4, s);
+    if (there && row < q.rows) out[k * at.by * kb * 4] = v[k].packed(mx_inverse(s));
+    give(row, at.piece / 4, s, row < q.rows);
   }
 }
 
@@ -79,7 +123,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
   grid_launch_next();
   grid_wait();
   const int64_t kb = (q.cols + kMxBlock - 1) / kMxBlock;
-  quantize_rows<T>(q, blockIdx.x, [&](int64_t row, int64_t b, uint32_t s) { q.scales[row * kb + b] = (uint8_t)s; });
+  quantize_rows<T>(q, blockIdx.x, [] {}, [&](int64_t row, int64_t b, uint32_t s, bool there) {
+    if (there && b < kb && (threadIdx.x & 3) == 0) q.scales[row * kb + b] = (uint8_t)s;
+  });
 }
 
 __device__ __forceinline__ int clamped(const MxPrepare& q, int e) {
@@ -88,19 +134,19 @@ __device__ __forceinline__ int clamped(const MxPrepare& q, int e) {
 }
 
 // Byte of a token row's first scale: the slot of its tile (as Walk cuts ranges into
-// tiles), its row there; -1 for a row of no range.
-__device__ __forceinline__ int64_t token_scales(const MxPrepare& q, int row, int64_t part_bytes, int64_t slot_bytes) {
+// tiles), its row there; -1 for a row of no range.  ends: the ranges' offsets.
+__device__ __forceinline__ int64_t token_scales(const MxPrepare& q, const int* ends, int row, int64_t slot_bytes) {
   int e = 0, lo = 0, hi = (int)q.x.rows;
   if (q.experts) {  // the range that holds the row: the first that ends behind it
     int end = q.experts;
     while (e < end) {
       const int m = (e + end) / 2;
-      if (clamped(q, m + 1) > row) end = m;
+      if (ends[m + 1] > row) end = m;
       else e = m + 1;
     }
     if (e == q.experts) return -1;
-    lo = clamped(q, e);
-    hi = clamped(q, e + 1);
+    lo = ends[e];
+    hi = ends[e + 1];
     if (row < lo) return -1;
   }
   const int n = hi - lo, tiles = (n + q.tile_rows - 1) / q.tile_rows;
@@ -112,22 +158,43 @@ __device__ __forceinline__ int64_t token_scales(const MxPrepare& q, int row, int
 
 // What a product starts from, in one launch: the token rows, then the weights' scales
 // (of the matrices that any row reaches) through shared memory, 128 rows x 64 words.
-constexpr int kWords = 64;
+constexpr int kWords = 16;
+constexpr int kMostRows = kThreads / 4 * kRows;  // of a block
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
   __shared__ uint32_t words[128][kWords + 1];
-  grid_launch_next();
+  __shared__ int ends[1025];
+  __shared__ int64_t place[kMostRows];
   grid_wait();
+  // only now: the product reads the weights before it waits for this launch
+  grid_launch_next();
   const int64_t kb = (q.x.cols + kMxBlock - 1) / kMxBlock, parts = (kb + 3) / 4;
   if (blockIdx.x < q.x_blocks) {
     const int64_t part_bytes = 512 * mx_token_blocks(q.tile_rows), slot_bytes = parts * part_bytes;
-    quantize_rows<T>(q.x, blockIdx.x, [&](int64_t row, int64_t b, uint32_t s) {
-      const int64_t at = token_scales(q, (int)row, part_bytes, slot_bytes);
-      if (at >= 0) {
-        q.x.scales[at + (b >> 2) * part_bytes + (b & 3)] = (uint8_t)s;
-        // the part's blocks behind the row's end
+    const int across = 1 << q.x.log_across, rows = (kThreads >> q.x.log_across) * kRows;
+    const int64_t row0 = blockIdx.x / q.x.col_blocks * rows;
+    const auto find = [&] {  // (while the rows are on their way)
+      if (q.experts) {
+        for (int i = threadIdx.x; i <= q.experts; i += kThreads) ends[i] = clamped(q, i);
+        __syncthreads();
+      }
+      for (int i = threadIdx.x; i < rows; i += kThreads)
+        place[i] = row0 + i < q.x.rows ? token_scales(q, ends, (int)(row0 + i), slot_bytes) : -1;
+      __syncthreads();
+    };
+    quantize_rows<T>(q.x, blockIdx.x, find, [&](int64_t row, int64_t b, uint32_t s, bool there) {
+      // the scales of 128 steps in one store where a warp's lanes hold them (zeros behind
+      // the row's end)
+      const int64_t at = there && b < kb ? place[row - row0] : -1;
+      if (across >= 16) {
+        uint32_t v = s << (8 * (b & 3));
+        v |= __shfl_xor_sync(0xffffffffu, v, 4);
+        v |= __shfl_xor_sync(0xffffffffu, v, 8);
+        if (at >= 0 && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(q.x.scales + at + (b >> 2) * part_bytes) = v;
+      } else if (at >= 0 && (threadIdx.x & 3) == 0) {  // one part
+        q.x.scales[at + b] = (uint8_t)s;
         if (b + 1 == kb)
-          for (int64_t z = b + 1; z < parts * 4; ++z) q.x.scales[at + (z >> 2) * part_bytes + (z & 3)] = 0;
+          for (int64_t z = b + 1; z < 4; ++z) q.x.scales[at + z] = 0;
       }
     });
     return;
@@ -211,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_across(MxRows q, int i
     for (int w = 0; w < 4; ++w) {
       float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = s == kMxNan ? 0.f : to_f32(t[w * 8 + i].v[c]) * inv;
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(t[w * 8 + i].v[c]) * inv;
       v[w] = mx_pack8(f);
     }
     vals[2 * lane + c][warp ^ (lane & 7)] = make_uint4(v[0], v[1], v[2], v[3]);

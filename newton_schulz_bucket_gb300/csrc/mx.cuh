@@ -14,15 +14,15 @@ constexpr uint32_t kMxNan = 255;
 
 // The scale of a block whose largest magnitude has these bits (fp32 without its
 // sign): the power of two at or below it, over 2^2, the largest one at or below 6.
-// A block that holds an infinity or a NaN is NaN as a whole: the scale has no
-// infinity, and its elements would be 0, a factor of the finite ones lost.
+// A block that holds an infinity or a NaN is NaN as a whole (the scale has no
+// infinity), whatever its elements are.
 __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
   const uint32_t e = top >> 23;
   return e == 255 ? kMxNan : (e > 2 ? e - 2 : 0);
 }
-// 1 / scale (0 for NaN).  Both are powers of two, so that dividing by one is
+// 1 / scale (any number for NaN).  Both are powers of two, so that dividing by one is
 // exact; what is lost below 2^-126 is far below half of the smallest element.
-__device__ __forceinline__ float mx_inverse(uint32_t s) { return s == kMxNan ? 0.f : __uint_as_float((254 - s) << 23); }
+__device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254 - s) << 23 & 0x7f800000u); }
 __device__ __forceinline__ float mx_value(uint32_t s) {
   return __uint_as_float(s == kMxNan ? 0x7fc00000u : (s ? s << 23 : 0x00400000u));
 }
@@ -40,20 +40,6 @@ __device__ __forceinline__ uint32_t mx_pack8(const float* f) {
       : "=r"(r)
       : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
-}
-// A lane's eight of the 32 numbers that it shares with the three lanes beside it
-// (lanes 4 i .. 4 i + 3): packed, and their scale.
-__device__ __forceinline__ uint32_t mx_quantize8(float* f, uint32_t* scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  *scale = mx_scale(top);
-  const float inv = mx_inverse(*scale);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = *scale == kMxNan ? 0.f : f[i] * inv;
-  return mx_pack8(f);
 }
 __device__ __forceinline__ void mx_unpack8(uint32_t v, float scale, float* f) {
   uint32_t h[4];
