@@ -18,7 +18,10 @@ namespace muon {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a forward block: its warps' sums have to fit in shared memory.
+template <int NV>
+constexpr int kForward = NV > 16 ? 256 : 512;
+constexpr int kBackward = 256;
 constexpr int kRun = 64;     // tokens a lane adds up before they join the sum of sums
 constexpr float kInf = __builtin_huge_valf();
 
@@ -68,9 +71,9 @@ __device__ __forceinline__ bool exponentials(float* v, int lanes, bool* nan) {
 }
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) k_balance(BalanceArgs a, int lanes, bool vec) {
+__global__ void __launch_bounds__(kForward<NV>) k_balance(BalanceArgs a, int lanes, bool vec) {
   extern __shared__ float fold[];  // [warps][experts] sums, then [experts + 1] counts
-  constexpr int kWarps = kThreads / 32;
+  constexpr int kThreads = kForward<NV>, kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane & (lanes - 1)) * NV;
   int* hist = reinterpret_cast<int*>(fold + kWarps * a.experts);
   grid_launch_next();
@@ -81,15 +84,25 @@ __global__ void __launch_bounds__(kThreads) k_balance(BalanceArgs a, int lanes, 
   const int64_t t0 = a.tokens * blockIdx.x / gridDim.x, t1 = a.tokens * (blockIdx.x + 1) / gridDim.x;
   float sum[NV] = {}, run[NV] = {};
   int live = 0, turn = 0;
-  for (int64_t first = t0 + warp * per; first < t1; first += kWarps * per) {
-    const int64_t t = first + lane / lanes;
-    float v[NV];
+  const auto load = [&](int64_t t, float* v) {
     if (t < t1) {
       load_experts<T, NV>(static_cast<const T*>(a.logits) + t * a.stride, e0, a.experts, vec, v);
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = -kInf;
     }
+  };
+  float next[NV];  // on its way while a token is worked on
+  load(t0 + warp * per + lane / lanes, next);
+  for (int64_t i = t0 * a.top_k + threadIdx.x; i < t1 * a.top_k; i += kThreads) {
+    const int e = a.indices[i];
+    if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);  // whole numbers: the order of the additions does not show
+  }
+  for (int64_t first = t0 + warp * per; first < t1; first += kWarps * per) {
+    float v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = next[i];
+    load(first + kWarps * per + lane / lanes, next);
     bool nan;
     const bool open = exponentials<NV>(v, lanes, &nan);
     float total = 0.f;
@@ -112,11 +125,7 @@ __global__ void __launch_bounds__(kThreads) k_balance(BalanceArgs a, int lanes, 
     for (int o = lanes; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
     if (lane < lanes && e0 + i < a.experts) fold[warp * a.experts + e0 + i] = sum[i];
   }
-  if (live) atomicAdd(&hist[a.experts], live);  // whole numbers: the order of the additions does not show
-  for (int64_t i = t0 * a.top_k + threadIdx.x; i < t1 * a.top_k; i += kThreads) {
-    const int e = a.indices[i];
-    if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);
-  }
+  if (live) atomicAdd(&hist[a.experts], live);
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kThreads) {
     float s = 0.f;
@@ -128,59 +137,83 @@ __global__ void __launch_bounds__(kThreads) k_balance(BalanceArgs a, int lanes, 
     a.part_counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
 }
 
-// The blocks' sums and counts together, in 64 bits: one block, 32 experts at a time
-// (one a lane) with the blocks shared out over its warps.
+// The blocks' sums and counts together: one block.  A warp takes 32 experts
+// (one a lane) of a share of the blocks: as many shares as there are warps for.  Expert
+// `experts` is the tokens.
 __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
-  __shared__ double sums[32][33];
+  __shared__ float sums[32][33];
   __shared__ int counts[32][33];
+  __shared__ float dots[32];
+  __shared__ long long mades[32];
   __shared__ int tokens;
   grid_launch_next();
   grid_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double dot = 0.0;             // warp 0: of the lane's experts
+  const int groups = a.experts / 32 + 1, shares = groups < 32 ? 32 / groups : 1;
+  float dot = 0.f;
   long long made = 0;
-  for (int e0 = 0; e0 <= a.experts; e0 += 32) {  // expert `experts`: the tokens
-    const int e = e0 + lane;
-    double s = 0.0;
+  for (int g0 = 0; g0 < groups; g0 += 32 / shares) {
+    const int g = g0 + warp / shares, share = warp % shares, e = g * 32 + lane;
+    const bool live = warp / shares < 32 / shares && g < groups && e <= a.experts;
+    float s = 0.f;
     int c = 0;
-    for (int b = warp; b < a.blocks && e <= a.experts; b += 32) {
-      if (e < a.experts) s += a.part[(int64_t)b * a.experts + e];
-      c += a.part_counts[(int64_t)b * (a.experts + 1) + e];
+    if (live) {
+#pragma unroll 8
+      for (int b = share; b < a.blocks; b += shares) {
+        if (e < a.experts) s += a.part[(int64_t)b * a.experts + e];
+        c += a.part_counts[(int64_t)b * (a.experts + 1) + e];
+      }
     }
     sums[warp][lane] = s;
     counts[warp][lane] = c;
     __syncthreads();
-    if (warp == 0 && e <= a.experts) {
-      for (int w = 1; w < 32; ++w) { s += sums[w][lane]; c += counts[w][lane]; }
+    if (live && share == 0) {
+      for (int w = 1; w < shares; ++w) { s += sums[warp + w][lane]; c += counts[warp + w][lane]; }
       if (e < a.experts) {
         a.counts[e] = c;
         made += c;
-        dot += s * c;
+        dot = fmaf(s, (float)c, dot);
       } else {
         tokens = c;
       }
     }
     __syncthreads();
   }
-  if (warp == 0) {
-    for (int o = 16; o > 0; o >>= 1) {
-      dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      made += __shfl_xor_sync(0xffffffffu, made, o);
-    }
-    if (lane == 0) {
-      const double over = (double)(made > 0 ? made : 1) * (tokens > 0 ? tokens : 1);
-      *a.loss = (float)((double)a.coef * a.experts * dot / over);
-      *a.live = tokens;
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    made += __shfl_xor_sync(0xffffffffu, made, o);
+  }
+  if (lane == 0) { dots[warp] = dot; mades[warp] = made; }
+  __syncthreads();
+  if (warp > 0) return;
+  dot = warp_sum(dots[lane]);
+  made = mades[lane];
+  for (int o = 16; o > 0; o >>= 1) made += __shfl_xor_sync(0xffffffffu, made, o);
+  if (lane == 0) {
+    *a.loss = a.coef * (float)a.experts * (dot / (float)(made > 0 ? made : 1) / (float)(tokens > 0 ? tokens : 1));
+    *a.live = tokens;
   }
 }
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) k_balance_backward(BalanceArgs a, int lanes, bool vec) {
+__global__ void __launch_bounds__(kBackward) k_balance_backward(BalanceArgs a, int lanes, bool vec) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane & (lanes - 1)) * NV;
   grid_launch_next();
   grid_wait();
-  const int per = 32 / lanes, step = (int)(kThreads / 32) * per;
+  const int per = 32 / lanes, step = (int)(kBackward / 32) * per;
+  const T* res = static_cast<const T*>(a.residual);
+  float v[NV], r[NV];
+  const auto load = [&](int64_t t) {
+    if (t < a.tokens) {
+      load_experts<T, NV>(static_cast<const T*>(a.logits) + t * a.stride, e0, a.experts, vec, v);
+      if (res) load_experts<T, NV>(res + t * a.r_stride, e0, a.experts, vec, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = -kInf;
+    }
+  };
+  const int64_t begin = (int64_t)blockIdx.x * step + warp * per;
+  load(begin + lane / lanes);
   float share[NV], made = 0.f;
   {
     long long all = 0;
@@ -197,17 +230,9 @@ __global__ void __launch_bounds__(kThreads) k_balance_backward(BalanceArgs a, in
   }
   const int tokens = *a.live;
   const float scale = *a.dloss * a.coef * (float)a.experts / (float)(tokens > 0 ? tokens : 1);
-  const T* res = static_cast<const T*>(a.residual);
-  for (int64_t first = (int64_t)blockIdx.x * step + warp * per; first < a.tokens; first += (int64_t)gridDim.x * step) {
+  for (int64_t first = begin; first < a.tokens; first += (int64_t)gridDim.x * step) {
     const int64_t t = first + lane / lanes;
-    float v[NV], r[NV];
-    if (t < a.tokens) {
-      load_experts<T, NV>(static_cast<const T*>(a.logits) + t * a.stride, e0, a.experts, vec, v);
-      if (res) load_experts<T, NV>(res + t * a.r_stride, e0, a.experts, vec, r);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = -kInf;
-    }
+    if (first > begin) load(t);
     bool nan;
     const bool open = exponentials<NV>(v, lanes, &nan);
     float total = 0.f, dot = 0.f;
@@ -253,12 +278,12 @@ cudaError_t run_nv(const BalanceArgs& a, bool backward, bool vec, cudaStream_t s
   int lanes = 1;
   while (lanes * NV < a.experts) lanes *= 2;
   if (backward) {
-    const int64_t step = kThreads / lanes, rounds = (a.tokens + step - 1) / step, most = 8ll * num_sms();
-    return launch_early(k_balance_backward<T, NV>, dim3((unsigned)(rounds < most ? rounds : most)), dim3(kThreads), 0,
+    const int64_t step = kBackward / lanes, rounds = (a.tokens + step - 1) / step, most = 8ll * num_sms();
+    return launch_early(k_balance_backward<T, NV>, dim3((unsigned)(rounds < most ? rounds : most)), dim3(kBackward), 0,
                         s, a, lanes, vec);
   }
-  const size_t smem = sizeof(float) * (kThreads / 32) * a.experts + sizeof(int) * (a.experts + 1);
-  return launch_early(k_balance<T, NV>, dim3((unsigned)a.blocks), dim3(kThreads), smem, s, a, lanes, vec);
+  const size_t smem = sizeof(float) * (kForward<NV> / 32) * a.experts + sizeof(int) * (a.experts + 1);
+  return launch_early(k_balance<T, NV>, dim3((unsigned)a.blocks), dim3(kForward<NV>), smem, s, a, lanes, vec);
 }
 
 template <typename T>
@@ -282,10 +307,10 @@ cudaError_t dispatch(const BalanceArgs& a, bool backward, cudaStream_t s) {
 
 }  // namespace
 
-// Blocks of the forward pass: some tokens each, and at most two an SM (one block
+// Blocks of the forward pass: some tokens each, and at most one an SM (one block
 // joins their sums).
 int balance_blocks(int64_t tokens, int32_t experts) {
-  const int64_t some = (tokens * experts + 8191) / 8192, most = 2ll * num_sms();
+  const int64_t some = (tokens * experts + 4095) / 4096, most = num_sms();
   return (int)(some < 1 ? 1 : (some < most ? some : most));
 }
 

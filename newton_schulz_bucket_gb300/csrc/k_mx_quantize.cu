@@ -18,7 +18,9 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;         // rows of a thread, in flight together
+// Rows of a thread, in flight together.
+template <typename T>
+constexpr int kRowsOf = sizeof(T) == 4 ? 4 : 8;
 
 // Eight neighbouring numbers of a row.
 template <typename T>
@@ -39,8 +41,7 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = i < n ? p[i] : from_f32<T>(0.f);
   }
-  // The largest magnitude, as bits of fp32 (magnitudes compare as integers, a NaN above
-  // all).
+  // The largest magnitude, as bits of fp32; a NaN comes before all.
   __device__ __forceinline__ uint32_t top() const {
     if constexpr (sizeof(T) == 4) {
       uint32_t m = 0;
@@ -48,12 +49,11 @@ struct Eight {
       for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
       return m;
     } else {
-      uint32_t m = w[0] & 0x7fff7fffu;
-#pragma unroll
-      for (int i = 1; i < 4; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
-      m = max(m & 0xffffu, m >> 16);
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
-      else return __float_as_uint(__half2float(__ushort_as_half((uint16_t)m)));
+      using Pair = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+      const Pair* h = reinterpret_cast<const Pair*>(w);
+      Pair m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float_as_uint(__bfloat162float(__hmax_nan(m.x, m.y)));
+      else return __float_as_uint(__half2float(__hmax_nan(m.x, m.y)));
     }
   }
   __device__ __forceinline__ uint32_t packed(float inverse) const {
@@ -71,60 +71,67 @@ struct Eight {
 
 // Where a thread of the row kernels works: its piece of eight columns, its first row.
 struct Spot {
-  int64_t piece, row;
-  int by;                        // rows between a thread's rows
+  int64_t row;
+  int piece, by;                 // rows between a thread's rows
 };
-__device__ __forceinline__ Spot spot(const MxRows& q, int64_t block) {
+template <int kRows>
+__device__ __forceinline__ Spot spot(const MxRows& q, uint32_t block) {
   const int across = 1 << q.log_across, down = kThreads >> q.log_across;
-  const int64_t cb = block % q.col_blocks, rb = block / q.col_blocks;
-  return {cb * across + (threadIdx.x & (across - 1)), rb * down * kRows + (threadIdx.x >> q.log_across), down};
+  const uint32_t rb = block / q.col_blocks, cb = block - rb * q.col_blocks;
+  return {(int64_t)rb * down * kRows + (threadIdx.x >> q.log_across),
+          (int)cb * across + ((int)threadIdx.x & (across - 1)), down};
 }
 
 // Loads and rounds a thread's rows; each row's block of 32 and its scale go to `give`,
-// which all lanes of a warp call together.
-// (rows counts those of all matrices; one row after the other in the outputs)
-template <typename T, typename M, typename F>
-__device__ __forceinline__ void quantize_rows(const MxRows& q, int64_t block, M meanwhile, F give) {
-  const Spot at = spot(q, block);
-  const int64_t col = at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
+// which all lanes of a warp call together.  kMats: rows of several matrices (rows counts
+// all of them; one row after the other in the outputs).
+template <typename T, bool kMats, typename M, typename F>
+__device__ __forceinline__ void quantize_rows(const MxRows& q, const Spot& at, M meanwhile, F give) {
+  constexpr int kRows = kRowsOf<T>;
+  const int64_t col = (int64_t)at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   const bool there = at.piece < 4 * kb;
-  const T* src = static_cast<const T*>(q.src) + at.row * q.stride + col;  // (of one matrix)
+  const T* src = static_cast<const T*>(q.src) + at.row * q.stride + col;
+  const int64_t step = at.by * q.stride;
+  const int left = (int)min((int64_t)kRows * at.by, q.rows - at.row);  // rows from the first on
   Eight<T> v[kRows];
   const bool whole = q.vec && col + 8 <= q.cols;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int64_t row = at.row + k * at.by;
     v[k].zero();
-    if (!there || row >= q.rows) continue;
-    const T* p = src + k * at.by * q.stride;
-    if (q.mat_rows != q.rows) {
+    const T* p = src + k * step;
+    if (kMats) {
+      const int64_t row = at.row + k * at.by;
       const int64_t mat = row / q.mat_rows;
       p = static_cast<const T*>(q.src) + mat * q.batch_stride + (row - mat * q.mat_rows) * q.stride + col;
     }
-    if (whole) v[k].fetch(p);
-    else v[k].fetch_some(p, q.cols - col);
+    if (there && k * at.by < left) {
+      if (whole) v[k].fetch(p);
+      else v[k].fetch_some(p, q.cols - col);
+    }
   }
   meanwhile();
   uint32_t* out = reinterpret_cast<uint32_t*>(q.values) + at.row * kb * 4 + at.piece;
+  const int64_t out_step = at.by * kb * 4;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {  // four lanes share a block
     uint32_t top = v[k].top();
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t s = mx_scale(top);
-    const int64_t row = at.row + k * at.by;
-    if (there && row < q.rows) out[k * at.by * kb * 4] = v[k].packed(mx_inverse(s));
-    give(row, at.piece / 4, s, row < q.rows);
+    const bool live = k * at.by < left;
+    if (there && live) out[k * out_step] = v[k].packed(mx_inverse(s));
+    give(k, at.piece / 4, s, live);
   }
 }
 
-template <typename T>
+template <typename T, bool kMats>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
   grid_launch_next();
   grid_wait();
   const int64_t kb = (q.cols + kMxBlock - 1) / kMxBlock;
-  quantize_rows<T>(q, blockIdx.x, [] {}, [&](int64_t row, int64_t b, uint32_t s, bool there) {
-    if (there && b < kb && (threadIdx.x & 3) == 0) q.scales[row * kb + b] = (uint8_t)s;
+  const Spot at = spot<kRowsOf<T>>(q, blockIdx.x);
+  quantize_rows<T, kMats>(q, at, [] {}, [&](int k, int b, uint32_t s, bool live) {
+    if (live && b < kb && (threadIdx.x & 3) == 0) q.scales[(at.row + k * at.by) * kb + b] = (uint8_t)s;
   });
 }
 
@@ -133,76 +140,78 @@ __device__ __forceinline__ int clamped(const MxPrepare& q, int e) {
   return v < 0 ? 0 : (v > rows ? rows : v);
 }
 
-// Byte of a token row's first scale: the slot of its tile (as Walk cuts ranges into
-// tiles), its row there; -1 for a row of no range.  ends: the ranges' offsets.
-__device__ __forceinline__ int64_t token_scales(const MxPrepare& q, const int* ends, int row, int64_t slot_bytes) {
+// Where a token row's scales start, in words of 128 steps' (four): the slot of its tile
+// (as Walk cuts ranges into tiles), its row there; kNowhere for a row of no range.
+constexpr uint32_t kNowhere = 0xffffffffu;
+__device__ __forceinline__ uint32_t token_scales(const MxPrepare& q, int row, uint32_t slot_words) {
   int e = 0, lo = 0, hi = (int)q.x.rows;
   if (q.experts) {  // the range that holds the row: the first that ends behind it
     int end = q.experts;
     while (e < end) {
       const int m = (e + end) / 2;
-      if (ends[m + 1] > row) end = m;
+      if (clamped(q, m + 1) > row) end = m;
       else e = m + 1;
     }
-    if (e == q.experts) return -1;
-    lo = ends[e];
-    hi = ends[e + 1];
-    if (row < lo) return -1;
+    if (e == q.experts) return kNowhere;
+    lo = clamped(q, e);
+    hi = clamped(q, e + 1);
+    if (row < lo) return kNowhere;
   }
   const int n = hi - lo, tiles = (n + q.tile_rows - 1) / q.tile_rows;
   const int units = (n + 31) / 32, each = units / tiles, more = units - each * tiles, u = (row - lo) / 32;
   const int tile = u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
   const int r = row - lo - token_start(n, tiles, tile);
-  return (int64_t)(mx_token_slot(lo, e, q.tile_rows) + tile) * slot_bytes + (r >> 7) * 512 + mx_scale_byte(r, 0);
+  return (mx_token_slot(lo, e, q.tile_rows) + tile) * slot_words + (r >> 7) * 128 + mx_scale_byte(r, 0) / 4;
 }
 
 // What a product starts from, in one launch: the token rows, then the weights' scales
 // (of the matrices that any row reaches) through shared memory, 128 rows x 64 words.
 constexpr int kWords = 16;
-constexpr int kMostRows = kThreads / 4 * kRows;  // of a block
-template <typename T>
+// kWide: rows of at least a warp's 256 columns.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
   __shared__ uint32_t words[128][kWords + 1];
-  __shared__ int ends[1025];
-  __shared__ int64_t place[kMostRows];
   grid_wait();
   // only now: the product reads the weights before it waits for this launch
   grid_launch_next();
   const int64_t kb = (q.x.cols + kMxBlock - 1) / kMxBlock, parts = (kb + 3) / 4;
-  if (blockIdx.x < q.x_blocks) {
-    const int64_t part_bytes = 512 * mx_token_blocks(q.tile_rows), slot_bytes = parts * part_bytes;
-    const int across = 1 << q.x.log_across, rows = (kThreads >> q.x.log_across) * kRows;
-    const int64_t row0 = blockIdx.x / q.x.col_blocks * rows;
+  if (blockIdx.x < (uint32_t)q.x_blocks) {
+    constexpr int kRows = kRowsOf<T>;
+    const uint32_t part_words = 128 * mx_token_blocks(q.tile_rows), slot_words = (uint32_t)parts * part_words;
+    const Spot at = spot<kRows>(q.x, blockIdx.x);
+    // lanes of a warp that share a row (w of them) find the places of its kRows rows
+    const int across = kWide ? 32 : 1 << q.x.log_across, own = threadIdx.x & (across - 1);
+    uint32_t place[2] = {kNowhere, kNowhere};  // of rows own and own + across
     const auto find = [&] {  // (while the rows are on their way)
-      if (q.experts) {
-        for (int i = threadIdx.x; i <= q.experts; i += kThreads) ends[i] = clamped(q, i);
-        __syncthreads();
+#pragma unroll
+      for (int h = 0; h < (kWide ? 1 : 2); ++h) {
+        const int64_t row = at.row + (own + h * across) * at.by;
+        if (own + h * across < kRows && row < q.x.rows) place[h] = token_scales(q, (int)row, slot_words);
       }
-      for (int i = threadIdx.x; i < rows; i += kThreads)
-        place[i] = row0 + i < q.x.rows ? token_scales(q, ends, (int)(row0 + i), slot_bytes) : -1;
-      __syncthreads();
     };
-    quantize_rows<T>(q.x, blockIdx.x, find, [&](int64_t row, int64_t b, uint32_t s, bool there) {
+    quantize_rows<T, false>(q.x, at, find, [&](int k, int b, uint32_t s, bool) {
       // the scales of 128 steps in one store where a warp's lanes hold them (zeros behind
       // the row's end)
-      const int64_t at = there && b < kb ? place[row - row0] : -1;
-      if (across >= 16) {
+      const uint32_t to = kWide ? __shfl_sync(0xffffffffu, place[0], k)
+                                : __shfl_sync(0xffffffffu, k < across ? place[0] : place[1], k & (across - 1), across);
+      const uint32_t word = to + (uint32_t)(b >> 2) * part_words;
+      if (kWide || across == 16) {
         uint32_t v = s << (8 * (b & 3));
         v |= __shfl_xor_sync(0xffffffffu, v, 4);
         v |= __shfl_xor_sync(0xffffffffu, v, 8);
-        if (at >= 0 && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(q.x.scales + at + (b >> 2) * part_bytes) = v;
-      } else if (at >= 0 && (threadIdx.x & 3) == 0) {  // one part
-        q.x.scales[at + b] = (uint8_t)s;
-        if (b + 1 == kb)
-          for (int64_t z = b + 1; z < 4; ++z) q.x.scales[at + z] = 0;
+        if (to != kNowhere && b < (int)kb && (threadIdx.x & 15) == 0) reinterpret_cast<uint32_t*>(q.x.scales)[word] = v;
+      } else if (to != kNowhere && b < (int)kb && (threadIdx.x & 3) == 0) {  // one part
+        uint8_t* bytes = q.x.scales + (int64_t)word * 4;
+        bytes[b] = (uint8_t)s;
+        if (b + 1 == (int)kb)
+          for (int z = b + 1; z < 4; ++z) bytes[z] = 0;
       }
     });
     return;
   }
-  int64_t j = blockIdx.x - q.x_blocks;
-  const int64_t run = j % q.w_parts, tiles = (q.out + 127) / 128;
-  j /= q.w_parts;
-  const int64_t mat = j / tiles, row0 = j % tiles * 128;
+  const uint32_t j = blockIdx.x - (uint32_t)q.x_blocks, runs = (uint32_t)q.w_parts;
+  const uint32_t tiles = (uint32_t)((q.out + 127) / 128), tile = j / runs;
+  const int64_t run = j - tile * runs, mat = tile / tiles, row0 = (int64_t)(tile - mat * tiles) * 128;
   if (q.experts && clamped(q, (int)mat) >= clamped(q, (int)mat + 1)) return;
   const uint8_t* src = q.w_scales + (mat * q.out + row0) * kb;
   const int rows = (int)min((int64_t)128, q.out - row0);
@@ -233,39 +242,38 @@ __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
   }
 }
 
-// Two neighbouring columns of one row of a matrix stored across the sum.
-template <typename T>
-struct Two {
-  T v[2];
-  __device__ __forceinline__ void fetch(const T* p, int n, bool vec) {
-    if (vec && n >= 2) {
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint2*>(v) = __ldcs(reinterpret_cast<const uint2*>(p));
-      else *reinterpret_cast<uint32_t*>(v) = __ldcs(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      v[0] = n > 0 ? p[0] : from_f32<T>(0.f);
-      v[1] = n > 1 ? p[1] : from_f32<T>(0.f);
-    }
-  }
-};
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize_across(MxRows q, int in_tiles, int out_tiles) {
   __shared__ uint4 vals[64][8];  // [column][block ^ (column / 2 & 7)]
   __shared__ uint8_t scale[64][8];
+  struct Two {
+    T v[2];
+  };
+  using Word = typename std::conditional<sizeof(T) == 4, uint2, uint32_t>::type;
   grid_launch_next();
   grid_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t b = blockIdx.x;
-  const int64_t o0 = b % out_tiles * 64, kb = (q.cols + kMxBlock - 1) / kMxBlock;
-  b /= out_tiles;
-  const int64_t b0 = b % in_tiles * 8, mat = b / in_tiles;
+  uint32_t b = blockIdx.x / (uint32_t)out_tiles;
+  const int64_t o0 = (int64_t)(blockIdx.x - b * out_tiles) * 64, kb = (q.cols + kMxBlock - 1) / kMxBlock;
+  const int64_t mat = b / (uint32_t)in_tiles, b0 = (int64_t)(b - (uint32_t)mat * in_tiles) * 8;
   const int64_t i0 = (b0 + warp) * kMxBlock, o = o0 + 2 * lane;
   const int n = (int)max((int64_t)0, min((int64_t)2, q.mat_rows - o));  // the lane's columns
   const int steps = (int)max((int64_t)0, min((int64_t)kMxBlock, q.cols - i0));
   const T* src = static_cast<const T*>(q.src) + mat * q.batch_stride + i0 * q.stride + o;
-  Two<T> t[kMxBlock];
+  Two t[kMxBlock];
+  if (q.vec && n == 2 && steps == kMxBlock) {
 #pragma unroll
-  for (int i = 0; i < kMxBlock; ++i) t[i].fetch(src + i * q.stride, i < steps ? n : 0, q.vec);
+    for (int i = 0; i < kMxBlock; ++i) {
+      const Word u = __ldcs(reinterpret_cast<const Word*>(src + i * q.stride));
+      t[i] = *reinterpret_cast<const Two*>(&u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMxBlock; ++i) {
+      t[i].v[0] = i < steps && n > 0 ? src[i * q.stride] : from_f32<T>(0.f);
+      t[i].v[1] = i < steps && n > 1 ? src[i * q.stride + 1] : from_f32<T>(0.f);
+    }
+  }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint32_t top = 0;
@@ -295,12 +303,14 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_across(MxRows q, int i
   }
 }
 
+constexpr int kBackRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
   grid_launch_next();
   grid_wait();
-  const Spot at = spot(q, blockIdx.x);
-  const int64_t col = at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
+  constexpr int kRows = kBackRows;
+  const Spot at = spot<kRows>(q, blockIdx.x);
+  const int64_t col = (int64_t)at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   if (col >= q.cols) return;
   uint32_t v[kRows], s[kRows];
 #pragma unroll
@@ -333,12 +343,12 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
 }
 
 // How blocks cover rows of pieces of eight columns; their number.
-int64_t shape_rows(MxRows* q) {
+int64_t shape_rows(MxRows* q, int each) {
   const int64_t pieces = 4 * mx_blocks_of(q->cols);
   q->log_across = 2;
   while (q->log_across < 8 && (1 << q->log_across) < pieces) ++q->log_across;
-  q->col_blocks = (pieces + (1 << q->log_across) - 1) >> q->log_across;
-  const int64_t down = (int64_t)(kThreads >> q->log_across) * kRows;
+  q->col_blocks = (uint32_t)(pieces + (1 << q->log_across) - 1) >> q->log_across;
+  const int64_t down = (int64_t)(kThreads >> q->log_across) * each;
   return (q->rows + down - 1) / down * q->col_blocks;
 }
 // 16-byte loads: every row starts on 16 bytes.
@@ -357,22 +367,24 @@ cudaError_t run(MxRows q, MxOp op, cudaStream_t s) {
     return launch_early(k_mx_quantize_across<T>, dim3((unsigned)(ti * to * (q.rows / q.mat_rows))), dim3(kThreads), 0, s,
                         q, (int)ti, (int)to);
   }
-  const dim3 grid((unsigned)shape_rows(&q));
+  const dim3 grid((unsigned)shape_rows(&q, op == MX_BACK ? kBackRows : kRowsOf<T>));
   if (op == MX_BACK) {
     q.vec = reinterpret_cast<uintptr_t>(q.dst) % 16 == 0 && q.cols % 8 == 0;
     return launch_early(k_mx_dequantize<T>, grid, dim3(kThreads), 0, s, q);
   }
   q.vec = vector_rows<T>(q);
-  return launch_early(k_mx_quantize_rows<T>, grid, dim3(kThreads), 0, s, q);
+  return q.mat_rows == q.rows ? launch_early(k_mx_quantize_rows<T, false>, grid, dim3(kThreads), 0, s, q)
+                              : launch_early(k_mx_quantize_rows<T, true>, grid, dim3(kThreads), 0, s, q);
 }
 
 template <typename T>
 cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
-  q.x_blocks = shape_rows(&q.x);
+  q.x_blocks = shape_rows(&q.x, kRowsOf<T>);
   q.x.vec = vector_rows<T>(q.x);
   q.w_parts = (mx_parts(q.x.cols) + kWords - 1) / kWords;
   const int64_t grid = q.x_blocks + q.w_parts * ((q.out + 127) / 128) * q.mats;
-  return launch_early(k_mx_prepare<T>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
+  return q.x.log_across >= 5 ? launch_early(k_mx_prepare<T, true>, dim3((unsigned)grid), dim3(kThreads), 0, s, q)
+                             : launch_early(k_mx_prepare<T, false>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
 }
 
 }  // namespace
@@ -380,7 +392,7 @@ cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
 // Blocks of the largest grid of these kernels.
 int64_t mx_blocks(int64_t rows, int64_t mat_rows, int64_t cols) {
   const int64_t kb = (cols + kMxBlock - 1) / kMxBlock;
-  const int64_t along = (rows / kRows + 1) * ((kb * 4 + 255) / 256);
+  const int64_t along = (rows / 4 + 1) * ((kb * 4 + 255) / 256);
   const int64_t across = (kb + 7) / 8 * ((mat_rows + 63) / 64) * (mat_rows ? rows / mat_rows : 0);
   return along > across ? along : across;
 }

@@ -3,14 +3,21 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + r,   dw = sum over rows of dy xh,   db = sum of dy.
 //
 // Every tensor crosses HBM once: a row stays in the registers of its threads (16
-// elements each) between the sums over it and its result, and the next row's loads
-// are in flight meanwhile.  Rows of up to 512 elements belong to 1 to 32 lanes of a
+// elements each) between the sums over it and its result, and the next rows are on
+// their way meanwhile: several, by bulk copies into a ring in shared memory, where a row
+// belongs to a block and starts on 16 bytes; else the next one, into registers.  Rows of up to 512 elements belong to 1 to 32 lanes of a
 // warp, longer ones to a block.  The variance is the sum of squares about the mean,
 // not a difference of two large sums.  Blocks stay for many rows, so that the
 // weights are read once a block and the sums over rows (dw, db) grow in registers
 // too; each part of rows leaves one partial sum, and a second kernel adds the
 // parts in a fixed order.  No atomics: the same bits every time.
+#include <mutex>
+#include <type_traits>
+#include <utility>
+#include <vector>
+
 #include "common.cuh"
+#include "mbarrier.cuh"
 #include "ops.h"
 
 namespace muon {
@@ -58,51 +65,131 @@ template <typename T, int N>
 __device__ __forceinline__ void put(T* p, const float* f) {
   if constexpr (N == 1) {
     *p = from_f32<T>(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   } else {
-    alignas(16) T h[N];
+    uint4 u;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-    for (int i = 0; i < N; ++i) h[i] = from_f32<T>(f[i]);
-#pragma unroll
-    for (int i = 0; i < N * (int)sizeof(T) / 16; ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(h)[i];
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = u;
   }
 }
+
+// Two elements at a time.
+__device__ __forceinline__ float2 at2(const float* f, int i) { return make_float2(f[2 * i], f[2 * i + 1]); }
+__device__ __forceinline__ void set2(float* f, int i, float2 v) { f[2 * i] = v.x; f[2 * i + 1] = v.y; }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Sums over the threads of a row: lanes of a warp (lanes of them, a power of two),
 // or the block.  A block's sums alternate between two buffers, so that one barrier
 // each is enough.
+using Sums = float[2][2][32];  // [buffer][value][warp], zeros behind the last warp
 template <bool kWarp>
 struct RowSum {
-  float (*red)[2][32];  // [buffer][value][warp]
+  Sums* red;
   int lanes, turn;
+  __device__ __forceinline__ void init() {
+    if constexpr (!kWarp) {
+      for (int i = threadIdx.x; i < 128; i += blockDim.x) (&(*red)[0][0][0])[i] = 0.f;
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ float join(int value) {
+    const float4* r = reinterpret_cast<const float4*>((*red)[turn][value]);
+    float4 t = r[0];
+    for (int w = 1; 128 * w < (int)blockDim.x; ++w) {
+      const float4 u = r[w];
+      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+    return (t.x + t.y) + (t.z + t.w);
+  }
+  __device__ __forceinline__ float lanes_sum(float a) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+  }
   __device__ __forceinline__ void operator()(float& a, float& b) {
     if constexpr (kWarp) {
-      for (int o = lanes >> 1; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
+      a = lanes_sum(a);
+      b = lanes_sum(b);
     } else {
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
       a = warp_sum(a);
       b = warp_sum(b);
-      if (lane == 0) { red[turn][0][warp] = a; red[turn][1][warp] = b; }
+      if ((threadIdx.x & 31) == 0) { (*red)[turn][0][threadIdx.x >> 5] = a; (*red)[turn][1][threadIdx.x >> 5] = b; }
       __syncthreads();
-      a = warp_sum(lane < warps ? red[turn][0][lane] : 0.f);
-      b = warp_sum(lane < warps ? red[turn][1][lane] : 0.f);
+      a = join(0);
+      b = join(1);
       turn ^= 1;
     }
   }
   __device__ __forceinline__ void operator()(float& a) {
     if constexpr (kWarp) {
-      for (int o = lanes >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      a = lanes_sum(a);
     } else {
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
       a = warp_sum(a);
-      if (lane == 0) red[turn][0][warp] = a;
+      if ((threadIdx.x & 31) == 0) (*red)[turn][0][threadIdx.x >> 5] = a;
       __syncthreads();
-      a = warp_sum(lane < warps ? red[turn][0][lane] : 0.f);
+      a = join(0);
       turn ^= 1;
     }
+  }
+};
+
+// Rows of a block on their way: `kTensors` tensors' rows to a slot, by bulk copies that
+// one thread issues and a barrier counts.  A slot is free once every thread of the block
+// has taken its pieces: after the next __syncthreads.
+constexpr int kMostSlots = 8;
+template <int kTensors>
+struct RowRing {
+  uint8_t* slots;
+  uint64_t* full;
+  volatile int* abort_flag;
+  int* err;
+  uint32_t row_bytes, slot_bytes;
+  int n, at;                   // slots, the current one
+  uint32_t phase;
+  const uint8_t* src[kTensors];  // nullable
+  int64_t pitch[kTensors];       // bytes between rows
+
+  static __device__ __forceinline__ uint32_t shared(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < n; ++i) mbar_init(shared(full + i), 1);
+      *abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void fetch(int slot, int64_t row) {  // one thread
+    const uint32_t bar = shared(full + slot);
+    uint32_t to = shared(slots) + slot * slot_bytes, bytes = 0;
+#pragma unroll
+    for (int t = 0; t < kTensors; ++t) bytes += src[t] ? row_bytes : 0;
+    mbar_expect_tx(bar, bytes);
+#pragma unroll
+    for (int t = 0; t < kTensors; ++t, to += row_bytes) {
+      if (!src[t]) continue;
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                   "l"(src[t] + row * pitch[t]), "r"(row_bytes), "r"(bar)
+                   : "memory");
+    }
+  }
+  // The current slot, once its rows are there.  (A wait that runs out is reported by the
+  // error word; the block goes on, so that its threads stay together.)
+  __device__ __forceinline__ const uint8_t* take() {
+    mbar_wait(shared(full + at), phase, abort_flag, err, 1 << 16);
+    return slots + at * slot_bytes;
+  }
+  __device__ __forceinline__ void next() {
+    if (++at == n) { at = 0; phase ^= 1; }
   }
 };
 
@@ -133,13 +220,19 @@ __device__ __forceinline__ void load_weights(const void* w, int col, bool live, 
   }
 }
 
-template <typename T, typename W, int N, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm(NormArgs a, int lanes) {
-  constexpr int P = kEach / N;
-  __shared__ float red[2][2][32];
+// E elements a thread; kThreads: most threads of a block, kBlocks of which fit on an SM.
+template <typename T, typename W, int N, int E, bool kWarp, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lanes) {
+  constexpr int P = E / N;
+  constexpr bool kRing = !kWarp && N > 1;
+  __shared__ __align__(16) Sums red;
+  extern __shared__ __align__(128) uint8_t ring_bytes[];
+  __shared__ uint64_t full[kMostSlots];
+  __shared__ int aborted;
   grid_launch_next();
   const Place at = place<kWarp, N>(lanes);
-  RowSum<kWarp> sum{red, lanes, 0};
+  RowSum<kWarp> sum{&red, lanes, 0};
+  sum.init();
   const int h = (int)a.width;
   bool live[P];
 #pragma unroll
@@ -149,11 +242,19 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm(Nor
   T* y = static_cast<T*>(a.y) + at.col;
   const int64_t by = (int64_t)gridDim.x * at.rows;
   int64_t first = (int64_t)blockIdx.x * at.rows;  // the round's first row: the same for the block
+  RowRing<1> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.slot_bytes, a.slots, 0, 0,
+                  {static_cast<const uint8_t*>(a.x)}, {a.x_stride * (int64_t)sizeof(T)}};
   Piece<T, N> v[P];
+  if constexpr (kRing) {
+    ring.init();
+    if (threadIdx.x == 0)
+      for (int i = 0; i < a.slots && first + i * by < a.rows; ++i) ring.fetch(i, first + i * by);
+  } else {
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (live[p] && first + at.row < a.rows) v[p].stream(x + (first + at.row) * a.x_stride + p * at.step);
-  float w[kEach], b[kEach];
+    for (int p = 0; p < P; ++p)
+      if (live[p] && first + at.row < a.rows) v[p].stream(x + (first + at.row) * a.x_stride + p * at.step);
+  }
+  float w[E], b[E];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
@@ -161,38 +262,54 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm(Nor
   }
   for (; first < a.rows; first += by) {
     const int64_t row = first + at.row;
-    float f[kEach];
-    float s = 0.f;
+    float f[E];
+    if constexpr (kRing) {
+      const T* slot = reinterpret_cast<const T*>(ring.take()) + at.col;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        if (live[p]) v[p].fetch(slot + p * at.step);
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
+      if (live[p] && row < a.rows) {
+        v[p].open(f + p * N);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[p * N + i] = 0.f;
+      }
+      if (!kRing && live[p] && row + by < a.rows) v[p].stream(x + (row + by) * a.x_stride + p * at.step);
+    }
+    float2 s2 = at2(f, 0);
+#pragma unroll
+    for (int i = 1; i < E / 2; ++i) s2 = __fadd2_rn(s2, at2(f, i));
+    float s = s2.x + s2.y;
+    sum(s);
+    if constexpr (kRing) {  // (every thread has its pieces: the sum was a barrier)
+      if (threadIdx.x == 0 && row + a.slots * by < a.rows) ring.fetch(ring.at, row + a.slots * by);
+      ring.next();
+    }
+    const float mean = s / (float)h;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) set2(f, i, __fadd2_rn(at2(f, i), both(-mean)));
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (live[p]) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) f[p * N + i] = 0.f;
-      if (live[p] && row < a.rows) v[p].open(f + p * N);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s += f[p * N + i];
-      if (live[p] && row + by < a.rows) v[p].stream(x + (row + by) * a.x_stride + p * at.step);
     }
-    sum(s);
-    const float mean = s / (float)h;
-    float q = 0.f;
+    float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        f[p * N + i] -= mean;
-        if (live[p]) q = fmaf(f[p * N + i], f[p * N + i], q);
-      }
-    }
+    for (int i = 0; i < E / 2; ++i) q2 = __ffma2_rn(at2(f, i), at2(f, i), q2);
+    float q = q2.x + q2.y;
     sum(q);
     const float rstd = 1.f / sqrtf(q / (float)h + a.eps);
     if (row >= a.rows) continue;  // (after the sums, which every lane takes part in)
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (!live[p]) continue;
+    for (int i = 0; i < E / 2; ++i)
+      set2(f, i, __ffma2_rn(__fmul2_rn(at2(f, i), both(rstd)), at2(w, i), at2(b, i)));
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[p * N + i] = fmaf(f[p * N + i] * rstd, w[p * N + i], b[p * N + i]);
-      put<T, N>(y + row * h + p * at.step, f + p * N);
-    }
+    for (int p = 0; p < P; ++p)
+      if (live[p]) put<T, N>(y + row * h + p * at.step, f + p * N);
     if (at.col == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -204,11 +321,16 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm(Nor
 template <typename T, typename W, int N, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_backward(NormArgs a, int lanes) {
   constexpr int P = kEach / N;
-  __shared__ float red[2][2][32];
-  extern __shared__ float fold[];  // kWarp: [warps][2][width]
+  constexpr bool kRing = !kWarp && N > 1;
+  __shared__ __align__(16) Sums red;
+  extern __shared__ __align__(128) uint8_t ring_bytes[];
+  float* fold = reinterpret_cast<float*>(ring_bytes);  // kWarp: [warps][2][width]
+  __shared__ uint64_t full[kMostSlots];
+  __shared__ int aborted;
   grid_launch_next();
   const Place at = place<kWarp, N>(lanes);
-  RowSum<kWarp> sum{red, lanes, 0};
+  RowSum<kWarp> sum{&red, lanes, 0};
+  sum.init();
   const int h = (int)a.width;
   bool live[P];
 #pragma unroll
@@ -222,9 +344,19 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
   const float per = 1.f / (float)h;
+  RowRing<3> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.slot_bytes, a.slots, 0, 0,
+                  {static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.dy),
+                   a.dx ? static_cast<const uint8_t*>(a.residual) : nullptr},
+                  {a.x_stride * (int64_t)sizeof(T), a.dy_stride * (int64_t)sizeof(T), a.r_stride * (int64_t)sizeof(T)}};
+  if constexpr (kRing) ring.init();
   for (int64_t part = blockIdx.x; part < a.parts; part += gridDim.x) {
     const int64_t last = min(a.rows, (part + 1) * a.part_rows);
     int64_t first = part * a.part_rows;
+    if constexpr (kRing) {  // (the part before has used up what it fetched)
+      if (threadIdx.x == 0)
+        for (int i = 0; i < a.slots && first + i < last; ++i)
+          ring.fetch(ring.at + i < a.slots ? ring.at + i : ring.at + i - a.slots, first + i);
+    }
     float sw[kEach] = {}, sb[kEach] = {};
     Piece<T, N> vx[P], vd[P];
     float mean = 0.f, rstd = 0.f;
@@ -234,7 +366,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
       rstd = a.rstd[row];
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        if (!live[p]) continue;
+        if (kRing || !live[p]) continue;
         vx[p].stream(x + row * a.x_stride + p * at.step);
         vd[p].stream(dy + row * a.dy_stride + p * at.step);
       }
@@ -243,29 +375,47 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
       const int64_t row = first + at.row, next = row + at.rows;
       const bool mine = row < last;
       float xh[kEach], d[kEach];
-      float s1 = 0.f, s2 = 0.f;
+      float s1, s2;
+      Piece<T, N> vr[P];
+      if constexpr (kRing) {
+        const T* slot = reinterpret_cast<const T*>(ring.take()) + at.col;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (!live[p]) continue;
+          vx[p].fetch(slot + p * at.step);
+          vd[p].fetch(slot + h + p * at.step);
+          if (a.residual) vr[p].fetch(slot + 2 * h + p * at.step);
+        }
+      }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) xh[p * N + i] = mean, d[p * N + i] = 0.f;
         if (mine && live[p]) {
           vx[p].open(xh + p * N);
           vd[p].open(d + p * N);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) xh[p * N + i] = mean, d[p * N + i] = 0.f;
         }
-        if (next < last && live[p]) {
+        if (!kRing && next < last && live[p]) {
           vx[p].stream(x + next * a.x_stride + p * at.step);
           vd[p].stream(dy + next * a.dy_stride + p * at.step);
         }
       }
       const float r = rstd;
+      {
+        float2 t1 = make_float2(0.f, 0.f), t2 = t1;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        xh[i] = (xh[i] - mean) * r;
-        const float g = d[i] * w[i];
-        s1 += g;
-        s2 = fmaf(g, xh[i], s2);
-        sw[i] = fmaf(d[i], xh[i], sw[i]);
-        sb[i] += d[i];
+        for (int i = 0; i < kEach / 2; ++i) {
+          const float2 x2 = __fmul2_rn(__fadd2_rn(at2(xh, i), both(-mean)), both(r)), d2 = at2(d, i);
+          const float2 g = __fmul2_rn(d2, at2(w, i));
+          t1 = __fadd2_rn(t1, g);
+          t2 = __ffma2_rn(g, x2, t2);
+          set2(sw, i, __ffma2_rn(d2, x2, at2(sw, i)));
+          set2(sb, i, __fadd2_rn(at2(sb, i), d2));
+          set2(xh, i, x2);
+        }
+        s1 = t1.x + t1.y;
+        s2 = t2.x + t2.y;
       }
       if (next < last) {
         mean = a.mean[next];
@@ -273,14 +423,18 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
       } else {
         mean = rstd = 0.f;
       }
-      if (!a.dx) continue;
-      Piece<T, N> vr[P];
-      if (a.residual && mine) {
+      if (!kRing && !a.dx) continue;
+      if (!kRing && a.residual && mine) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
           if (live[p]) vr[p].stream(res + row * a.r_stride + p * at.step);
       }
       sum(s1, s2);
+      if constexpr (kRing) {  // (every thread has its pieces: the sum was a barrier)
+        if (threadIdx.x == 0 && row + a.slots < last) ring.fetch(ring.at, row + a.slots);
+        ring.next();
+        if (!a.dx) continue;
+      }
       s1 *= per;
       s2 *= per;
       if (!mine) continue;
@@ -289,9 +443,16 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
         if (!live[p]) continue;
         float o[N], add[N] = {};
         if (a.residual) vr[p].open(add);
+        if constexpr (N == 1) {
+          o[0] = fmaf(r, fmaf(-xh[p], s2, fmaf(d[p], w[p], -s1)), add[0]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          o[i] = fmaf(r, d[p * N + i] * w[p * N + i] - s1 - xh[p * N + i] * s2, add[i]);
+          for (int i = 0; i < N / 2; ++i) {
+            const int j = p * (N / 2) + i;
+            const float2 t = __ffma2_rn(at2(d, j), at2(w, j), both(-s1));
+            set2(o, i, __ffma2_rn(both(r), __ffma2_rn(at2(xh, j), both(-s2), t), at2(add, i)));
+          }
+        }
         put<T, N>(dx + row * h + p * at.step, o);
       }
     }
@@ -348,10 +509,11 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
 // Rows that no block holds: read again for each sum (from L2).  One block a row.
 template <typename T, typename W, int N>
 __global__ void __launch_bounds__(1024) k_norm_wide(NormArgs a) {
-  __shared__ float red[2][2][32];
+  __shared__ __align__(16) Sums red;
   grid_launch_next();
   grid_wait();
-  RowSum<false> sum{red, 32, 0};
+  RowSum<false> sum{&red, 32, 0};
+  sum.init();
   const int64_t h = a.width, step = (int64_t)blockDim.x * N, c0 = (int64_t)threadIdx.x * N;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
@@ -396,10 +558,11 @@ __global__ void __launch_bounds__(1024) k_norm_wide(NormArgs a) {
 
 template <typename T, typename W, int N>
 __global__ void __launch_bounds__(1024) k_norm_wide_dx(NormArgs a) {
-  __shared__ float red[2][2][32];
+  __shared__ __align__(16) Sums red;
   grid_launch_next();
   grid_wait();
-  RowSum<false> sum{red, 32, 0};
+  RowSum<false> sum{&red, 32, 0};
+  sum.init();
   const int64_t h = a.width, step = (int64_t)blockDim.x * N, c0 = (int64_t)threadIdx.x * N;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
@@ -498,24 +661,36 @@ __global__ void __launch_bounds__(1024) k_norm_join(NormArgs a) {
   }
 }
 
-// How rows of this width are held.
+// How rows of this width are held: by lanes of a warp, by a block (`each` elements a
+// thread, `blocks` blocks an SM), or by none.  Forward, 16-bit rows take 32 elements a
+// thread where there are rows enough to fill the GPU: the sums over a row then cost half as
+// much of a thread ([8192, 4096] bf16: 25.5 us against 31; fp32 is bound by HBM, 47
+// against 45).
 struct Form {
   bool warp, wide;
-  int lanes, threads;
+  int lanes, threads, each, blocks;
 };
-Form form_of(int64_t width, int n) {
-  const int64_t pieces = (width + n - 1) / n, threads = (pieces * n + kEach - 1) / kEach;
-  Form f{false, false, 32, 0};
-  if (threads <= 32) {
+Form form_of(int64_t rows, int64_t width, int n, bool backward) {
+  const auto threads_of = [&](int64_t each) { return ((width + n - 1) / n * n + each - 1) / each; };
+  const int64_t t = threads_of(kEach), t2 = threads_of(2 * kEach);
+  Form f{false, false, 32, 0, kEach, 1};
+  if (t <= 32) {
     f.warp = true;
     f.lanes = 1;
-    while (f.lanes < threads) f.lanes *= 2;
+    while (f.lanes < t) f.lanes *= 2;
     f.threads = kSmallBlock;
-  } else if (threads <= kMostThreads) {
-    f.threads = (int)((threads + 31) / 32 * 32);
+    f.blocks = backward ? 4 : 6;
+  } else if (backward || n == 1 ? t <= 512 : (t <= 256 && (n != 8 || rows < 2 * num_sms() || t2 < 64))) {
+    f.threads = (int)((t + 31) / 32 * 32);
+    f.blocks = f.threads > 256 ? 1 : (backward ? 512 : 768) / f.threads;
+  } else if (!backward && n > 1 && t2 <= 512) {
+    f.each = 2 * kEach;
+    f.threads = (int)((t2 + 31) / 32 * 32);
+    f.blocks = 512 / f.threads;
   } else {
     f.wide = true;
     f.threads = 1024;
+    f.blocks = 2;
   }
   return f;
 }
@@ -535,14 +710,14 @@ bool vector_rows(const NormArgs& a) {
 // Parts of the sum over rows: one a resident block (about 512 threads an SM), and
 // no more than kPartRows rows one after another.
 void set_parts(NormArgs* a, int n) {
-  const Form f = form_of(a->width, n);
+  const Form f = form_of(a->rows, a->width, n, true);
   int64_t each, most;
   if (f.wide) {
     const int64_t col_blocks = (a->width + 256ll * n - 1) / (256ll * n);
     most = (8ll * num_sms() + col_blocks - 1) / col_blocks;
     each = 1;
   } else {
-    most = (int64_t)num_sms() * (512 / f.threads);
+    most = (int64_t)num_sms() * f.blocks;
     each = f.warp ? f.threads / f.lanes : 1;  // rows a round
   }
   int64_t rows = (a->rows + most - 1) / most;
@@ -552,21 +727,57 @@ void set_parts(NormArgs* a, int n) {
   a->parts = (a->rows + a->part_rows - 1) / a->part_rows;
 }
 
+// The ring of a block: what fits of `blocks` blocks an SM.
+constexpr int64_t kRingBytes = 208 * 1024;
+size_t set_slots(NormArgs* a, int64_t slot_bytes, int64_t blocks) {
+  const int64_t n = kRingBytes / (blocks < 1 ? 1 : blocks) / slot_bytes;
+  a->slot_bytes = (uint32_t)slot_bytes;
+  a->slots = (int)(n < 1 ? 1 : (n < kMostSlots ? n : kMostSlots));
+  return (size_t)(a->slots * slot_bytes);
+}
+// Shared memory beyond the default (once per device and kernel).
+template <typename F>
+cudaError_t allow(F fn) {
+  static std::mutex mu;
+  static std::vector<std::pair<F, int>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& d : done)
+    if (d.first == fn && d.second == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+  if (e == cudaSuccess) done.emplace_back(fn, dev);
+  return e;
+}
+
 template <typename T, typename W, int N>
-cudaError_t forward(const NormArgs& a, cudaStream_t s) {
-  const Form f = form_of(a.width, N);
+cudaError_t forward(NormArgs a, cudaStream_t s) {
+  const Form f = form_of(a.rows, a.width, N, false);
   const int64_t each = f.warp ? f.threads / f.lanes : 1;
-  const int64_t rounds = (a.rows + each - 1) / each, most = (int64_t)num_sms() * (f.wide ? 2 : 1024 / f.threads);
+  const int64_t rounds = (a.rows + each - 1) / each, most = (int64_t)num_sms() * f.blocks;
   const dim3 grid((unsigned)(rounds < most ? rounds : most)), block((unsigned)f.threads);
   if (f.wide) return launch_early(k_norm_wide<T, W, N>, grid, block, 0, s, a);
-  if (f.warp) return launch_early(k_norm<T, W, N, true>, grid, block, 0, s, a, f.lanes);
-  return launch_early(k_norm<T, W, N, false>, grid, block, 0, s, a, f.lanes);
+  if (f.warp) return launch_early(k_norm<T, W, N, kEach, true, kSmallBlock, 6>, grid, block, 0, s, a, f.lanes);
+  auto fn = k_norm<T, W, N, kEach, false, 256, 3>;
+  if constexpr (N == 1) {
+    if (f.threads > 256) fn = k_norm<T, W, N, kEach, false, 512, 1>;
+  } else if (f.each > kEach) {
+    fn = f.threads > 256 ? k_norm<T, W, N, 2 * kEach, false, 512, 1> : k_norm<T, W, N, 2 * kEach, false, 256, 2>;
+  }
+  size_t smem = 0;
+  cudaError_t e = ops_error_word(&a.err);
+  if (e == cudaSuccess && N > 1) {
+    smem = set_slots(&a, a.width * (int64_t)sizeof(T), f.blocks);
+    e = allow(fn);
+  }
+  return e == cudaSuccess ? launch_early(fn, grid, block, smem, s, a, f.lanes) : e;
 }
 
 template <typename T, typename W, int N>
 cudaError_t backward(NormArgs a, cudaStream_t s) {
   set_parts(&a, N);
-  const Form f = form_of(a.width, N);
+  const Form f = form_of(a.rows, a.width, N, true);
   cudaError_t e = cudaSuccess;
   if (f.wide) {
     const int64_t most = (int64_t)num_sms() * 2;
@@ -576,9 +787,15 @@ cudaError_t backward(NormArgs a, cudaStream_t s) {
     if (e == cudaSuccess && a.part)
       e = launch_early(k_norm_wide_dw<T, N>, dim3((unsigned)(col_blocks * a.parts)), dim3(256), 0, s, a, col_blocks);
   } else {
-    const int64_t most = (int64_t)num_sms() * (512 / f.threads);
+    const int64_t most = (int64_t)num_sms() * f.blocks;
     const dim3 grid((unsigned)(a.parts < most ? a.parts : most)), block((unsigned)f.threads);
-    const size_t smem = f.warp ? sizeof(float) * 2 * a.width * (f.threads / 32) : 0;
+    size_t smem = f.warp ? sizeof(float) * 2 * a.width * (f.threads / 32) : 0;
+    e = ops_error_word(&a.err);
+    if (e == cudaSuccess && !f.warp && N > 1) {
+      smem = set_slots(&a, 3 * a.width * (int64_t)sizeof(T), f.blocks);
+      e = allow(k_norm_backward<T, W, N, false>);
+    }
+    if (e != cudaSuccess) return e;
     e = f.warp ? launch_early(k_norm_backward<T, W, N, true>, grid, block, smem, s, a, f.lanes)
                : launch_early(k_norm_backward<T, W, N, false>, grid, block, smem, s, a, f.lanes);
   }

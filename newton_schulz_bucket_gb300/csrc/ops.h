@@ -150,7 +150,10 @@ struct NormArgs {
   void* dw;                    // nullable
   void* db;                    // nullable
   float* part;                 // nullable: [parts][2][width] sums of dw and db
-  int64_t parts, part_rows;    // set by the launch
+  int64_t parts, part_rows;    // set by the launch, as what follows
+  uint32_t slot_bytes;         // of the ring of rows on their way
+  int32_t slots;
+  int* err;
 };
 int64_t norm_part_rows(int64_t rows, int64_t width);  // most parts that launch_norm_backward uses
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
@@ -187,7 +190,7 @@ struct MxRows {
   uint8_t* values;
   uint8_t* scales;
   void* dst;                   // back: [rows][cols]
-  int64_t col_blocks;          // set by the launch
+  uint32_t col_blocks;         // set by the launch
   int log_across;
   bool vec;
 };

@@ -59,6 +59,10 @@ muon_status_t check_product(const char* what, const muon_mx_linear_args* a) {
   const int64_t mats = a->experts ? a->experts : 1;
   if ((a->rows / 64 + mats) * ((a->out + 255) / 256) > kMaxBlocks)
     return fail(MUON_ERR_UNSUPPORTED, "%s: too many tiles for one launch", what);
+  // token rows' ordered scales are placed in words of 32 bits
+  const int tile = mx_tile_rows(a->rows, a->experts, a->out);
+  if (mx_token_slots(a->rows, a->experts, tile) * mx_parts(a->in) * mx_token_blocks(tile) >= (0xffffffffll >> 7))
+    return fail(MUON_ERR_UNSUPPORTED, "%s: [%lld, %lld] has too many scales", what, (long long)a->rows, (long long)a->in);
   if (mx_prepare_blocks(a->rows, a->in, a->out, mats) > kMaxBlocks)
     return fail(MUON_ERR_UNSUPPORTED, "%s: too many blocks for one launch", what);
   return MUON_OK;
