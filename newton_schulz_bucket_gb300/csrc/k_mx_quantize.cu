@@ -41,7 +41,8 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = i < n ? p[i] : from_f32<T>(0.f);
   }
-  // The largest magnitude, as bits of fp32; a NaN comes before all.
+  // The largest magnitude as the type's bits, a NaN above all (they compare as
+  // integers).
   __device__ __forceinline__ uint32_t top() const {
     if constexpr (sizeof(T) == 4) {
       uint32_t m = 0;
@@ -51,10 +52,16 @@ struct Eight {
     } else {
       using Pair = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
       const Pair* h = reinterpret_cast<const Pair*>(w);
-      Pair m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float_as_uint(__bfloat162float(__hmax_nan(m.x, m.y)));
-      else return __float_as_uint(__half2float(__hmax_nan(m.x, m.y)));
+      const Pair m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+      const T one = __hmax_nan(m.x, m.y);
+      return *reinterpret_cast<const uint16_t*>(&one);
     }
+  }
+  // The scale of a block whose largest magnitude has these bits.
+  static __device__ __forceinline__ uint32_t scale(uint32_t top) {
+    if constexpr (sizeof(T) == 4) return mx_scale(top);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value) return mx_scale(top << 16);
+    else return mx_scale(__float_as_uint(__half2float(__ushort_as_half((uint16_t)top))));
   }
   __device__ __forceinline__ uint32_t packed(float inverse) const {
     float f[8];
@@ -112,12 +119,29 @@ __device__ __forceinline__ void quantize_rows(const MxRows& q, const Spot& at, M
   meanwhile();
   uint32_t* out = reinterpret_cast<uint32_t*>(q.values) + at.row * kb * 4 + at.piece;
   const int64_t out_step = at.by * kb * 4;
+  uint32_t top[kRows];
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {  // four lanes share a block
-    uint32_t top = v[k].top();
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t s = mx_scale(top);
+  for (int k = 0; k < kRows; ++k) top[k] = v[k].top();
+  // four lanes share a block; two rows of 16 bits go through the shuffles together
+#pragma unroll
+  for (int k = 0; k < kRows; k += 2) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = k; j < k + 2; ++j) {
+        top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
+        top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
+      }
+    } else {
+      uint32_t t = __byte_perm(top[k], top[k + 1], 0x5410);
+      asm("max.u16x2 %0, %0, %1;" : "+r"(t) : "r"(__shfl_xor_sync(0xffffffffu, t, 1)));
+      asm("max.u16x2 %0, %0, %1;" : "+r"(t) : "r"(__shfl_xor_sync(0xffffffffu, t, 2)));
+      top[k] = t & 0xffffu;
+      top[k + 1] = t >> 16;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const uint32_t s = Eight<T>::scale(top[k]);
     const bool live = k * at.by < left;
     if (there && live) out[k * out_step] = v[k].packed(mx_inverse(s));
     give(k, at.piece / 4, s, live);
@@ -167,10 +191,10 @@ __device__ __forceinline__ uint32_t token_scales(const MxPrepare& q, int row, ui
 // What a product starts from, in one launch: the token rows, then the weights' scales
 // (of the matrices that any row reaches) through shared memory, 128 rows x 64 words.
 constexpr int kWords = 16;
-// kWide: rows of at least a warp's 256 columns.
-template <typename T, bool kWide>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
   __shared__ uint32_t words[128][kWords + 1];
+  __shared__ uint32_t place[kThreads / 4 * kRowsOf<T>];
   grid_wait();
   // only now: the product reads the weights before it waits for this launch
   grid_launch_next();
@@ -179,33 +203,25 @@ __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
     constexpr int kRows = kRowsOf<T>;
     const uint32_t part_words = 128 * mx_token_blocks(q.tile_rows), slot_words = (uint32_t)parts * part_words;
     const Spot at = spot<kRows>(q.x, blockIdx.x);
-    // lanes of a warp that share a row (w of them) find the places of its kRows rows
-    const int across = kWide ? 32 : 1 << q.x.log_across, own = threadIdx.x & (across - 1);
-    uint32_t place[2] = {kNowhere, kNowhere};  // of rows own and own + across
-    const auto find = [&] {  // (while the rows are on their way)
-#pragma unroll
-      for (int h = 0; h < (kWide ? 1 : 2); ++h) {
-        const int64_t row = at.row + (own + h * across) * at.by;
-        if (own + h * across < kRows && row < q.x.rows) place[h] = token_scales(q, (int)row, slot_words);
-      }
+    // the block's rows' places, while the rows are on their way (each warp for itself took
+    // half of the instructions of the whole kernel)
+    const int rows = (kThreads >> q.x.log_across) * kRows, across = 1 << q.x.log_across;
+    const int64_t row0 = at.row - (threadIdx.x >> q.x.log_across);
+    const auto find = [&] {
+      for (int i = threadIdx.x; i < rows; i += kThreads)
+        place[i] = row0 + i < q.x.rows ? token_scales(q, (int)(row0 + i), slot_words) : kNowhere;
+      __syncthreads();
     };
+    // four lanes store the scales of 128 steps side by side, zeros behind the row's end
+    const int last = across >= 16 ? (int)parts * 4 : (int)kb;
+    const uint32_t* mine = place + (at.row - row0);
     quantize_rows<T, false>(q.x, at, find, [&](int k, int b, uint32_t s, bool) {
-      // the scales of 128 steps in one store where a warp's lanes hold them (zeros behind
-      // the row's end)
-      const uint32_t to = kWide ? __shfl_sync(0xffffffffu, place[0], k)
-                                : __shfl_sync(0xffffffffu, k < across ? place[0] : place[1], k & (across - 1), across);
-      const uint32_t word = to + (uint32_t)(b >> 2) * part_words;
-      if (kWide || across == 16) {
-        uint32_t v = s << (8 * (b & 3));
-        v |= __shfl_xor_sync(0xffffffffu, v, 4);
-        v |= __shfl_xor_sync(0xffffffffu, v, 8);
-        if (to != kNowhere && b < (int)kb && (threadIdx.x & 15) == 0) reinterpret_cast<uint32_t*>(q.x.scales)[word] = v;
-      } else if (to != kNowhere && b < (int)kb && (threadIdx.x & 3) == 0) {  // one part
-        uint8_t* bytes = q.x.scales + (int64_t)word * 4;
-        bytes[b] = (uint8_t)s;
-        if (b + 1 == (int)kb)
-          for (int z = b + 1; z < 4; ++z) bytes[z] = 0;
-      }
+      const uint32_t to = mine[k * at.by];
+      if (to == kNowhere || (threadIdx.x & 3) != 0 || b >= last) return;
+      uint8_t* word = q.x.scales + (int64_t)(to + (uint32_t)(b >> 2) * part_words) * 4;
+      word[b & 3] = (uint8_t)s;
+      if (across < 16 && b + 1 == (int)kb)  // no lanes there
+        for (int z = b + 1; z < 4; ++z) word[z] = 0;
     });
     return;
   }
@@ -383,8 +399,7 @@ cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
   q.x.vec = vector_rows<T>(q.x);
   q.w_parts = (mx_parts(q.x.cols) + kWords - 1) / kWords;
   const int64_t grid = q.x_blocks + q.w_parts * ((q.out + 127) / 128) * q.mats;
-  return q.x.log_across >= 5 ? launch_early(k_mx_prepare<T, true>, dim3((unsigned)grid), dim3(kThreads), 0, s, q)
-                             : launch_early(k_mx_prepare<T, false>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
+  return launch_early(k_mx_prepare<T>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
 }
 
 }  // namespace

@@ -161,3 +161,93 @@ def combine_backward(dy, ys, slot, weights):
                 dys[slot[t, j]] = float(weights[t, j]) * dy[t]
                 dwts[t, j] = ys[slot[t, j]] @ dy[t]
     return dys, dwts
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5):
+    """(y, mean, rstd)"""
+    mean = x.mean(axis=1)
+    d = x - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(axis=1) + eps)
+    y = d * rstd[:, None]
+    if w is not None:
+        y = y * w
+    return (y if b is None else y + b), mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, w=None, r=None):
+    """(dx, dw, db)"""
+    xh = (x - mean[:, None]) * rstd[:, None]
+    g = dy if w is None else dy * w
+    dx = rstd[:, None] * (g - g.mean(axis=1, keepdims=True) - xh * (g * xh).mean(axis=1, keepdims=True))
+    return (dx if r is None else dx + r), (dy * xh).sum(axis=0), dy.sum(axis=0)
+
+
+def balance_loss(logits, indices, coef=1.0):
+    """(loss, counts, live)"""
+    tokens, experts = logits.shape
+    counts = np.zeros(experts, dtype=np.int32)
+    for e in indices.reshape(-1):
+        if 0 <= e < experts:
+            counts[e] += 1
+    live, mass = 0, np.zeros(experts)
+    for t in range(tokens):
+        open_ = logits[t] != -math.inf
+        if open_.any():
+            live += 1
+            p = np.exp(logits[t][open_] - logits[t][open_].max())
+            mass[open_] += p / p.sum()
+    share = counts / max(int(counts.sum()), 1)
+    return coef * experts * float((share * mass).sum()) / max(live, 1), counts, live
+
+
+def balance_loss_backward(dloss, logits, counts, live, coef=1.0, r=None):
+    out = np.zeros(logits.shape) if r is None else np.array(r, dtype=np.float64)
+    share = counts / max(int(counts.sum()), 1)
+    for t in range(logits.shape[0]):
+        open_ = logits[t] != -math.inf
+        if not open_.any():
+            continue
+        p = np.exp(logits[t][open_] - logits[t][open_].max())
+        p /= p.sum()
+        f = share[open_]
+        out[t][open_] += dloss * coef * logits.shape[1] / max(live, 1) * p * (f - (p * f).sum())
+    return out
+
+
+MX_GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx_round(x):
+    """(values of x as microscaled 4-bit numbers, scale bytes): blocks of 32 along the
+    last axis, each scaled by the power of two at or below its largest magnitude, over
+    4, and rounded to the nearest of MX_GRID, ties to the even code."""
+    *lead, n = x.shape
+    blocks = -(-n // 32)
+    rows = np.zeros((int(np.prod(lead, dtype=np.int64)), 32 * blocks))
+    rows[:, :n] = np.asarray(x, dtype=np.float64).reshape(-1, n)
+    rows = rows.reshape(-1, blocks, 32)
+    scales = np.zeros(rows.shape[:2], dtype=np.uint8)
+    out = np.zeros_like(rows)
+    for i in range(rows.shape[0]):
+        for b in range(blocks):
+            block = rows[i, b]
+            if not np.isfinite(block).all():
+                scales[i, b], out[i, b] = 255, math.nan
+                continue
+            top = float(np.abs(block).max())
+            e = -127 if top == 0.0 else min(max(math.frexp(top)[1] - 1 - 2, -127), 127)
+            scales[i, b] = e + 127
+            a = np.abs(block) / 2.0 ** e
+            gap = np.abs(a[:, None] - MX_GRID)
+            near = gap == gap.min(axis=1, keepdims=True)
+            code = np.where(near.sum(axis=1) > 1, 2 * (near.argmax(axis=1) // 2 + near.argmax(axis=1) % 2), near.argmax(axis=1))
+            out[i, b] = np.sign(block) * MX_GRID[code] * 2.0 ** e
+    return out.reshape(-1, 32 * blocks)[:, :n].reshape(*lead, n), scales.reshape(*lead, blocks)
+
+
+def mx_held(values, scales, n):
+    """The numbers that packed bytes [.., 16 * blocks] and scale bytes [.., blocks] stand for."""
+    v = np.stack((values & 15, values >> 4), axis=-1).reshape(*values.shape[:-1], -1)
+    x = np.where(v & 8, -1.0, 1.0) * MX_GRID[v & 7]
+    factor = np.where(scales == 255, math.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return (x * np.repeat(factor, 32, axis=-1))[..., :n]
