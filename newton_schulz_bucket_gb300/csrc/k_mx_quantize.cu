@@ -84,7 +84,7 @@ struct Spot {
 template <int kRows>
 __device__ __forceinline__ Spot spot(const MxRows& q, uint32_t block) {
   const int across = 1 << q.log_across, down = kThreads >> q.log_across;
-  const uint32_t rb = block / q.col_blocks, cb = block - rb * q.col_blocks;
+  const uint32_t rb = block / q.col_blocks, cb = block - rb * q.col_blocks;  // (the first of its column blocks)
   return {(int64_t)rb * down * kRows + (threadIdx.x >> q.log_across),
           (int)cb * across + ((int)threadIdx.x & (across - 1)), down};
 }
@@ -215,46 +215,54 @@ __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
     // four lanes store the scales of 128 steps side by side, zeros behind the row's end
     const int last = across >= 16 ? (int)parts * 4 : (int)kb;
     const uint32_t* mine = place + (at.row - row0);
-    quantize_rows<T, false>(q.x, at, find, [&](int k, int b, uint32_t s, bool) {
+    const auto give = [&](int k, int b, uint32_t s, bool) {
       const uint32_t to = mine[k * at.by];
       if (to == kNowhere || (threadIdx.x & 3) != 0 || b >= last) return;
       uint8_t* word = q.x.scales + (int64_t)(to + (uint32_t)(b >> 2) * part_words) * 4;
       word[b & 3] = (uint8_t)s;
       if (across < 16 && b + 1 == (int)kb)  // no lanes there
         for (int z = b + 1; z < 4; ++z) word[z] = 0;
-    });
+    };
+    quantize_rows<T, false>(q.x, at, find, give);
+    // (enough rows to fill the GPU: one block takes all columns of its own)
+    for (Spot next = at; next.piece + across * (int)q.x.col_blocks < across * q.x.col_total;) {
+      next.piece += across * (int)q.x.col_blocks;
+      quantize_rows<T, false>(q.x, next, [] {}, give);
+    }
     return;
   }
   const uint32_t j = blockIdx.x - (uint32_t)q.x_blocks, runs = (uint32_t)q.w_parts;
   const uint32_t tiles = (uint32_t)((q.out + 127) / 128), tile = j / runs;
-  const int64_t run = j - tile * runs, mat = tile / tiles, row0 = (int64_t)(tile - mat * tiles) * 128;
+  const int64_t mat = tile / tiles, row0 = (int64_t)(tile - mat * tiles) * 128;
   if (q.experts && clamped(q, (int)mat) >= clamped(q, (int)mat + 1)) return;
   const uint8_t* src = q.w_scales + (mat * q.out + row0) * kb;
   const int rows = (int)min((int64_t)128, q.out - row0);
-  const int64_t w0 = run * kWords;
-  const int n = (int)min((int64_t)kWords, parts - w0);
   const bool vec = kb % 4 == 0 && (reinterpret_cast<uintptr_t>(q.w_scales) & 3) == 0;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < 128 * kWords; i += kThreads) {
-    const int r = i / kWords, w = i % kWords;
-    uint32_t v = 0;
-    if (r < rows && w < n) {
-      const uint8_t* p = src + r * kb + (w0 + w) * 4;
-      if (vec) {
-        v = *reinterpret_cast<const uint32_t*>(p);
-      } else {
+  for (int64_t w0 = (int64_t)(j - tile * runs) * kWords; w0 < parts; w0 += runs * kWords) {
+    const int n = (int)min((int64_t)kWords, parts - w0);
+    __syncthreads();  // the words of the round before are stored
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((w0 + w) * 4 + k < kb) v |= (uint32_t)p[k] << (8 * k);
+    for (int i = threadIdx.x; i < 128 * kWords; i += kThreads) {
+      const int r = i / kWords, w = i % kWords;
+      uint32_t v = 0;
+      if (r < rows && w < n) {
+        const uint8_t* p = src + r * kb + (w0 + w) * 4;
+        if (vec) {
+          v = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((w0 + w) * 4 + k < kb) v |= (uint32_t)p[k] << (8 * k);
+        }
       }
+      words[r][w] = v;
     }
-    words[r][w] = v;
-  }
-  __syncthreads();
-  uint4* out = reinterpret_cast<uint4*>(q.w_ordered + ((mat * tiles + row0 / 128) * parts + w0) * 512);
-  for (int i = threadIdx.x; i < n * 32; i += kThreads) {
-    const int w = i >> 5, lane = i & 31;
-    out[i] = make_uint4(words[lane][w], words[32 + lane][w], words[64 + lane][w], words[96 + lane][w]);
+    __syncthreads();
+    uint4* out = reinterpret_cast<uint4*>(q.w_ordered + ((mat * tiles + row0 / 128) * parts + w0) * 512);
+    for (int i = threadIdx.x; i < n * 32; i += kThreads) {
+      const int w = i >> 5, lane = i & 31;
+      out[i] = make_uint4(words[lane][w], words[32 + lane][w], words[64 + lane][w], words[96 + lane][w]);
+    }
   }
 }
 
@@ -327,33 +335,40 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(MxRows q) {
   constexpr int kRows = kBackRows;
   const Spot at = spot<kRows>(q, blockIdx.x);
   const int64_t col = (int64_t)at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
-  if (col >= q.cols) return;
-  uint32_t v[kRows], s[kRows];
+  // lanes of a warp that share a row
+  const int w = min(1 << q.log_across, 32), own = threadIdx.x & (w - 1);
+  uint32_t v[kRows] = {}, s[kRows] = {};
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = at.row + k * at.by;
-    if (row >= q.rows) break;
+    if (row >= q.rows || col >= q.cols) break;
     v[k] = *reinterpret_cast<const uint32_t*>(q.values + (row * kb * 4 + at.piece) * 4);
     s[k] = q.scales[row * kb + at.piece / 4];
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = at.row + k * at.by;
-    if (row >= q.rows) break;
-    float f[8];
-    mx_unpack8(v[k], mx_value(s[k]), f);
-    T* out = static_cast<T*>(q.dst) + row * q.cols + col;
+    if (q.vec && (row >= q.rows || col >= q.cols)) break;
     if (q.vec) {  // (then cols is a multiple of 8)
+      float f[8];
+      mx_unpack8(v[k], mx_value(s[k]), f);
+      T* out = static_cast<T*>(q.dst) + row * q.cols + col;
       alignas(16) T h[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = from_f32<T>(f[i]);
 #pragma unroll
       for (int i = 0; i < (int)sizeof(T) / 2; ++i)
         reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(h)[i];
-    } else {
+    } else {  // element by element, neighbouring ones in neighbouring lanes
+      T* out = static_cast<T*>(q.dst) + row * q.cols + (col - own * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < q.cols) out[i] = from_f32<T>(f[i]);
+      for (int j = 0; j < 8; ++j) {
+        const int i = j * w + own;  // of the w pieces that these lanes hold
+        const uint32_t from = __shfl_sync(0xffffffffu, v[k], i >> 3, w), by = __shfl_sync(0xffffffffu, s[k], i >> 3, w);
+        float f[8];
+        mx_unpack8(from >> (4 * (i & 7)), mx_value(by), f);
+        if (row < q.rows && col - own * 8 + i < q.cols) out[i] = from_f32<T>(f[0]);
+      }
     }
   }
 }
@@ -363,7 +378,8 @@ int64_t shape_rows(MxRows* q, int each) {
   const int64_t pieces = 4 * mx_blocks_of(q->cols);
   q->log_across = 2;
   while (q->log_across < 8 && (1 << q->log_across) < pieces) ++q->log_across;
-  q->col_blocks = (uint32_t)(pieces + (1 << q->log_across) - 1) >> q->log_across;
+  q->col_blocks = (uint32_t)((pieces + (1 << q->log_across) - 1) >> q->log_across);
+  q->col_total = (int32_t)q->col_blocks;
   const int64_t down = (int64_t)(kThreads >> q->log_across) * each;
   return (q->rows + down - 1) / down * q->col_blocks;
 }
@@ -397,8 +413,15 @@ template <typename T>
 cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
   q.x_blocks = shape_rows(&q.x, kRowsOf<T>);
   q.x.vec = vector_rows<T>(q.x);
-  q.w_parts = (mx_parts(q.x.cols) + kWords - 1) / kWords;
-  const int64_t grid = q.x_blocks + q.w_parts * ((q.out + 127) / 128) * q.mats;
+  // a block takes all columns of its rows, or all parts of its 128 features, where that
+  // leaves blocks enough
+  if (q.x_blocks / q.x.col_blocks >= 4 * num_sms()) {
+    q.x_blocks /= q.x.col_blocks;
+    q.x.col_blocks = 1;
+  }
+  const int64_t features = (q.out + 127) / 128 * q.mats;
+  q.w_parts = features >= 2 * num_sms() ? 1 : (mx_parts(q.x.cols) + kWords - 1) / kWords;
+  const int64_t grid = q.x_blocks + q.w_parts * features;
   return launch_early(k_mx_prepare<T>, dim3((unsigned)grid), dim3(kThreads), 0, s, q);
 }
 

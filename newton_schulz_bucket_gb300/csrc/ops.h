@@ -190,7 +190,8 @@ struct MxRows {
   uint8_t* values;
   uint8_t* scales;
   void* dst;                   // back: [rows][cols]
-  uint32_t col_blocks;         // set by the launch
+  uint32_t col_blocks;         // set by the launch: column blocks of the grid, and of a row
+  int32_t col_total;
   int log_across;
   bool vec;
 };

@@ -35,7 +35,8 @@ def _check(logits, idx, coef=1.0, residual=None):
     RES = None if residual is None else to64(residual)
     D = ref.balance_loss_backward(float(dloss), L, COUNTS, LIVE, coef, RES)
     open_ = np.isfinite(L)
-    p = np.where(open_, np.exp(np.where(open_, L, 0) - np.where(open_, L, -1e300).max(1, keepdims=True)), 0)
+    m = np.where(open_, L, -1e300)
+    p = np.where(open_, np.exp(m - m.max(1, keepdims=True)), 0)
     p /= np.maximum(p.sum(1, keepdims=True), 1e-300)
     share = COUNTS / max(int(COUNTS.sum()), 1)
     size = abs(float(dloss) * coef) * L.shape[1] / max(LIVE, 1) * p * (share + (p * share).sum(1, keepdims=True))
