@@ -13,8 +13,6 @@
 // parts in a fixed order.  No atomics: the same bits every time.
 #include <mutex>
 #include <type_traits>
-#include <utility>
-#include <vector>
 
 #include "common.cuh"
 #include "mbarrier.cuh"
@@ -735,19 +733,29 @@ size_t set_slots(NormArgs* a, int64_t slot_bytes, int64_t blocks) {
   a->slots = (int)(n < 1 ? 1 : (n < kMostSlots ? n : kMostSlots));
   return (size_t)(a->slots * slot_bytes);
 }
-// Shared memory beyond the default (once per device and kernel).
+// Shared memory beyond the default (once per device and kernel; kernels of one type
+// share a table).
 template <typename F>
 cudaError_t allow(F fn) {
   static std::mutex mu;
-  static std::vector<std::pair<F, int>> done;
+  static struct {
+    F fn;
+    bool ready[64];
+  } table[4] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  for (const auto& d : done)
-    if (d.first == fn && d.second == dev) return cudaSuccess;
+  bool* ready = nullptr;
+  for (auto& t : table) {
+    if (t.fn == nullptr) t.fn = fn;
+    if (t.fn != fn) continue;
+    if (dev < 64) ready = &t.ready[dev];
+    break;
+  }
+  if (ready && *ready) return cudaSuccess;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
-  if (e == cudaSuccess) done.emplace_back(fn, dev);
+  if (e == cudaSuccess && ready) *ready = true;
   return e;
 }
 
