@@ -540,12 +540,12 @@ def balance_loss(logits, indices, coef=1.0):
     top_k = indices.shape[1]
     ip = _contiguous(indices, "indices", dev, _I32, (tokens, top_k))
     size = _scratch_size("muon_balance_loss_workspace", tokens, _int32(experts))
-    ws = _empty(size, dtype=torch.uint8, device=dev)
+    ws = _empty(size, dtype=torch.uint8, device=dev) if size else None
     loss, live = _empty((), dtype=_F32, device=dev), _empty((), dtype=_I32, device=dev)
     counts = _empty(experts, dtype=_I32, device=dev)
     st = _c.load().muon_balance_loss(code, tokens, experts, _int32(top_k), coef, logits.data_ptr(),
                                      _rows(logits, "logits"), ip, loss.data_ptr(), counts.data_ptr(), live.data_ptr(),
-                                     ws.data_ptr(), size, stream)
+                                     ws.data_ptr() if size else None, size, stream)
     if st:
         _c.check(st, "muon_balance_loss")
     return loss, counts, live

@@ -47,7 +47,8 @@ def _check(logits, idx, coef=1.0, residual=None):
 
 
 CASES = [(1, 1, 1), (1, 64, 8), (5, 2, 2), (9, 8, 4), (33, 31, 32), (100, 33, 7), (257, 64, 8), (64, 65, 1), (50, 128, 6),
-         (21, 200, 8), (40, 256, 8), (17, 257, 16), (30, 512, 9), (9, 600, 9), (7, 1024, 32), (3, 1000, 2), (5000, 16, 2)]
+         (21, 200, 8), (40, 256, 8), (17, 257, 16), (30, 512, 9), (9, 600, 9), (7, 1024, 32), (3, 1000, 2), (5000, 16, 2),
+         (4096, 256, 4), (4097, 256, 4), (70000, 16, 2), (2000, 600, 3)]  # one cluster's, and just above
 
 
 @pytest.mark.parametrize("dtype", list(DT))

@@ -54,12 +54,13 @@ def test_layer_norm_refuses(lib):
 
 def test_balance_loss_refuses(lib):
     n = C.c_size_t()
-    assert lib.muon_balance_loss_workspace(100, 64, C.byref(n)) == OK and n.value > 0
+    assert lib.muon_balance_loss_workspace(100, 64, C.byref(n)) == OK and n.value == 0  # few: one launch, no scratch
+    assert lib.muon_balance_loss_workspace(100000, 64, C.byref(n)) == OK and n.value > 0
     for t, e in ((-1, 64), (4, 0), (4, 1025)):
         assert lib.muon_balance_loss_workspace(t, e, C.byref(n)) == INVALID
     assert lib.muon_balance_loss_workspace(4, 16, None) == INVALID
-    lib.muon_balance_loss_workspace(4, 16, C.byref(n))
-    good = [0, 4, 16, 3, 1.0, P, 16, P, P, P, P, P, n.value, None]
+    lib.muon_balance_loss_workspace(100000, 16, C.byref(n))
+    good = [0, 100000, 16, 3, 1.0, P, 16, P, P, P, P, P, n.value, None]
     _refuses(lib.muon_balance_loss, good,
              [(0, 5), (1, -1), (2, 0), (3, 0), (3, 17), (4, float("nan")), (5, None), (6, 15), (7, None), (8, None),
               (9, None), (10, None), (11, None), (11, P + 8), (12, n.value - 1)])
