@@ -306,7 +306,7 @@ typedef struct {
   const void* residual;
   const int32_t* offsets;
   void* y;             /* contiguous [rows, out]                              */
-  void* workspace;     /* the rounded rows, and scales in the order of the MMAs */
+  void* workspace;     /* the rounded rows, and scales in the order of the MMAs (none for few rows) */
   size_t workspace_bytes;
 } muon_mx_linear_args;
 

@@ -15,9 +15,14 @@
 // Tiles are those of k_linear_tc.cu's rows form: a CTA pair computes 256 features x up
 // to 192 tokens (two accumulators of 192 columns and 5 x 24 columns of scales fill
 // TMEM), each CTA stages its 128 rows of weights and its half of the tokens, 256 steps a
-// stage.  The bytes in flight set the pace: about 3900 cycles pass from a stage's release to
-// its next use, so that 5 stages gave 790 cycles each.  Up to 64 rows of one matrix take the form of k_linear_few.cu: 128 features a
-// cluster of up to eight CTAs that share the sum.
+// stage.  Waits, scale copies, MMAs and commits are issued by three warps: in one they
+// took 800 cycles a stage, where the MMAs take 384.  [8192 x 8192] x [8192, 8192] 196 us with
+// the rounding (5600 TFLOP/s): the tensor pipe is 82% busy and the clock at 1.58 GHz, under
+// the power cap.
+//
+// Up to 64 rows of one matrix take the form of k_linear_few.cu: 128 features a cluster of
+// up to eight CTAs that share the sum.  Up to 16 of them need no launch before: the warps
+// that wait for the sum round the rows and order the scales meanwhile.
 #include <cuda.h>
 
 #include <mutex>
@@ -373,6 +378,10 @@ constexpr int kMaxShares = 8;
 static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct FewArgs {
+  const void* x;            // with kOwn: the rows, and the weights' scales as they are held
+  int64_t x_stride;
+  const uint8_t* w_scales;
+  int in, x_vec;
   int rows, M, K;           // token rows, features, length of the sum
   int cols;                 // columns of an MMA: rows in steps of 16
   int stages;
@@ -399,6 +408,57 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   return n;
 }
 
+// What one of the four warps puts into a stage itself (kOwn): the scales of 32 weight
+// rows, and of the 16 token rows every fourth, 256 steps each, eight a lane.
+template <typename T>
+struct OwnStage {
+  uint2 w;
+  Eight<T> x[4];
+  __device__ __forceinline__ void fetch(const FewArgs& p, int m0, int warp, int lane, int k) {
+    const int kb = p.K / kMxBlock, at = k / kMxBlock, row = m0 + 32 * warp + lane;
+    w = make_uint2(0, 0);
+    if (row < p.M) {
+      const uint8_t* q = p.w_scales + (int64_t)row * kb + at;
+      if (at + 8 <= kb && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
+        w = *reinterpret_cast<const uint2*>(q);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i < kb) (i < 4 ? w.x : w.y) |= (uint32_t)q[i] << (8 * (i & 3));
+      }
+    }
+    const int col = k + 8 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = warp + 4 * i;
+      x[i].zero();
+      if (t >= p.rows || col >= p.in) continue;
+      const T* src = static_cast<const T*>(p.x) + t * p.x_stride + col;
+      if (p.x_vec && col + 8 <= p.in) x[i].fetch(src);
+      else x[i].fetch_some(src, p.in - col);
+    }
+  }
+  __device__ __forceinline__ void put(const FewArgs& p, uint8_t* rows, uint8_t* sa, uint8_t* sb, int warp, int lane) const {
+    *reinterpret_cast<uint32_t*>(sa + lane * 16 + warp * 4) = w.x;
+    *reinterpret_cast<uint32_t*>(sa + kScaleBlock + lane * 16 + warp * 4) = w.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = warp + 4 * i, block = lane >> 2;
+      if (t >= p.rows) break;  // (the same for the warp; columns of no token take what is there)
+      uint32_t top = x[i].top();
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t s = Eight<T>::scale(top);
+      // (the copies' 128-byte swizzle)
+      *reinterpret_cast<uint32_t*>(rows + t * 128 + ((block ^ (t & 7)) << 4) + (lane & 3) * 4) = x[i].packed(mx_inverse(s));
+      if ((lane & 3) == 0) sb[(block >> 2) * kScaleBlock + t * 16 + (block & 3)] = (uint8_t)s;
+    }
+  }
+};
+
+// kOwn (up to 16 rows): no launch before this one has rounded the rows or ordered the
+// scales.
+template <bool kOwn, typename T>
 __global__ void __launch_bounds__(kFewThreads, 2)
     k_mx_few(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
              const __grid_constant__ ScaleMaps scales, const __grid_constant__ FewArgs p) {
@@ -417,12 +477,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t sa_at = kWeights + (uint32_t)p.cols * kRowBytes, sb_at = sa_at + kScaleA;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    for (int s = 0; s < p.stages; ++s) { mbar_init(full(s), kOwn ? 5 : 1); mbar_init(empty(s), 1); }
     mbar_init(all, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&mapW) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapX) : "memory");
+    if (!kOwn) asm volatile("prefetch.tensormap [%0];" ::"l"(&mapX) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
@@ -435,7 +495,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_launch_next();
-  if (warp != 0) grid_wait();  // (the producer's weights come early, as in k_mx_tiles)
+  if (kOwn || warp != 0) grid_wait();  // (the producer's weights come early, as in k_mx_tiles)
 
   const int blocks = (p.K + kStep - 1) / kStep;  // blocks * shares stays below 2^31
   const int k0 = blocks * rank / shares * kStep;
@@ -445,21 +505,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
-    int early = min(p.stages, (k1 - k0 + kStep - 1) / kStep);
-    if (elect_lane())
+    int early = kOwn ? 0 : min(p.stages, (k1 - k0 + kStep - 1) / kStep);
+    if (!kOwn && elect_lane())
       for (int i = 0; i < early; ++i)
         tma_load_3d(ring + i * p.stage_bytes, &mapW, full(i), (k0 + i * kStep) / 4, m0, 0);
     __syncwarp();
-    grid_wait();
+    if (!kOwn) grid_wait();
     for (int k = k0; k < k1; k += kStep) {
       if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 4096))) break;
       if (elect_lane()) {
         const uint32_t sw = ring + s * p.stage_bytes;
-        mbar_expect_tx(full(s), p.stage_bytes);
+        mbar_expect_tx(full(s), kOwn ? kWeights : p.stage_bytes);
         if (early == 0) tma_load_3d(sw, &mapW, full(s), k / 4, m0, 0);
-        tma_load_3d(sw + kWeights, &mapX, full(s), k / 4, 0, 0);
-        tma_load_3d(sw + sa_at, &scales.w, full(s), 0, k / 128, m0 / 128);
-        tma_load_3d(sw + sb_at, &scales.x, full(s), 0, k / 128, 0);
+        if constexpr (!kOwn) {
+          tma_load_3d(sw + kWeights, &mapX, full(s), k / 4, 0, 0);
+          tma_load_3d(sw + sa_at, &scales.w, full(s), 0, k / 128, m0 / 128);
+          tma_load_3d(sw + sb_at, &scales.x, full(s), 0, k / 128, 0);
+        }
       }
       __syncwarp();
       if (early) --early;
@@ -492,6 +554,30 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncwarp();
     volatile int keep_waiting = 0;
     mbar_wait(all, 0, &keep_waiting, p.err, 256);  // every MMA is done before the ring is reused
+  } else if constexpr (kOwn) {  // ---- rows and scales ----
+    constexpr int kSets = 2;  // one is put into its stage while the other's loads are under way
+    OwnStage<T> set[kSets];
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      if (k0 + i * kStep < k1) set[i].fetch(p, m0, warp - 2, lane, k0 + i * kStep);
+    for (int k = k0; ok && k < k1; k += kSets * kStep) {
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        const int at = k + i * kStep;
+        if (!ok || at >= k1) continue;
+        if (!(ok = mbar_wait(empty(s), ph, abort_flag, p.err, 16384))) continue;
+        uint8_t* stage = smem + s * p.stage_bytes;
+        set[i].put(p, stage + kWeights, stage + sa_at, stage + sb_at, warp - 2, lane);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(s));
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+        if (at + kSets * kStep < k1) set[i].fetch(p, m0, warp - 2, lane, at + kSets * kStep);
+      }
+    }
   }
   // every copy has landed and been read, so the ring can take the partial sums:
   // [token][128 features]
@@ -584,10 +670,12 @@ cudaError_t encode_scales(ScaleMaps* m, const MxProduct& p, int64_t w_blocks, in
   return e;
 }
 
+template <bool kOwn, typename T>
 cudaError_t run_few(const MxProduct& p, cudaStream_t s) {
   static bool ready[64] = {};
   static std::mutex mu;
-  cudaError_t e = prepare(k_mx_few, kFewSmem, ready, mu);
+  auto fn = k_mx_few<kOwn, T>;
+  cudaError_t e = prepare(fn, kFewSmem, ready, mu);
   if (e != cudaSuccess) return e;
   const int64_t kb = mx_blocks_of(p.in);
   FewArgs a{};
@@ -599,17 +687,25 @@ cudaError_t run_few(const MxProduct& p, cudaStream_t s) {
   a.type = p.dtype; a.act = p.act; a.D = p.y; a.bias = p.bias; a.residual = p.residual; a.r_m = p.r_stride;
   a.err = p.err;
   const int tiles = (a.M + 127) / 128, blocks = (a.K + kStep - 1) / kStep, places = 2 * num_sms();
-  CUtensorMap mw, mx;
-  ScaleMaps ms;
+  CUtensorMap mw, mx{};
+  ScaleMaps ms{};
   e = encode(&mw, p.w_values, kb, p.out, 1, 128);
-  if (e == cudaSuccess) e = encode(&mx, p.x_values, kb, p.rows, 1, (uint32_t)a.cols);
-  if (e == cudaSuccess) e = encode_scales(&ms, p, tiles, 1, 1);
+  if (kOwn) {
+    a.x = p.x;
+    a.x_stride = p.x_stride;
+    a.w_scales = p.w_scales;
+    a.in = (int)p.in;
+    a.x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && (p.rows == 1 || p.x_stride * (int64_t)sizeof(T) % 16 == 0);
+  } else {
+    if (e == cudaSuccess) e = encode(&mx, p.x_values, kb, p.rows, 1, (uint32_t)a.cols);
+    if (e == cudaSuccess) e = encode_scales(&ms, p, tiles, 1, 1);
+  }
   if (e != cudaSuccess) return e;
   // shares of the sum: as many as one wave of two CTAs an SM takes, as in k_linear_few.cu
   int shares = places / tiles < kMaxShares ? places / tiles : kMaxShares;
   if (shares > blocks) shares = blocks;
   if (shares < 1) shares = 1;
-  return launch_cluster(k_mx_few, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, ms, a);
+  return launch_cluster(fn, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, ms, a);
 }
 
 template <int NB>
@@ -663,7 +759,14 @@ int mx_tile_rows(int64_t rows, int32_t experts, int64_t out) {
 }
 
 cudaError_t launch_mx_linear(const MxProduct& p, cudaStream_t s) {
-  if (!p.experts && p.rows <= 64) return run_few(p, s);
+  if (mx_own_rows(p.rows, p.experts)) {
+    switch (p.dtype) {
+      case DT_F16: return run_few<true, __half>(p, s);
+      case DT_BF16: return run_few<true, __nv_bfloat16>(p, s);
+      default: return run_few<true, float>(p, s);
+    }
+  }
+  if (!p.experts && p.rows <= 64) return run_few<false, float>(p, s);
   return mx_token_blocks(p.tile_rows) == 2 ? run_tiles<2>(p, s) : run_tiles<1>(p, s);
 }
 

@@ -37,7 +37,7 @@ Scratch scratch_of(const muon_mx_linear_args* a) {
   Scratch c{};
   const int64_t parts = mx_parts(a->in), mats = a->experts ? a->experts : 1;
   c.tile_rows = mx_tile_rows(a->rows, a->experts, a->out);
-  if (a->rows == 0) return c;
+  if (a->rows == 0 || mx_own_rows(a->rows, a->experts)) return c;
   c.x_scales = align256((size_t)(a->rows * blocks_of(a->in) * 16));
   c.w_scales = c.x_scales + align256((size_t)(mx_token_slots(a->rows, a->experts, c.tile_rows) * parts * 512 *
                                               mx_token_blocks(c.tile_rows)));
@@ -166,8 +166,14 @@ muon_status_t muon_mx_linear(const muon_mx_linear_args* args, void* stream) {
   p.w_values = static_cast<const uint8_t*>(a.w_values);
   p.w_scales = q.w_ordered;
   p.bias = a.bias; p.residual = a.residual; p.r_stride = a.residual ? a.residual_stride : 0; p.y = a.y;
+  const bool own = mx_own_rows(a.rows, a.experts);
+  if (own) {
+    p.x = a.x;
+    p.x_stride = a.x_stride;
+    p.w_scales = q.w_scales;
+  }
   cudaError_t e = ops_error_word(&p.err);
-  if (e == cudaSuccess) e = launch_mx_prepare(a.dtype, q, s);
+  if (e == cudaSuccess && !own) e = launch_mx_prepare(a.dtype, q, s);
   if (e == cudaSuccess) e = launch_mx_linear(p, s);
   return cuda_status(what, e);
 }

@@ -84,7 +84,7 @@ def test_mx_quantize_refuses(lib):
 
 def _args(**kw):
     a = _capi.muon_mx_linear_args()
-    base = {"dtype": 2, "rows": 8, "in": 64, "out": 24, "x_stride": 64, "residual_stride": 24, "x": P, "w_values": P,
+    base = {"dtype": 2, "rows": 80, "in": 64, "out": 24, "x_stride": 64, "residual_stride": 24, "x": P, "w_values": P,
             "w_scales": P, "y": P, "workspace": P, "workspace_bytes": 1 << 30}
     for k, v in {**base, **kw}.items():
         setattr(a, k, v)
@@ -122,6 +122,9 @@ def test_mx_workspace_holds_the_rounded_rows(lib, rows, experts):
     a = _args(rows=rows, experts=experts, **{"in": 1000, "x_stride": 1000})
     assert lib.muon_mx_linear_workspace(C.byref(a), C.byref(n)) == OK
     parts, mats = 8, max(experts, 1)
+    if rows == 1 and not experts:  # few rows: one launch, no scratch
+        assert n.value == 0
+        return
     assert n.value >= rows * 32 * 17 + mats * 512 * parts
     assert n.value <= 3 * rows * 32 * 17 + mats * (512 * parts * 2 + 1024 * parts) + 2048
 
