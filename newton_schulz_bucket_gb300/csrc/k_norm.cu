@@ -2,15 +2,22 @@
 // gradient: with xh = (x - mean) rstd and g = dy w,
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + r,   dw = sum over rows of dy xh,   db = sum of dy.
 //
-// Every tensor crosses HBM once: a row stays in the registers of its threads (16
-// elements each) between the sums over it and its result, and the next rows are on
-// their way meanwhile: several, by bulk copies into a ring in shared memory, where a row
-// belongs to a block and starts on 16 bytes; else the next one, into registers.  Rows of up to 512 elements belong to 1 to 32 lanes of a
-// warp, longer ones to a block.  The variance is the sum of squares about the mean,
-// not a difference of two large sums.  Blocks stay for many rows, so that the
-// weights are read once a block and the sums over rows (dw, db) grow in registers
-// too; each part of rows leaves one partial sum, and a second kernel adds the
-// parts in a fixed order.  No atomics: the same bits every time.
+// Every tensor crosses HBM once: a row stays in the registers of its threads (16 or 32
+// elements each) between the sums over it and its result, and the next rows are on their
+// way meanwhile: several, by bulk copies into a ring in shared memory, where a row belongs
+// to a block; else the next one, into registers.  Rows of up to 512 elements belong to 1
+// to 32 lanes of a warp, longer ones to a block.  The variance is the sum of squares about
+// the mean, not a difference of two large sums.  Blocks stay for many rows, so that the
+// weights are read once a block and the sums over rows (dw, db) grow in registers too;
+// each part of rows leaves one partial sum, and a second kernel adds the parts in a fixed
+// order.  No atomics: the same bits every time.
+//
+// Bound by HBM where rows are whole 16-byte pieces ([8192, 4096] bf16 24.5 us, 5.5 TB/s; its
+// gradient with a residual 50, without 43; [65536, 512] fp32 gradient 73, 5.5 TB/s), and by
+// issue where they are not and an element is a load from the ring and a store of its own
+// ([8192, 4095] bf16 50 and 81 us, fp32 48 and 71; read from memory by the lanes, without the
+// ring: 106 and 188, 123 and 206).  Few rows are bound by latency: one of 4096 3.1 us, its
+// gradient 5.7 in two launches.
 #include <mutex>
 #include <type_traits>
 
@@ -24,7 +31,13 @@ namespace {
 
 constexpr int kEach = 16;        // elements of a row that a thread holds
 constexpr int kSmallBlock = 128; // threads of a block whose warps hold whole rows
+// Blocks of them on an SM, by the elements of a load: as many as the registers allow
+// without spills that cost more than a block less ([131072, 256] bf16 back: 45 us with
+// four, 60 with three; [131072, 255]: 142 with four, 93 with two; forward: 51 with four,
+// 116 with six).
+constexpr int small_blocks(int n, bool backward) { return backward ? (n == 1 ? 2 : n == 4 ? 3 : 4) : (n == 1 ? 4 : 6); }
 constexpr int kMostThreads = 512;
+constexpr int kMostHeld = 1024;  // of k_norm_backward_held
 constexpr int kPartRows = 512;   // most rows a thread adds up one after another
 
 // N neighbouring elements (16 bytes of them if N > 1) in the form they are loaded in.
@@ -47,6 +60,14 @@ struct Piece {
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+    if constexpr (N == 1) {
+      one = T(0.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) u[i] = make_uint4(0, 0, 0, 0);
     }
   }
   __device__ __forceinline__ void open(float* f) const {
@@ -143,15 +164,17 @@ struct RowSum {
 
 // Rows of a block on their way: `kTensors` tensors' rows to a slot, by bulk copies that
 // one thread issues and a barrier counts.  A slot is free once every thread of the block
-// has taken its pieces: after the next __syncthreads.
+// has taken its pieces: after the next __syncthreads.  A row that starts or ends between
+// two 16-byte boundaries comes with the bytes around it up to them (of the same 16 as its
+// own ends, so of the same allocation), which nobody looks at.
 constexpr int kMostSlots = 8;
-template <int kTensors>
+template <int kTensors, bool kWhole>  // kWhole: rows start and end on 16 bytes
 struct RowRing {
   uint8_t* slots;
   uint64_t* full;
   volatile int* abort_flag;
   int* err;
-  uint32_t row_bytes, slot_bytes;
+  uint32_t row_bytes, part_bytes, slot_bytes;  // part: of a slot, for one tensor
   int n, at;                   // slots, the current one
   uint32_t phase;
   const uint8_t* src[kTensors];  // nullable
@@ -166,25 +189,34 @@ struct RowRing {
     }
     __syncthreads();
   }
+  __device__ __forceinline__ uintptr_t start(int t, int64_t row) const {
+    return reinterpret_cast<uintptr_t>(src[t]) + row * pitch[t];
+  }
+  __device__ __forceinline__ uint32_t window(uintptr_t p) const {
+    return kWhole ? row_bytes : ((uint32_t)(p & 15) + row_bytes + 15) & ~15u;
+  }
   __device__ __forceinline__ void fetch(int slot, int64_t row) {  // one thread
     const uint32_t bar = shared(full + slot);
     uint32_t to = shared(slots) + slot * slot_bytes, bytes = 0;
 #pragma unroll
-    for (int t = 0; t < kTensors; ++t) bytes += src[t] ? row_bytes : 0;
+    for (int t = 0; t < kTensors; ++t) bytes += src[t] ? window(start(t, row)) : 0;
     mbar_expect_tx(bar, bytes);
 #pragma unroll
-    for (int t = 0; t < kTensors; ++t, to += row_bytes) {
+    for (int t = 0; t < kTensors; ++t, to += part_bytes) {
       if (!src[t]) continue;
+      const uintptr_t p = start(t, row);
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-                   "l"(src[t] + row * pitch[t]), "r"(row_bytes), "r"(bar)
+                   "l"(p & ~(uintptr_t)15), "r"(window(p)), "r"(bar)
                    : "memory");
     }
   }
-  // The current slot, once its rows are there.  (A wait that runs out is reported by the
-  // error word; the block goes on, so that its threads stay together.)
-  __device__ __forceinline__ const uint8_t* take() {
+  // Waits for the current slot's rows.  (A wait that runs out is reported by the error
+  // word; the block goes on, so that its threads stay together.)
+  __device__ __forceinline__ void take() {
     mbar_wait(shared(full + at), phase, abort_flag, err, 1 << 16);
-    return slots + at * slot_bytes;
+  }
+  __device__ __forceinline__ const uint8_t* row_of(int t, int64_t row) const {
+    return slots + at * slot_bytes + t * part_bytes + (kWhole ? 0 : start(t, row) & 15);
   }
   __device__ __forceinline__ void next() {
     if (++at == n) { at = 0; phase ^= 1; }
@@ -218,11 +250,21 @@ __device__ __forceinline__ void load_weights(const void* w, int col, bool live, 
   }
 }
 
+template <int N>
+__device__ __forceinline__ void put_sums(float* out, const float* s) {
+  if constexpr (N == 1) {
+    *out = *s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(out + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+  }
+}
+
 // E elements a thread; kThreads: most threads of a block, kBlocks of which fit on an SM.
 template <typename T, typename W, int N, int E, bool kWarp, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lanes) {
   constexpr int P = E / N;
-  constexpr bool kRing = !kWarp && N > 1;
+  constexpr bool kRing = !kWarp;
   __shared__ __align__(16) Sums red;
   extern __shared__ __align__(128) uint8_t ring_bytes[];
   __shared__ uint64_t full[kMostSlots];
@@ -240,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
   T* y = static_cast<T*>(a.y) + at.col;
   const int64_t by = (int64_t)gridDim.x * at.rows;
   int64_t first = (int64_t)blockIdx.x * at.rows;  // the round's first row: the same for the block
-  RowRing<1> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.slot_bytes, a.slots, 0, 0,
+  RowRing<1, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes, a.slots, 0, 0,
                   {static_cast<const uint8_t*>(a.x)}, {a.x_stride * (int64_t)sizeof(T)}};
   Piece<T, N> v[P];
   if constexpr (kRing) {
@@ -262,20 +304,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
     const int64_t row = first + at.row;
     float f[E];
     if constexpr (kRing) {
-      const T* slot = reinterpret_cast<const T*>(ring.take()) + at.col;
+      ring.take();
+      const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + at.col;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-        if (live[p]) v[p].fetch(slot + p * at.step);
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (live[p] && row < a.rows) {
-        v[p].open(f + p * N);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[p * N + i] = 0.f;
+      for (int p = 0; p < P; ++p) {
+        Piece<T, N> u;
+        u.zero();
+        if (live[p]) u.fetch(sx + p * at.step);
+        u.open(f + p * N);
       }
-      if (!kRing && live[p] && row + by < a.rows) v[p].stream(x + (row + by) * a.x_stride + p * at.step);
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (live[p] && row < a.rows) {
+          v[p].open(f + p * N);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[p * N + i] = 0.f;
+        }
+        if (live[p] && row + by < a.rows) v[p].stream(x + (row + by) * a.x_stride + p * at.step);
+      }
     }
     float2 s2 = at2(f, 0);
 #pragma unroll
@@ -317,9 +365,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
 
 // Rows first .. last - 1 of a part; its sums go to row `part` of a.part.
 template <typename T, typename W, int N, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_backward(NormArgs a, int lanes) {
+__global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads, kWarp ? small_blocks(N, true) : 1)
+    k_norm_backward(NormArgs a, int lanes) {
   constexpr int P = kEach / N;
-  constexpr bool kRing = !kWarp && N > 1;
+  constexpr bool kRing = !kWarp;
   __shared__ __align__(16) Sums red;
   extern __shared__ __align__(128) uint8_t ring_bytes[];
   float* fold = reinterpret_cast<float*>(ring_bytes);  // kWarp: [warps][2][width]
@@ -342,7 +391,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
   const float per = 1.f / (float)h;
-  RowRing<3> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.slot_bytes, a.slots, 0, 0,
+  RowRing<3, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes, a.slots, 0, 0,
                   {static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.dy),
                    a.dx ? static_cast<const uint8_t*>(a.residual) : nullptr},
                   {a.x_stride * (int64_t)sizeof(T), a.dy_stride * (int64_t)sizeof(T), a.r_stride * (int64_t)sizeof(T)}};
@@ -376,27 +425,39 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
       float s1, s2;
       Piece<T, N> vr[P];
       if constexpr (kRing) {
-        const T* slot = reinterpret_cast<const T*>(ring.take()) + at.col;
+        ring.take();
+        const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + at.col;
+        const T* sd = reinterpret_cast<const T*>(ring.row_of(1, row)) + at.col;
+        const T* sr = reinterpret_cast<const T*>(ring.row_of(2, row)) + at.col;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          if (!live[p]) continue;
-          vx[p].fetch(slot + p * at.step);
-          vd[p].fetch(slot + h + p * at.step);
-          if (a.residual) vr[p].fetch(slot + 2 * h + p * at.step);
-        }
-      }
+          Piece<T, N> ux, ud;
+          ud.zero();
+          if (live[p]) {
+            ux.fetch(sx + p * at.step);
+            ud.fetch(sd + p * at.step);
+            if (ring.src[2]) vr[p].fetch(sr + p * at.step);
+          }
+          ux.open(xh + p * N);
+          ud.open(d + p * N);
+          if (live[p]) continue;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (mine && live[p]) {
-          vx[p].open(xh + p * N);
-          vd[p].open(d + p * N);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) xh[p * N + i] = mean, d[p * N + i] = 0.f;
+          for (int i = 0; i < N; ++i) xh[p * N + i] = mean;
         }
-        if (!kRing && next < last && live[p]) {
-          vx[p].stream(x + next * a.x_stride + p * at.step);
-          vd[p].stream(dy + next * a.dy_stride + p * at.step);
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (mine && live[p]) {
+            vx[p].open(xh + p * N);
+            vd[p].open(d + p * N);
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) xh[p * N + i] = mean, d[p * N + i] = 0.f;
+          }
+          if (next < last && live[p]) {
+            vx[p].stream(x + next * a.x_stride + p * at.step);
+            vd[p].stream(dy + next * a.dy_stride + p * at.step);
+          }
         }
       }
       const float r = rstd;
@@ -487,19 +548,108 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads) k_norm_bac
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         if (!live[p]) continue;
-        if constexpr (N == 1) {
-          out[p * at.step] = sw[p];
-          out[h + p * at.step] = sb[p];
-        } else {
+        put_sums<N>(out + p * at.step, sw + p * N);
+        put_sums<N>(out + h + p * at.step, sb + p * N);
+      }
+    }
+  }
+}
+
+// The gradient of rows that fill a block's registers with their sums over rows alone:
+// they stay in the ring, and are read twice from there ([2048, 16384] bf16 79 us, [3000,
+// 9000] 64; read again from memory, and once more for dw: 120 and 118).
+template <typename T, typename W, int N>
+__global__ void __launch_bounds__(kMostHeld) k_norm_backward_held(NormArgs a) {
+  constexpr int P = kEach / N;
+  __shared__ __align__(16) Sums red;
+  extern __shared__ __align__(128) uint8_t ring_bytes[];
+  __shared__ uint64_t full[kMostSlots];
+  __shared__ int aborted;
+  grid_launch_next();
+  RowSum<false> sum{&red, 32, 0};
+  sum.init();
+  const int h = (int)a.width, step = (int)blockDim.x * N, col = (int)threadIdx.x * N;
+  grid_wait();
+  const float per = 1.f / (float)h;
+  RowRing<3, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes,
+                           a.slots, 0, 0,
+                           {static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.dy),
+                            a.dx ? static_cast<const uint8_t*>(a.residual) : nullptr},
+                           {a.x_stride * (int64_t)sizeof(T), a.dy_stride * (int64_t)sizeof(T),
+                            a.r_stride * (int64_t)sizeof(T)}};
+  ring.init();
+  for (int64_t part = blockIdx.x; part < a.parts; part += gridDim.x) {
+    const int64_t first = part * a.part_rows, last = min(a.rows, first + a.part_rows);
+    if (threadIdx.x == 0)
+      for (int i = 0; i < a.slots && first + i < last; ++i)
+        ring.fetch(ring.at + i < a.slots ? ring.at + i : ring.at + i - a.slots, first + i);
+    float sw[kEach] = {}, sb[kEach] = {};
+    float next_mean = a.mean[first], next_rstd = a.rstd[first];
+    for (int64_t row = first; row < last; ++row) {
+      const float mean = next_mean, rstd = next_rstd;
+      if (row + 1 < last) {
+        next_mean = a.mean[row + 1];
+        next_rstd = a.rstd[row + 1];
+      }
+      ring.take();
+      const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + col;
+      const T* sd = reinterpret_cast<const T*>(ring.row_of(1, row)) + col;
+      const T* sr = reinterpret_cast<const T*>(ring.row_of(2, row)) + col;
+      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-          for (int i = 0; i < N; i += 4) {
-            *reinterpret_cast<float4*>(out + p * at.step + i) =
-                make_float4(sw[p * N + i], sw[p * N + i + 1], sw[p * N + i + 2], sw[p * N + i + 3]);
-            *reinterpret_cast<float4*>(out + h + p * at.step + i) =
-                make_float4(sb[p * N + i], sb[p * N + i + 1], sb[p * N + i + 2], sb[p * N + i + 3]);
-          }
+      for (int p = 0; p < P; ++p) {
+        if (col + p * step >= h) continue;
+        Piece<T, N> v;
+        float x[N], d[N], w[N];
+        v.fetch(sx + p * step);
+        v.open(x);
+        v.fetch(sd + p * step);
+        v.open(d);
+        load_weights<W, N>(a.w, col + p * step, true, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float xh = (x[i] - mean) * rstd, g = d[i] * w[i];
+          s1 += g;
+          s2 = fmaf(g, xh, s2);
+          sw[p * N + i] = fmaf(d[i], xh, sw[p * N + i]);
+          sb[p * N + i] += d[i];
         }
       }
+      if (a.dx) {
+        sum(s1, s2);
+        s1 *= per;
+        s2 *= per;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (col + p * step >= h) continue;
+          Piece<T, N> v;
+          float x[N], d[N], w[N], add[N] = {};
+          v.fetch(sx + p * step);
+          v.open(x);
+          v.fetch(sd + p * step);
+          v.open(d);
+          if (a.residual) {
+            v.fetch(sr + p * step);
+            v.open(add);
+          }
+          load_weights<W, N>(a.w, col + p * step, true, 1.f, w);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            x[i] = fmaf(rstd, fmaf((mean - x[i]) * rstd, s2, fmaf(d[i], w[i], -s1)), add[i]);
+          put<T, N>(static_cast<T*>(a.dx) + row * h + col + p * step, x);
+        }
+      }
+      __syncthreads();  // everyone is done with the slot
+      if (threadIdx.x == 0 && row + a.slots < last) ring.fetch(ring.at, row + a.slots);
+      ring.next();
+    }
+    if (!a.part) continue;
+    float* out = a.part + part * 2 * h + col;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (col + p * step >= h) continue;
+      put_sums<N>(out + p * step, sw + p * N);
+      put_sums<N>(out + h + p * step, sb + p * N);
     }
   }
 }
@@ -660,31 +810,35 @@ __global__ void __launch_bounds__(1024) k_norm_join(NormArgs a) {
 }
 
 // How rows of this width are held: by lanes of a warp, by a block (`each` elements a
-// thread, `blocks` blocks an SM), or by none.  Forward, 16-bit rows take 32 elements a
-// thread where there are rows enough to fill the GPU: the sums over a row then cost half as
-// much of a thread ([8192, 4096] bf16: 25.5 us against 31; fp32 is bound by HBM, 47
-// against 45).
+// thread, `blocks` blocks an SM), in the ring, or by none.  Forward, rows but fp32 ones in
+// whole pieces take 32 elements a thread where there are rows enough to fill the GPU: the
+// sums over a row then cost half as much of a thread ([8192, 4096] bf16: 25.5 us against 31;
+// fp32 in whole pieces is bound by HBM, 47 against 45).  Rows that 512 threads of 16 do not
+// hold take 32 too ([2000, 12001] bf16 47 us; read again for each sum 83).
 struct Form {
-  bool warp, wide;
+  bool warp, held, wide;
   int lanes, threads, each, blocks;
 };
 Form form_of(int64_t rows, int64_t width, int n, bool backward) {
   const auto threads_of = [&](int64_t each) { return ((width + n - 1) / n * n + each - 1) / each; };
   const int64_t t = threads_of(kEach), t2 = threads_of(2 * kEach);
-  Form f{false, false, 32, 0, kEach, 1};
+  Form f{false, false, false, 32, 0, kEach, 1};
   if (t <= 32) {
     f.warp = true;
     f.lanes = 1;
     while (f.lanes < t) f.lanes *= 2;
     f.threads = kSmallBlock;
-    f.blocks = backward ? 4 : 6;
-  } else if (backward || n == 1 ? t <= 512 : (t <= 256 && (n != 8 || rows < 2 * num_sms() || t2 < 64))) {
+    f.blocks = small_blocks(n, backward);
+  } else if (backward ? t <= 512 : (t <= 256 && (n == 4 || rows < 2 * num_sms() || t2 < 64))) {
     f.threads = (int)((t + 31) / 32 * 32);
     f.blocks = f.threads > 256 ? 1 : (backward ? 512 : 768) / f.threads;
-  } else if (!backward && n > 1 && t2 <= 512) {
+  } else if (!backward && t2 <= 512) {
     f.each = 2 * kEach;
     f.threads = (int)((t2 + 31) / 32 * 32);
     f.blocks = 512 / f.threads;
+  } else if (backward && t <= kMostHeld) {
+    f.held = true;
+    f.threads = (int)((t + 31) / 32 * 32);
   } else {
     f.wide = true;
     f.threads = 1024;
@@ -727,7 +881,9 @@ void set_parts(NormArgs* a, int n) {
 
 // The ring of a block: what fits of `blocks` blocks an SM.
 constexpr int64_t kRingBytes = 208 * 1024;
-size_t set_slots(NormArgs* a, int64_t slot_bytes, int64_t blocks) {
+size_t set_slots(NormArgs* a, int64_t row_bytes, int tensors, bool whole, int64_t blocks) {
+  a->part_bytes = (uint32_t)(whole ? row_bytes : (row_bytes + 15) / 16 * 16 + 16);
+  const int64_t slot_bytes = (int64_t)tensors * a->part_bytes;
   const int64_t n = kRingBytes / (blocks < 1 ? 1 : blocks) / slot_bytes;
   a->slot_bytes = (uint32_t)slot_bytes;
   a->slots = (int)(n < 1 ? 1 : (n < kMostSlots ? n : kMostSlots));
@@ -741,7 +897,7 @@ cudaError_t allow(F fn) {
   static struct {
     F fn;
     bool ready[64];
-  } table[4] = {};
+  } table[40] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -766,17 +922,14 @@ cudaError_t forward(NormArgs a, cudaStream_t s) {
   const int64_t rounds = (a.rows + each - 1) / each, most = (int64_t)num_sms() * f.blocks;
   const dim3 grid((unsigned)(rounds < most ? rounds : most)), block((unsigned)f.threads);
   if (f.wide) return launch_early(k_norm_wide<T, W, N>, grid, block, 0, s, a);
-  if (f.warp) return launch_early(k_norm<T, W, N, kEach, true, kSmallBlock, 6>, grid, block, 0, s, a, f.lanes);
+  if (f.warp) return launch_early(k_norm<T, W, N, kEach, true, kSmallBlock, small_blocks(N, false)>, grid, block, 0, s, a, f.lanes);
   auto fn = k_norm<T, W, N, kEach, false, 256, 3>;
-  if constexpr (N == 1) {
-    if (f.threads > 256) fn = k_norm<T, W, N, kEach, false, 512, 1>;
-  } else if (f.each > kEach) {
+  if (f.each > kEach)
     fn = f.threads > 256 ? k_norm<T, W, N, 2 * kEach, false, 512, 1> : k_norm<T, W, N, 2 * kEach, false, 256, 2>;
-  }
   size_t smem = 0;
   cudaError_t e = ops_error_word(&a.err);
-  if (e == cudaSuccess && N > 1) {
-    smem = set_slots(&a, a.width * (int64_t)sizeof(T), f.blocks);
+  if (e == cudaSuccess) {
+    smem = set_slots(&a, a.width * (int64_t)sizeof(T), 1, N > 1, f.blocks);
     e = allow(fn);
   }
   return e == cudaSuccess ? launch_early(fn, grid, block, smem, s, a, f.lanes) : e;
@@ -799,13 +952,14 @@ cudaError_t backward(NormArgs a, cudaStream_t s) {
     const dim3 grid((unsigned)(a.parts < most ? a.parts : most)), block((unsigned)f.threads);
     size_t smem = f.warp ? sizeof(float) * 2 * a.width * (f.threads / 32) : 0;
     e = ops_error_word(&a.err);
-    if (e == cudaSuccess && !f.warp && N > 1) {
-      smem = set_slots(&a, 3 * a.width * (int64_t)sizeof(T), f.blocks);
-      e = allow(k_norm_backward<T, W, N, false>);
+    if (e == cudaSuccess && !f.warp) {
+      smem = set_slots(&a, a.width * (int64_t)sizeof(T), a.dx && a.residual ? 3 : 2, N > 1, f.blocks);
+      e = f.held ? allow(k_norm_backward_held<T, W, N>) : allow(k_norm_backward<T, W, N, false>);
     }
     if (e != cudaSuccess) return e;
-    e = f.warp ? launch_early(k_norm_backward<T, W, N, true>, grid, block, smem, s, a, f.lanes)
-               : launch_early(k_norm_backward<T, W, N, false>, grid, block, smem, s, a, f.lanes);
+    if (f.held) e = launch_early(k_norm_backward_held<T, W, N>, grid, block, smem, s, a);
+    else e = f.warp ? launch_early(k_norm_backward<T, W, N, true>, grid, block, smem, s, a, f.lanes)
+                    : launch_early(k_norm_backward<T, W, N, false>, grid, block, smem, s, a, f.lanes);
   }
   if (e == cudaSuccess && a.part)
     e = launch_early(k_norm_join<W>, dim3((unsigned)((2 * a.width + 31) / 32)), dim3(1024), 0, s, a);

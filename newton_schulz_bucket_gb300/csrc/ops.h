@@ -151,7 +151,7 @@ struct NormArgs {
   void* db;                    // nullable
   float* part;                 // nullable: [parts][2][width] sums of dw and db
   int64_t parts, part_rows;    // set by the launch, as what follows
-  uint32_t slot_bytes;         // of the ring of rows on their way
+  uint32_t part_bytes, slot_bytes;  // of the ring of rows on their way
   int32_t slots;
   int* err;
 };

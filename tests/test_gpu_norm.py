@@ -127,6 +127,23 @@ def test_rows_do_not_depend_on_their_batch(width):
     _check(x[pick], w, b)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,width", [(1200, 700), (700, 4097), (400, 9001), (330, 16383)])
+def test_rows_between_boundaries(rows, width, dtype):
+    """Rows that start and end anywhere, each tensor's elsewhere, many to a block."""
+    dt = DT[dtype]
+    x, w, b, dy, r = _inputs(rows, width, dt, 8)
+
+    def within(t, lead, more):
+        wide = torch.full((rows, width + more), float("nan"), dtype=dt, device="cuda")
+        wide[:, lead:lead + width] = t
+        return wide[:, lead:lead + width]
+
+    x, dy, r = within(x, 3, 7), within(dy, 1, 1), within(r, 0, 4)
+    _, mean, rstd = _check(x, w, b)
+    _check_backward(dy, x, mean, rstd, w, r)
+
+
 def test_large_and_small_rows():
     """Means far above the spread, tiny and constant rows, the largest numbers."""
     g = torch.Generator(device="cuda").manual_seed(5)
