@@ -63,6 +63,29 @@ __device__ __forceinline__ uint4 pack8(const float* f, int type) {
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
   return u;
 }
+// SiLU and the tanh form of GELU of 16-bit tensors, two values at a time: the operations of
+// activate<true> in the same order (all 2^32 arguments give the same bits).  The hardware's
+// exponential and reciprocal may flush numbers below 2^-126 to zero here: e^-v is far below
+// the last place of 1 then, and __fdividef gives zero too.  The epilogue takes issue slots
+// and power from the product: 4096 tokens, [4096, 16384] in 4 bits, bias, gelu_tanh 113 us
+// against 121 one value at a time, silu 109 against 113.  (Done so for GELU too, that form
+// gains nothing, 139, and the others lose it again, 128 and 122.)
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = __fmul2_rn(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));  // e^-v = 2^t
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
+}
+__device__ __forceinline__ float2 silu2(float2 z) { return __fmul2_rn(z, sigmoid2(z)); }
+__device__ __forceinline__ float2 gelu_tanh2(float2 z) {
+  const float c = kTanhCubic, k = 2.f * kSqrt2OverPi;
+  const float2 zz = __fmul2_rn(__fmul2_rn(z, make_float2(c, c)), z);
+  return __fmul2_rn(z, sigmoid2(__fmul2_rn(__ffma2_rn(zz, z, z), make_float2(k, k))));
+}
 template <int N, bool kFast>
 __device__ __forceinline__ void activate_n(float* v, int act) {
   switch (act) {  // outside the loop over values
@@ -73,7 +96,16 @@ __device__ __forceinline__ void activate_n(float* v, int act) {
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_SILU);
+      for (int i = 0; i < N; i += 2) {
+        if constexpr (kFast) {
+          const float2 r = silu2(make_float2(v[i], v[i + 1]));
+          v[i] = r.x;
+          v[i + 1] = r.y;
+        } else {
+          v[i] = activate<kFast>(v[i], ACT_SILU);
+          v[i + 1] = activate<kFast>(v[i + 1], ACT_SILU);
+        }
+      }
       break;
     case ACT_GELU:
 #pragma unroll
@@ -81,7 +113,16 @@ __device__ __forceinline__ void activate_n(float* v, int act) {
       break;
     default:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = activate<kFast>(v[i], ACT_GELU_TANH);
+      for (int i = 0; i < N; i += 2) {
+        if constexpr (kFast) {
+          const float2 r = gelu_tanh2(make_float2(v[i], v[i + 1]));
+          v[i] = r.x;
+          v[i + 1] = r.y;
+        } else {
+          v[i] = activate<kFast>(v[i], ACT_GELU_TANH);
+          v[i + 1] = activate<kFast>(v[i + 1], ACT_GELU_TANH);
+        }
+      }
   }
 }
 
