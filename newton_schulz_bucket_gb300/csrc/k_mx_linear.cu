@@ -20,7 +20,7 @@
 // the rounding (5600 TFLOP/s): the tensor pipe is 82% busy and the clock at 1.58 GHz, under
 // the power cap.
 //
-// Up to 64 rows of one matrix take the form of k_linear_few.cu: 128 features a cluster of
+// Up to 64 rows of one matrix can take the form of k_linear_few.cu: 128 features a cluster of
 // up to eight CTAs that share the sum.  Up to 16 of them need no launch before: the warps
 // that wait for the sum round the rows and order the scales meanwhile.
 #include <cuda.h>
@@ -743,19 +743,26 @@ cudaError_t run_tiles(const MxProduct& p, cudaStream_t s) {
 
 }  // namespace
 
-// Most token rows of a tile: as many as fill the tensor cores' columns, fewer where
-// that leaves pairs without a tile.  An expert often has more rows than the average,
-// which is all the host knows: not where that would need another tile.
+// Most token rows of a tile: as many as fill the tensor cores' columns, fewer where that
+// leaves pairs without a tile (512 rows, 4096 -> 16384: 25.3 us with 192, 26.9 with 128;
+// 4096 -> 4096: 14.6 and 14.3; with 64 35 and 17).  An expert often has more rows than the
+// average, which is all the host knows: not where that would need another tile (64 experts
+// [7168, 2048] of 32 rows 113 us with 64, 115 with 192; of 64 rows 125 with 128, 131 with 64;
+// of 128 rows 147 with 192, 152 with 128).
 int mx_tile_rows(int64_t rows, int32_t experts, int64_t out) {
-  const int64_t pairs = num_sms() / 2, features = (out + BM - 1) / BM;
   if (experts) {
     const int64_t ranges = rows < experts ? rows : experts, each = ranges ? (rows + ranges - 1) / ranges : 0;
     return each <= 32 ? 64 : (each <= 64 ? 128 : 192);
   }
   if (rows <= 64) return 64;
-  for (int t : {192, 128})
-    if (features * ((rows + t - 1) / t) >= pairs) return t;
-  return 64;
+  return (out + BM - 1) / BM * ((rows + 191) / 192) >= num_sms() / 2 ? 192 : 128;
+}
+
+// Few rows of one matrix, where four CTAs or more can share a sum (32 rows, 4096 -> 4096: 9.4
+// us, 10.9 in tiles; 64 rows, 16384 -> 4096: 16.3 and 20.8; with three shares 64 rows, 4096
+// -> 12288 16.8 and 13.2).  (Rows that a product rounds itself always.)
+static bool few_rows(const MxProduct& p) {
+  return !p.experts && p.rows <= 64 && 4 * ((p.out + 127) / 128) <= 2 * num_sms();
 }
 
 cudaError_t launch_mx_linear(const MxProduct& p, cudaStream_t s) {
@@ -766,7 +773,7 @@ cudaError_t launch_mx_linear(const MxProduct& p, cudaStream_t s) {
       default: return run_few<true, float>(p, s);
     }
   }
-  if (!p.experts && p.rows <= 64) return run_few<false, float>(p, s);
+  if (few_rows(p)) return run_few<false, float>(p, s);
   return mx_token_blocks(p.tile_rows) == 2 ? run_tiles<2>(p, s) : run_tiles<1>(p, s);
 }
 

@@ -106,7 +106,7 @@ def test_quantize_non_finite_blocks(dtype, out_in):
 # tokens; sums of part of a block, an odd number of 128 steps, part of a stage of 256
 LINEAR = [(1, 32, 1), (1, 64, 128), (1, 1000, 129), (3, 512, 300), (16, 777, 129), (17, 1024, 256), (40, 2048, 100),
           (64, 300, 500), (64, 4096, 260), (65, 64, 128), (100, 33, 7), (129, 256, 256), (190, 384, 300), (200, 777, 129),
-          (300, 1024, 512), (1000, 130, 1000), (2, 12345, 40), (70, 9000, 70)]
+          (300, 1024, 512), (1000, 130, 1000), (2, 12345, 40), (70, 9000, 70), (33, 320, 9800), (64, 96, 12300), (7, 96, 12300)]
 
 
 @pytest.mark.parametrize("dtype", list(DT))
