@@ -11,6 +11,9 @@
 // experts' probabilities over its tokens, in two levels (kRun tokens, then their
 // sums), so that long batches keep their digits; lanes, warps and blocks are then
 // added in a fixed order, and counts are whole numbers: the same bits every time.
+// Bound by issue (the exponentials and a token's reductions), not by HBM: 131072 tokens of 64
+// experts, fp32, 34 MB, take 21 us (back, 67 MB, 18), 32768 of 512 44 (49); 16384 of 64 9.7
+// (4.7), where the latency of the two launches counts.
 #include "common.cuh"
 #include "ops.h"
 

@@ -5,7 +5,9 @@
 // so that loads and stores are whole lines.  Weights stored across the sum go through
 // a tile of 256 steps of it by 64 columns: a lane takes 32 steps of two neighbouring
 // columns, so that it has a block to itself, and the packed rows meet in shared
-// memory.  Bound by HBM.
+// memory.  Bound by HBM: [4096, 16384] bf16 into 4 bits and back 57.6 us, 340 MB with the
+// packed numbers (5.9 TB/s).  In front of a product, 32768 rows of 7168 and the scales of 64
+// matrices [7168, 2048] take 133 us, 646 MB (4.9 TB/s), with 60% of the issue slots busy.
 #include "common.cuh"
 #include "linear_tiles.cuh"
 #include "mx.cuh"
@@ -133,7 +135,7 @@ __device__ __forceinline__ uint32_t token_scales(const MxPrepare& q, int row, ui
 }
 
 // What a product starts from, in one launch: the token rows, then the weights' scales
-// (of the matrices that any row reaches) through shared memory, 128 rows x 64 words.
+// (of the matrices that any row reaches) through shared memory, 128 rows x 16 words.
 constexpr int kWords = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
