@@ -17,8 +17,8 @@
 // to 192 tokens (two accumulators of 192 columns and 5 x 24 columns of scales fill
 // TMEM), each CTA stages its 128 rows of weights and its half of the tokens, 256 steps a
 // stage.  Waits, scale copies, MMAs and commits are issued by three warps: in one they
-// took 800 cycles a stage, where the MMAs take 384.  [8192 x 8192] x [8192, 8192] 196 us with
-// the rounding (5600 TFLOP/s): the tensor pipe is 82% busy and the clock at 1.58 GHz, under
+// took 800 cycles a stage, where the MMAs take 384.  [8192 x 8192] x [8192, 8192] 190 us with
+// the rounding (5790 TFLOP/s): the tensor pipe is 82% busy and the clock at 1.58 GHz, under
 // the power cap.
 //
 // Up to 64 rows of one matrix can take the form of k_linear_few.cu: 128 features a cluster of

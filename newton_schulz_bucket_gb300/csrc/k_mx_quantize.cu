@@ -7,7 +7,7 @@
 // columns, so that it has a block to itself, and the packed rows meet in shared
 // memory.  Bound by HBM: [4096, 16384] bf16 into 4 bits and back 57.6 us, 340 MB with the
 // packed numbers (5.9 TB/s).  In front of a product, 32768 rows of 7168 and the scales of 64
-// matrices [7168, 2048] take 133 us, 646 MB (4.9 TB/s), with 60% of the issue slots busy.
+// matrices [7168, 2048] take about 130 us, 646 MB (5 TB/s).
 #include "common.cuh"
 #include "linear_tiles.cuh"
 #include "mx.cuh"
@@ -18,9 +18,13 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-// Rows of a thread, in flight together.
+// Rows of a thread, in flight together: in front of a product (4096 rows of 4096 before
+// [4096, 16384]: 110 us with four, 112 with eight or two; 32 rows over 64 experts 50.6, 54,
+// 51.2), and of weights held along the sum (into 4 bits and back, [16384, 4096] bf16 56 us with
+// four, 59 with two; [4096, 4096] fp32 31.9 and 31.1, five [777, 1001] 16.8 and 14.2).
+constexpr int kRowsOf = 4;
 template <typename T>
-constexpr int kRowsOf = sizeof(T) == 4 ? 4 : 8;
+constexpr int kWeightRows = sizeof(T) == 4 ? 2 : 4;
 
 // Where a thread of the row kernels works: its piece of eight columns, its first row.
 struct Spot {
@@ -38,9 +42,8 @@ __device__ __forceinline__ Spot spot(const MxRows& q, uint32_t block) {
 // Loads and rounds a thread's rows; each row's block of 32 and its scale go to `give`,
 // which all lanes of a warp call together.  kMats: rows of several matrices (rows counts
 // all of them; one row after the other in the outputs).
-template <typename T, bool kMats, typename M, typename F>
+template <typename T, int kRows, bool kMats, typename M, typename F>
 __device__ __forceinline__ void quantize_rows(const MxRows& q, const Spot& at, M meanwhile, F give) {
-  constexpr int kRows = kRowsOf<T>;
   const int64_t col = (int64_t)at.piece * 8, kb = (q.cols + kMxBlock - 1) / kMxBlock;
   const bool there = at.piece < 4 * kb;
   const T* src = static_cast<const T*>(q.src) + at.row * q.stride + col;
@@ -99,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_rows(MxRows q) {
   grid_launch_next();
   grid_wait();
   const int64_t kb = (q.cols + kMxBlock - 1) / kMxBlock;
-  const Spot at = spot<kRowsOf<T>>(q, blockIdx.x);
-  quantize_rows<T, kMats>(q, at, [] {}, [&](int k, int b, uint32_t s, bool live) {
+  const Spot at = spot<kWeightRows<T>>(q, blockIdx.x);
+  quantize_rows<T, kWeightRows<T>, kMats>(q, at, [] {}, [&](int k, int b, uint32_t s, bool live) {
     if (live && b < kb && (threadIdx.x & 3) == 0) q.scales[(at.row + k * at.by) * kb + b] = (uint8_t)s;
   });
 }
@@ -140,13 +143,13 @@ constexpr int kWords = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
   __shared__ uint32_t words[128][kWords + 1];
-  __shared__ uint32_t place[kThreads / 4 * kRowsOf<T>];
+  __shared__ uint32_t place[kThreads / 4 * kRowsOf];
   grid_wait();
   // only now: the product reads the weights before it waits for this launch
   grid_launch_next();
   const int64_t kb = (q.x.cols + kMxBlock - 1) / kMxBlock, parts = (kb + 3) / 4;
   if (blockIdx.x < (uint32_t)q.x_blocks) {
-    constexpr int kRows = kRowsOf<T>;
+    constexpr int kRows = kRowsOf;
     const uint32_t part_words = 128 * mx_token_blocks(q.tile_rows), slot_words = (uint32_t)parts * part_words;
     const Spot at = spot<kRows>(q.x, blockIdx.x);
     // the block's rows' places, while the rows are on their way (each warp for itself took
@@ -169,11 +172,11 @@ __global__ void __launch_bounds__(kThreads) k_mx_prepare(MxPrepare q) {
       if (across < 16 && b + 1 == (int)kb)  // no lanes there
         for (int z = b + 1; z < 4; ++z) word[z] = 0;
     };
-    quantize_rows<T, false>(q.x, at, find, give);
+    quantize_rows<T, kRows, false>(q.x, at, find, give);
     // (enough rows to fill the GPU: one block takes all columns of its own)
     for (Spot next = at; next.piece + across * (int)q.x.col_blocks < across * q.x.col_total;) {
       next.piece += across * (int)q.x.col_blocks;
-      quantize_rows<T, false>(q.x, next, [] {}, give);
+      quantize_rows<T, kRows, false>(q.x, next, [] {}, give);
     }
     return;
   }
@@ -345,7 +348,7 @@ cudaError_t run(MxRows q, MxOp op, cudaStream_t s) {
     return launch_early(k_mx_quantize_across<T>, dim3((unsigned)(ti * to * (q.rows / q.mat_rows))), dim3(kThreads), 0, s,
                         q, (int)ti, (int)to);
   }
-  const dim3 grid((unsigned)shape_rows(&q, op == MX_BACK ? kBackRows : kRowsOf<T>));
+  const dim3 grid((unsigned)shape_rows(&q, op == MX_BACK ? kBackRows : kWeightRows<T>));
   if (op == MX_BACK) {
     q.vec = reinterpret_cast<uintptr_t>(q.dst) % 16 == 0 && q.cols % 8 == 0;
     return launch_early(k_mx_dequantize<T>, grid, dim3(kThreads), 0, s, q);
@@ -357,7 +360,7 @@ cudaError_t run(MxRows q, MxOp op, cudaStream_t s) {
 
 template <typename T>
 cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
-  q.x_blocks = shape_rows(&q.x, kRowsOf<T>);
+  q.x_blocks = shape_rows(&q.x, kRowsOf);
   q.x.vec = vector_rows<T>(q.x);
   // a block takes all columns of its rows, or all parts of its 128 features, where that
   // leaves blocks enough
@@ -376,7 +379,7 @@ cudaError_t run_prepare(MxPrepare q, cudaStream_t s) {
 // Blocks of the largest grid of these kernels.
 int64_t mx_blocks(int64_t rows, int64_t mat_rows, int64_t cols) {
   const int64_t kb = (cols + kMxBlock - 1) / kMxBlock;
-  const int64_t along = (rows / 4 + 1) * ((kb * 4 + 255) / 256);
+  const int64_t along = (rows / 2 + 1) * ((kb * 4 + 255) / 256);
   const int64_t across = (kb + 7) / 8 * ((mat_rows + 63) / 64) * (mat_rows ? rows / mat_rows : 0);
   return along > across ? along : across;
 }
