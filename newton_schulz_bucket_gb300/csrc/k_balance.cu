@@ -58,27 +58,26 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-// v becomes exp(v - max), -inf gives 0; returns whether any of the token's logits is
-// above -inf (a NaN counts: its token comes out NaN).  masked: a bit for each of the
-// lane's logits that is -inf (an exponential of 0 does not tell: it may have underflowed).
+__device__ __forceinline__ bool masked(float v) { return __float_as_uint(v) == 0x80000000u; }
+// v becomes exp(v - max); returns whether any of the token's logits is above -inf (a NaN
+// counts: its token comes out NaN).  A logit of -inf gives -0, which tells it from an
+// exponential that underflowed (+0) and adds nothing all the same; a mask word beside the
+// exponentials took 4% more of the way back.
 template <int NV>
-__device__ __forceinline__ bool exponentials(float* v, int lanes, bool* nan, uint32_t* masked) {
-  static_assert(NV <= 32, "a bit each");
+__device__ __forceinline__ bool exponentials(float* v, int lanes, bool* nan) {
   float high = -kInf;
   bool bad = false;
-  *masked = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     bad |= v[i] != v[i];
     high = fmaxf(high, v[i]);
-    *masked |= v[i] == -kInf ? 1u << i : 0u;
   }
   for (int o = lanes >> 1; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
   const unsigned any = __ballot_sync(0xffffffffu, bad);
   const int first = (threadIdx.x & 31) & ~(lanes - 1);
   *nan = (any >> first) & (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = v[i] == -kInf ? 0.f : expf(v[i] - high);
+  for (int i = 0; i < NV; ++i) v[i] = v[i] == -kInf ? -0.f : expf(v[i] - high);
   return high > -kInf || *nan;
 }
 
@@ -147,8 +146,7 @@ __global__ void __launch_bounds__(kCluster ? kClusterThreads : kForward<NV>) k_b
     for (int i = 0; i < NV; ++i) v[i] = next[i];
     load(first + kWarps * per + lane / lanes, next);
     bool nan;
-    uint32_t masked;
-    const bool open = exponentials<NV>(v, lanes, &nan, &masked);
+    const bool open = exponentials<NV>(v, lanes, &nan);
     float total = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) total += v[i];
@@ -328,8 +326,7 @@ __global__ void __launch_bounds__(kBackward) k_balance_backward(BalanceArgs a, i
     const int64_t t = first + lane / lanes;
     if (first > begin) load(t);
     bool nan;
-    uint32_t masked;
-    const bool open = exponentials<NV>(v, lanes, &nan, &masked);
+    const bool open = exponentials<NV>(v, lanes, &nan);
     float total = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(kBackward) k_balance_backward(BalanceArgs a, i
     for (int i = 0; i < NV; ++i) {
       // (a masked expert's gradient is 0 whatever the others are; in a token with a NaN or
       // +inf every open one's is NaN, the underflowed ones' too: inv and dot are)
-      const float d = masked >> i & 1 ? 0.f : scale * (v[i] * inv) * (share[i] - dot);
+      const float d = masked(v[i]) ? 0.f : scale * (v[i] * inv) * (share[i] - dot);
       h[i] = from_f32<T>(res ? d + r[i] : d);
     }
     constexpr int kPiece = 16 / (int)sizeof(T);
