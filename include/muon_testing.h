@@ -68,6 +68,21 @@ MUON_API int32_t muon_testing_skinny_max_clusters(int32_t ns_dtype, int64_t m);
  * `stream`. */
 MUON_API muon_status_t muon_testing_wait_probe(int32_t arrive, int64_t limit_cycles, void* stream);
 
+/* The same for the layer norm's rows on their way into shared memory: muon_layer_norm (dy
+ * NULL: out = y, mean and rstd nullable) or muon_layer_norm_backward (out = dx and dw,
+ * one of them nullable) without weights, where in one block (0 .. ) nothing completes the
+ * barrier of one slot of the ring (0 .. 7), so that the block's wait for the first row
+ * in it runs out after limit_cycles (1024 .. 2^33).  The block then stores nothing from
+ * that row on and ends, the other blocks' rows come out as ever, and the call returns
+ * TIMEOUT (OK if no row takes that slot); the context stays usable.  dtype:
+ * muon_dtype_t; width in 513 .. 16384 (rows that a block takes).  INVALID_ARG for other
+ * arguments; CUDA or OOM on a runtime failure.  Synchronises the device and clears the
+ * operators' error word. */
+MUON_API muon_status_t muon_testing_norm_lost_row(int32_t dtype, int64_t rows, int64_t width, int32_t block,
+                                                  int32_t slot, int64_t limit_cycles, const void* x,
+                                                  const void* dy, float* mean, float* rstd, void* out,
+                                                  void* dw, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -93,7 +93,7 @@ class muon_mx_linear_args(C.Structure):
 # test hooks declared in include/muon_testing.h
 EXPORTED_TESTING = ["muon_testing_tc_gemm", "muon_testing_skinny_max_clusters",
                     "muon_testing_tile_walk", "muon_testing_tile_walk_pair",
-                    "muon_testing_tc_pair_form", "muon_testing_wait_probe"]
+                    "muon_testing_tc_pair_form", "muon_testing_wait_probe", "muon_testing_norm_lost_row"]
 
 # every symbol include/muon.h declares, for the export check
 EXPORTED = ["muon_default_options", "muon_plan_describe", "muon_plan_create", "muon_step",
@@ -171,6 +171,8 @@ def load() -> C.CDLL:
     L.muon_testing_tc_pair_form.restype = i32
     L.muon_testing_wait_probe.argtypes = [i32, i64, vp]
     L.muon_testing_wait_probe.restype = C.c_int
+    L.muon_testing_norm_lost_row.argtypes = [i32, i64, i64, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp]
+    L.muon_testing_norm_lost_row.restype = C.c_int
     L.muon_linear_workspace.argtypes = [C.POINTER(muon_linear_args), i32, C.POINTER(C.c_size_t)]
     L.muon_linear.argtypes = [C.POINTER(muon_linear_args), vp]
     L.muon_linear_backward.argtypes = [C.POINTER(muon_linear_args), vp]

@@ -167,14 +167,20 @@ struct RowSum {
 // has taken its pieces: after the next __syncthreads.  A row that starts or ends between
 // two 16-byte boundaries comes with the bytes around it up to them (of the same 16 as its
 // own ends, so of the same allocation), which nobody looks at.
+//
+// A wait that runs out ends the block: who gave up sets the row's flag, which all of its
+// threads read after the next __syncthreads (gave_up), so that they agree; nothing more is
+// fetched or stored, the copies in flight land, and the block leaves.  A flag is set
+// again only behind a further barrier that everyone comes to after having read it:
+// rows with one barrier take turns at two flags.
 constexpr int kMostSlots = 8;
 template <int kTensors, bool kWhole>  // kWhole: rows start and end on 16 bytes
 struct RowRing {
   uint8_t* slots;
   uint64_t* full;
-  volatile int* abort_flag;
-  int* err;
-  uint32_t row_bytes, part_bytes, slot_bytes;  // part: of a slot, for one tensor
+  volatile int* state;         // two flags; the waits' limit in 1024 cycles
+  const NormArgs& a;
+  uint32_t row_bytes;
   int n, at;                   // slots, the current one
   uint32_t phase;
   const uint8_t* src[kTensors];  // nullable
@@ -182,11 +188,13 @@ struct RowRing {
 
   static __device__ __forceinline__ uint32_t shared(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
   __device__ __forceinline__ void init() {
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < n; ++i) mbar_init(shared(full + i), 1);
-      *abort_flag = 0;
+    const int i = threadIdx.x;  // (a barrier a thread: all by one took 0.1 us of the latency of few rows)
+    if (i < n) {
+      mbar_init(shared(full + i), i == a.lost_slot - 1 && (int)blockIdx.x == a.lost_block ? 2 : 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (i < 2) state[i] = 0;
+    if (i == 2) state[2] = a.wait_limit;
     __syncthreads();
   }
   __device__ __forceinline__ uintptr_t start(int t, int64_t row) const {
@@ -197,12 +205,12 @@ struct RowRing {
   }
   __device__ __forceinline__ void fetch(int slot, int64_t row) {  // one thread
     const uint32_t bar = shared(full + slot);
-    uint32_t to = shared(slots) + slot * slot_bytes, bytes = 0;
+    uint32_t to = shared(slots) + slot * a.slot_bytes, bytes = 0;
 #pragma unroll
     for (int t = 0; t < kTensors; ++t) bytes += src[t] ? window(start(t, row)) : 0;
     mbar_expect_tx(bar, bytes);
 #pragma unroll
-    for (int t = 0; t < kTensors; ++t, to += part_bytes) {
+    for (int t = 0; t < kTensors; ++t, to += a.part_bytes) {
       if (!src[t]) continue;
       const uintptr_t p = start(t, row);
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
@@ -210,13 +218,19 @@ struct RowRing {
                    : "memory");
     }
   }
-  // Waits for the current slot's rows.  (A wait that runs out is reported by the error
-  // word; the block goes on, so that its threads stay together.)
-  __device__ __forceinline__ void take() {
-    mbar_wait(shared(full + at), phase, abort_flag, err, 1 << 16);
+  // Waits for the current slot's rows: there unless a thread gave up.
+  __device__ __forceinline__ void take(int flag) {
+    mbar_wait_within(shared(full + at), phase, state + flag, a.err, 1 << 16, [&] { return (long long)state[2] << 10; });
+  }
+  __device__ __forceinline__ bool gave_up(int flag) const { return state[flag] != 0; }
+  // The copies in flight land before the block's shared memory goes to another.
+  __device__ __forceinline__ void drain() const {
+    if (threadIdx.x != 0) return;
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 21)) {}
   }
   __device__ __forceinline__ const uint8_t* row_of(int t, int64_t row) const {
-    return slots + at * slot_bytes + t * part_bytes + (kWhole ? 0 : start(t, row) & 15);
+    return slots + at * a.slot_bytes + t * a.part_bytes + (kWhole ? 0 : start(t, row) & 15);
   }
   __device__ __forceinline__ void next() {
     if (++at == n) { at = 0; phase ^= 1; }
@@ -268,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
   __shared__ __align__(16) Sums red;
   extern __shared__ __align__(128) uint8_t ring_bytes[];
   __shared__ uint64_t full[kMostSlots];
-  __shared__ int aborted;
+  __shared__ int state[3];
   grid_launch_next();
   const Place at = place<kWarp, N>(lanes);
   RowSum<kWarp> sum{&red, lanes, 0};
@@ -282,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
   T* y = static_cast<T*>(a.y) + at.col;
   const int64_t by = (int64_t)gridDim.x * at.rows;
   int64_t first = (int64_t)blockIdx.x * at.rows;  // the round's first row: the same for the block
-  RowRing<1, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes, a.slots, 0, 0,
+  RowRing<1, (N > 1)> ring{ring_bytes, full, state, a, (uint32_t)(h * sizeof(T)), a.slots, 0, 0,
                   {static_cast<const uint8_t*>(a.x)}, {a.x_stride * (int64_t)sizeof(T)}};
   Piece<T, N> v[P];
   if constexpr (kRing) {
@@ -300,11 +314,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
     load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
     load_weights<W, N>(a.bias, at.col + p * at.step, live[p], 0.f, b + p * N);
   }
+  // (a running address costs less than a product a row: [65536, 520] bf16 46.5 us against 49.2; the
+  // forms with more pieces have no registers left for it)
+  constexpr bool kRunning = kRing && N == 8;
+  T* out = y + first * h;
+  const int64_t out_step = by * h;
   for (; first < a.rows; first += by) {
     const int64_t row = first + at.row;
     float f[E];
     if constexpr (kRing) {
-      ring.take();
+      ring.take(0);
       const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + at.col;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -331,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
     float s = s2.x + s2.y;
     sum(s);
     if constexpr (kRing) {  // (every thread has its pieces: the sum was a barrier)
+      if (ring.gave_up(0)) { ring.drain(); return; }
       if (threadIdx.x == 0 && row + a.slots * by < a.rows) ring.fetch(ring.at, row + a.slots * by);
       ring.next();
     }
@@ -355,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_norm(NormArgs a, int lane
       set2(f, i, __ffma2_rn(__fmul2_rn(at2(f, i), both(rstd)), at2(w, i), at2(b, i)));
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      if (live[p]) put<T, N>(y + row * h + p * at.step, f + p * N);
+      if (live[p]) put<T, N>((kRunning ? out : y + row * h) + p * at.step, f + p * N);
+    if (kRunning) out += out_step;
     if (at.col == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -373,7 +394,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads, kWarp ? sm
   extern __shared__ __align__(128) uint8_t ring_bytes[];
   float* fold = reinterpret_cast<float*>(ring_bytes);  // kWarp: [warps][2][width]
   __shared__ uint64_t full[kMostSlots];
-  __shared__ int aborted;
+  __shared__ int state[3];
   grid_launch_next();
   const Place at = place<kWarp, N>(lanes);
   RowSum<kWarp> sum{&red, lanes, 0};
@@ -391,7 +412,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads, kWarp ? sm
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weights<W, N>(a.w, at.col + p * at.step, live[p], 1.f, w + p * N);
   const float per = 1.f / (float)h;
-  RowRing<3, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes, a.slots, 0, 0,
+  RowRing<3, (N > 1)> ring{ring_bytes, full, state, a, (uint32_t)(h * sizeof(T)), a.slots, 0, 0,
                   {static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.dy),
                    a.dx ? static_cast<const uint8_t*>(a.residual) : nullptr},
                   {a.x_stride * (int64_t)sizeof(T), a.dy_stride * (int64_t)sizeof(T), a.r_stride * (int64_t)sizeof(T)}};
@@ -425,7 +446,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads, kWarp ? sm
       float s1, s2;
       Piece<T, N> vr[P];
       if constexpr (kRing) {
-        ring.take();
+        ring.take(sum.turn);
         const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + at.col;
         const T* sd = reinterpret_cast<const T*>(ring.row_of(1, row)) + at.col;
         const T* sr = reinterpret_cast<const T*>(ring.row_of(2, row)) + at.col;
@@ -490,6 +511,7 @@ __global__ void __launch_bounds__(kWarp ? kSmallBlock : kMostThreads, kWarp ? sm
       }
       sum(s1, s2);
       if constexpr (kRing) {  // (every thread has its pieces: the sum was a barrier)
+        if (ring.gave_up(sum.turn ^ 1)) { ring.drain(); return; }
         if (threadIdx.x == 0 && row + a.slots < last) ring.fetch(ring.at, row + a.slots);
         ring.next();
         if (!a.dx) continue;
@@ -564,20 +586,20 @@ __global__ void __launch_bounds__(kMostHeld) k_norm_backward_held(NormArgs a) {
   __shared__ __align__(16) Sums red;
   extern __shared__ __align__(128) uint8_t ring_bytes[];
   __shared__ uint64_t full[kMostSlots];
-  __shared__ int aborted;
+  __shared__ int state[3];
   grid_launch_next();
   RowSum<false> sum{&red, 32, 0};
   sum.init();
   const int h = (int)a.width, step = (int)blockDim.x * N, col = (int)threadIdx.x * N;
   grid_wait();
   const float per = 1.f / (float)h;
-  RowRing<3, (N > 1)> ring{ring_bytes, full, &aborted, a.err, (uint32_t)(h * sizeof(T)), a.part_bytes, a.slot_bytes,
-                           a.slots, 0, 0,
+  RowRing<3, (N > 1)> ring{ring_bytes, full, state, a, (uint32_t)(h * sizeof(T)), a.slots, 0, 0,
                            {static_cast<const uint8_t*>(a.x), static_cast<const uint8_t*>(a.dy),
                             a.dx ? static_cast<const uint8_t*>(a.residual) : nullptr},
                            {a.x_stride * (int64_t)sizeof(T), a.dy_stride * (int64_t)sizeof(T),
                             a.r_stride * (int64_t)sizeof(T)}};
   ring.init();
+  int flag = 0;
   for (int64_t part = blockIdx.x; part < a.parts; part += gridDim.x) {
     const int64_t first = part * a.part_rows, last = min(a.rows, first + a.part_rows);
     if (threadIdx.x == 0)
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(kMostHeld) k_norm_backward_held(NormArgs a) {
         next_mean = a.mean[row + 1];
         next_rstd = a.rstd[row + 1];
       }
-      ring.take();
+      ring.take(flag);
       const T* sx = reinterpret_cast<const T*>(ring.row_of(0, row)) + col;
       const T* sd = reinterpret_cast<const T*>(ring.row_of(1, row)) + col;
       const T* sr = reinterpret_cast<const T*>(ring.row_of(2, row)) + col;
@@ -617,6 +639,7 @@ __global__ void __launch_bounds__(kMostHeld) k_norm_backward_held(NormArgs a) {
       }
       if (a.dx) {
         sum(s1, s2);
+        if (ring.gave_up(flag)) { ring.drain(); return; }
         s1 *= per;
         s2 *= per;
 #pragma unroll
@@ -640,8 +663,10 @@ __global__ void __launch_bounds__(kMostHeld) k_norm_backward_held(NormArgs a) {
         }
       }
       __syncthreads();  // everyone is done with the slot
+      if (ring.gave_up(flag)) { ring.drain(); return; }
       if (threadIdx.x == 0 && row + a.slots < last) ring.fetch(ring.at, row + a.slots);
       ring.next();
+      flag ^= 1;
     }
     if (!a.part) continue;
     float* out = a.part + part * 2 * h + col;
@@ -928,6 +953,7 @@ cudaError_t forward(NormArgs a, cudaStream_t s) {
     fn = f.threads > 256 ? k_norm<T, W, N, 2 * kEach, false, 512, 1> : k_norm<T, W, N, 2 * kEach, false, 256, 2>;
   size_t smem = 0;
   cudaError_t e = ops_error_word(&a.err);
+  if (a.wait_limit == 0) a.wait_limit = (int32_t)(kWaitCycles >> 10);
   if (e == cudaSuccess) {
     smem = set_slots(&a, a.width * (int64_t)sizeof(T), 1, N > 1, f.blocks);
     e = allow(fn);
@@ -952,6 +978,7 @@ cudaError_t backward(NormArgs a, cudaStream_t s) {
     const dim3 grid((unsigned)(a.parts < most ? a.parts : most)), block((unsigned)f.threads);
     size_t smem = f.warp ? sizeof(float) * 2 * a.width * (f.threads / 32) : 0;
     e = ops_error_word(&a.err);
+    if (a.wait_limit == 0) a.wait_limit = (int32_t)(kWaitCycles >> 10);
     if (e == cudaSuccess && !f.warp) {
       smem = set_slots(&a, a.width * (int64_t)sizeof(T), a.dx && a.residual ? 3 : 2, N > 1, f.blocks);
       e = f.held ? allow(k_norm_backward_held<T, W, N>) : allow(k_norm_backward<T, W, N, false>);

@@ -42,20 +42,26 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint32_t a, uint32_t parity
       : "memory");
 }
 // Bounded wait: false if another role aborted or the wait ran out (then the
-// error word gets bit `code` and every role is told to stop).
-__device__ __forceinline__ bool mbar_wait(uint32_t a, uint32_t parity, volatile int* abort_flag,
-                                          int* err, int code, long long limit = kWaitCycles) {
+// error word gets bit `code` and every role is told to stop).  limit(): cycles, asked
+// for only once the barrier was not there at first.
+template <typename L>
+__device__ __forceinline__ bool mbar_wait_within(uint32_t a, uint32_t parity, volatile int* abort_flag,
+                                                 int* err, int code, L limit) {
   if (mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(a, parity)) {
     if (*abort_flag) return false;
-    if (clock64() - t0 > limit) {
+    if (clock64() - t0 > limit()) {
       *abort_flag = 1;
       if (err) atomicOr(err, code);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t a, uint32_t parity, volatile int* abort_flag,
+                                          int* err, int code, long long limit = kWaitCycles) {
+  return mbar_wait_within(a, parity, abort_flag, err, code, [=] { return limit; });
 }
 
 }  // namespace muon

@@ -154,6 +154,9 @@ struct NormArgs {
   uint32_t part_bytes, slot_bytes;  // of the ring of rows on their way
   int32_t slots;
   int* err;
+  // Of the waits for a row: their limit in 1024 cycles (0: the library's); and for a test of
+  // one that runs out, the slot (from 1; 0: none) of a block whose barrier nothing completes.
+  int32_t wait_limit, lost_slot, lost_block;
 };
 int64_t norm_part_rows(int64_t rows, int64_t width);  // most parts that launch_norm_backward uses
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);

@@ -1,12 +1,13 @@
 // Test hooks (include/muon_testing.h): one tcgen05 product on caller buffers,
-// the GEMMs' tile walks, the skinny kernel's cluster occupancy, and a
-// bounded wait that times out.
+// the GEMMs' tile walks, the skinny kernel's cluster occupancy, and bounded
+// waits that time out.
 #include <cstring>
 
 #include <cuda_runtime.h>
 
 #include "../../include/muon_testing.h"
 #include "internal.h"
+#include "ops_checks.h"
 
 using namespace muon;
 
@@ -93,4 +94,35 @@ extern "C" muon_status_t muon_testing_wait_probe(int32_t arrive, int64_t limit_c
   cudaFree(err);
   if (e != cudaSuccess) return MUON_ERR_CUDA;
   return w ? MUON_ERR_TIMEOUT : MUON_OK;
+}
+
+extern "C" muon_status_t muon_testing_norm_lost_row(int32_t dtype, int64_t rows, int64_t width, int32_t block,
+                                                    int32_t slot, int64_t limit_cycles, const void* x, const void* dy,
+                                                    float* mean, float* rstd, void* out, void* dw, void* stream) {
+  if (!dtype_ok(dtype) || rows < 1 || rows > (1 << 20) || width <= 512 || width > 16384 || block < 0 || slot < 0 ||
+      slot > 7 || limit_cycles < 1024 || limit_cycles > (1ll << 33) || !x ||
+      (dy ? !mean || !rstd || (!out && !dw) : !out || dw))
+    return MUON_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormArgs a{};
+  a.dtype = a.w_dtype = dtype;
+  a.rows = rows; a.width = width; a.eps = 1e-5f;
+  a.x = x; a.x_stride = width;
+  a.mean = mean; a.rstd = rstd;
+  a.wait_limit = (int32_t)(limit_cycles >> 10);
+  a.lost_slot = slot + 1;
+  a.lost_block = block;
+  cudaError_t e = cudaSuccess;
+  if (dy) {
+    a.dy = dy; a.dy_stride = width; a.dx = out; a.dw = dw;
+    if (dw && cudaMalloc(&a.part, sizeof(float) * 2 * width * norm_part_rows(rows, width)) != cudaSuccess)
+      return MUON_ERR_OOM;
+    e = launch_norm_backward(a, s);
+  } else {
+    a.y = out;
+    e = launch_norm(a, s);
+  }
+  const muon_status_t st = muon_ops_check_error();
+  cudaFree(a.part);
+  return e == cudaSuccess ? st : MUON_ERR_CUDA;
 }
