@@ -63,15 +63,19 @@ __device__ __forceinline__ uint4 pack8(const float* f, int type) {
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
   return u;
 }
-// SiLU and the tanh form of GELU of 16-bit tensors, two values at a time: the operations of
-// activate<true> in the same order (all 2^32 arguments give the same bits).  The hardware's
-// exponential and reciprocal may flush numbers below 2^-126 to zero here: e^-v is far below
-// the last place of 1 then, and __fdividef gives zero too.  The epilogue takes issue slots
-// and power from the product: 4096 tokens, [4096, 16384] in 4 bits, bias, gelu_tanh 113 us
-// against 121 one value at a time, silu 109 against 113.  (Done so for GELU too, that form
-// gains nothing, 139, and the others lose it again, 128 and 122.)
+// SiLU and the tanh form of GELU of 16-bit tensors, two values at a time: both are z p
+// with p = 1 / (1 + e^-v) = 1 / (1 + 2^t), t = -v log2(e), on the hardware's power of two
+// and reciprocal (PTX ex2.approx, within 2^-22 of itself, and rcp.approx, 2^-23).  t is
+// rounded once and its factor once, which 2^t turns into 1.2 |v| 2^-24 of itself; with the
+// sum's and the product's roundings z p is within (1.2 |v| + 8) 2^-24 of itself: 7e-6 at
+// v = -87, far below half a step of the 16-bit store (2^-11, 2^-8).  Beyond, 2^t > 2^126,
+// p may be flushed to 0: off by 2^-126 |z| at most.  Infinite v give 1 and 0.  Every 16-bit
+// number is tested against these bounds.  The epilogue takes issue slots and power from the
+// product: 4096 tokens, [4096, 16384] in 4 bits, bias, gelu_tanh 113 us against 121 one
+// value at a time, silu 109 against 113.  (Done so for GELU too, that form gains nothing,
+// 139, and the others lose it again, 128 and 122.)
 __device__ __forceinline__ float2 sigmoid2(float2 v) {
-  const float2 t = __fmul2_rn(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));  // e^-v = 2^t
+  const float2 t = __fmul2_rn(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
   float2 e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
