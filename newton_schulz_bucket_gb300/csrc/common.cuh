@@ -60,6 +60,26 @@ inline cudaError_t launch_early(void (*fn)(P...), dim3 grid, dim3 block, size_t 
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, fn, P(args)...);
 }
+// The same in clusters of `cluster` blocks.
+template <typename... P, typename... A>
+inline cudaError_t launch_early_cluster(void (*fn)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                                        cudaStream_t s, A... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(grid);
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 2;
+  return cudaLaunchKernelEx(&lc, fn, P(args)...);
+}
 
 // Sum over a warp with a fixed butterfly: the result depends only on the 32
 // inputs, never on timing.

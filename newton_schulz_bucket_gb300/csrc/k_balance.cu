@@ -16,6 +16,7 @@
 // (4.7), where the latency of the two launches counts.
 #include "common.cuh"
 #include "ops.h"
+#include "tcgen05.cuh"
 
 namespace muon {
 
@@ -81,15 +82,9 @@ __device__ __forceinline__ bool exponentials(float* v, int lanes, bool* nan) {
   return high > -kInf || *nan;
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t word_of(const void* p, int rank) {  // of the same place in block `rank`
-  const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
-  uint32_t remote, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
+template <typename T>
+__device__ __forceinline__ T word_of(const T* p, int rank) {  // of the same place in block `rank`
+  return ld_shared_of<T>(saddr(p), (uint32_t)rank);
 }
 
 __device__ __forceinline__ void write_loss(const BalanceArgs& a, float dot, long long made, int tokens) {
@@ -189,8 +184,8 @@ __global__ void __launch_bounds__(kCluster ? kClusterThreads : kForward<NV>) k_b
         int c = 0;
 #pragma unroll
         for (int r = 0; r < kClusterBlocks; ++r) {
-          if (e < a.experts) s += __uint_as_float(word_of(fold + e, r));
-          c += (int)word_of(hist + e, r);
+          if (e < a.experts) s += word_of(fold + e, r);
+          c += word_of(hist + e, r);
         }
         if (e < a.experts) {
           a.counts[e] = c;
@@ -366,25 +361,6 @@ __global__ void __launch_bounds__(kBackward) k_balance_backward(BalanceArgs a, i
   }
 }
 
-template <typename F, typename... A>
-cudaError_t launch_cluster(F fn, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(kClusterBlocks);
-  lc.blockDim = dim3(kClusterThreads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kClusterBlocks;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, fn, args...);
-}
-
 template <typename T, int NV>
 cudaError_t run_nv(const BalanceArgs& a, bool backward, bool vec, cudaStream_t s) {
   int lanes = 1;
@@ -397,7 +373,8 @@ cudaError_t run_nv(const BalanceArgs& a, bool backward, bool vec, cudaStream_t s
   const auto smem = [&](int threads) { return sizeof(float) * (threads / 32) * a.experts + sizeof(int) * (a.experts + 1); };
   if constexpr (NV == 8) {
     if (a.blocks == 0) {
-      return launch_cluster(k_balance<T, NV, true>, smem(kClusterThreads), s, a, lanes, vec);
+      return launch_early_cluster(k_balance<T, NV, true>, kClusterBlocks, kClusterThreads, smem(kClusterThreads),
+                                  kClusterBlocks, s, a, lanes, vec);
     }
   }
   return launch_early(k_balance<T, NV, false>, dim3((unsigned)a.blocks), dim3(kForward<NV>), smem(kForward<NV>), s, a, lanes,
@@ -435,7 +412,8 @@ int balance_blocks(int64_t tokens, int32_t experts) {
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
   cudaError_t e = dispatch(a, false, s);
-  if (e == cudaSuccess && a.blocks > 0) e = launch_cluster(k_balance_join, 0, s, a);
+  if (e == cudaSuccess && a.blocks > 0)
+    e = launch_early_cluster(k_balance_join, kClusterBlocks, kClusterThreads, 0, kClusterBlocks, s, a);
   return e;
 }
 cudaError_t launch_balance_backward(const BalanceArgs& a, cudaStream_t s) { return dispatch(a, true, s); }

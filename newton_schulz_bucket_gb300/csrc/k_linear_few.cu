@@ -41,17 +41,6 @@ struct FewArgs {
   int* err;
 };
 
-__device__ __forceinline__ float ld_shared_of(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to(addr, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
 // ACROSS: weights stored across the sum ([in][out] for y).
 template <bool ACROSS>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -175,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t t = i >> 7, f = m0 + (i & 127);
     if (f >= p.M) continue;
     float z = 0.f;
-    for (int r = 0; r < shares; ++r) z += ld_shared_of(saddr(part + i), (uint32_t)r);
+    for (int r = 0; r < shares; ++r) z += ld_shared_of<float>(saddr(part + i), (uint32_t)r);
     if (p.bias) z += ld_el(p.bias, f, p.type);
     if (p.preact) st_el(p.preact, t * p.M + f, z, p.type);
     z = p.type == DT_F32 ? activate<false>(z, p.act) : activate<true>(z, p.act);
@@ -206,21 +195,7 @@ cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const FewArgs& 
       if (dev < 64) ready[dev] = true;
     }
   }
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)(tiles * shares));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = kSmemBytes;
-  lc.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)shares;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, fn, mw, mx, q);
+  return launch_early_cluster(fn, (unsigned)(tiles * shares), kThreads, kSmemBytes, (unsigned)shares, s, mw, mx, q);
 }
 
 }  // namespace

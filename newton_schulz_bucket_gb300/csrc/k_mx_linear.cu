@@ -396,20 +396,6 @@ struct FewArgs {
   int* err;
 };
 
-__device__ __forceinline__ float4 ld_shared_of(uint32_t addr, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(map_to(addr, rank))
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
 // What one of the four warps puts into a stage itself (kOwn): the scales of 32 weight
 // rows, and of the 16 token rows every fourth, 256 steps each, eight a lane.
 template <typename T>
@@ -606,7 +592,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     float4 v[kMaxShares];
 #pragma unroll
     for (int r = 0; r < kMaxShares; ++r)
-      if (r < shares) v[r] = ld_shared_of(saddr(part + 4 * i), (uint32_t)r);
+      if (r < shares) v[r] = ld_shared_of<float4>(saddr(part + 4 * i), (uint32_t)r);
     float z[4] = {};
 #pragma unroll
     for (int r = 0; r < kMaxShares; ++r)
@@ -638,26 +624,6 @@ cudaError_t prepare(F fn, uint32_t smem, bool* ready, std::mutex& mu) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && dev < 64) ready[dev] = true;
   return e;
-}
-
-template <typename F, typename... A>
-cudaError_t launch_cluster(F fn, unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
-                           A... args) {
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(grid);
-  lc.blockDim = dim3(threads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, fn, args...);
 }
 
 // Rows of `blocks` 16-byte blocks as 16-bit elements (a stage's rows are 64 of them).
@@ -707,7 +673,7 @@ cudaError_t run_few(const MxProduct& p, cudaStream_t s) {
   int shares = places / tiles < kMaxShares ? places / tiles : kMaxShares;
   if (shares > blocks) shares = blocks;
   if (shares < 1) shares = 1;
-  return launch_cluster(fn, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, ms, a);
+  return launch_early_cluster(fn, (unsigned)(tiles * shares), kFewThreads, kFewSmem, (unsigned)shares, s, mw, mx, ms, a);
 }
 
 template <int NB>
@@ -740,7 +706,7 @@ cudaError_t run_tiles(const MxProduct& p, cudaStream_t s) {
   if (p.experts) most = p.rows / a.tile_rows + (p.rows < mats ? p.rows : mats);  // at most
   most *= a.tiles_m;
   const unsigned grid = (unsigned)(2 * (most < 1 ? 1 : (most < pairs ? most : pairs)));
-  return launch_cluster(k_mx_tiles<NB>, grid, kThreads, kSmem, 2, s, mw, mx, ms, a);
+  return launch_early_cluster(k_mx_tiles<NB>, grid, kThreads, kSmem, 2, s, mw, mx, ms, a);
 }
 
 }  // namespace

@@ -108,6 +108,28 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+// Shared memory of CTA `rank` at this CTA's address `addr`.
+template <typename T>
+__device__ __forceinline__ T ld_shared_of(uint32_t addr, uint32_t rank) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 16, "a word or four");
+  union {
+    uint32_t u[sizeof(T) / 4];
+    T v;
+  } r;
+  if constexpr (sizeof(T) == 4)
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r.u[0]) : "r"(map_to(addr, rank)) : "memory");
+  else
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.u[0]), "=r"(r.u[1]), "=r"(r.u[2]), "=r"(r.u[3])
+                 : "r"(map_to(addr, rank))
+                 : "memory");
+  return r.v;
+}
 // A tile copy whose completion is counted on an mbarrier that may sit in the
 // peer CTA of the pair (`mbar` a shared::cluster address).
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t mbar,
