@@ -17,8 +17,9 @@
  *
  * Conventions, beyond those of muon.h (statuses, muon_last_error, streams):
  *  - Stateless calls.  Every buffer is the caller's; scratch is a caller
- *    buffer whose size the operator's _workspace call gives, 256-byte aligned, free for reuse once the call's work on `stream` is
- *    done.  No call allocates device memory or synchronises, so every call can
+ *    buffer whose size the operator's _workspace call gives, 256-byte
+ *    aligned, free for reuse once the call's work on `stream` is done.  No
+ *    call allocates device memory or synchronises, so every call can
  *    be captured in a CUDA graph (the first call of each operator on a device
  *    sets kernel attributes: host work, make it before a capture).
  *  - The current device must be the device of `stream` and of the buffers.
@@ -72,7 +73,8 @@ typedef enum { MUON_W_IN_OUT = 0, MUON_W_OUT_IN = 1 } muon_weight_layout_t;
  * go through matrix e, with row e of bias [E, out].  Rows before offsets[0] and
  * from offsets[E] on belong to no expert: their outputs are zero and they add to
  * no gradient.
- * (Offsets outside [0, rows] are clamped, so they cannot lead out of a buffer.)
+ * (Offsets outside [0, rows] are clamped, so they cannot lead out of a buffer; where they
+ * decrease, rows get results of no meaning, and no access leads out of a buffer either.)
  *
  * muon_linear reads x, w, bias (nullable), residual (nullable; added after
  * the activation) and writes y, and z to preact_out (nullable) for the way
@@ -204,7 +206,9 @@ MUON_API muon_status_t muon_combine_backward(int32_t dtype, int64_t tokens, int6
  *   y[t] = (x[t] - mean[t]) * rstd[t] * w + bias.
  * x: `dtype` [rows, width] with row stride x_stride; w and bias: w_dtype (dtype or
  * F32) [width], nullable (ones, zeros); y: `dtype` [rows, width]; mean and rstd: fp32
- * [rows], nullable, for the way back.  Errors: INVALID_ARG (NULL x or y with rows >
+ * [rows], nullable, for the way back.  The sums are fp32, as long as a row may be: one
+ * whose elements add up beyond the largest fp32 number gets a mean of infinity, and one
+ * whose squared deviations do an rstd of 0.  Errors: INVALID_ARG (NULL x or y with rows >
  * 0; rows not in [0, 2^30], width not in [1, 2^30]; eps negative or not finite;
  * stride; dtypes; stream), CUDA. */
 MUON_API muon_status_t muon_layer_norm(int32_t dtype, int32_t w_dtype, int64_t rows, int64_t width,
@@ -238,9 +242,10 @@ MUON_API muon_status_t muon_balance_loss_workspace(int64_t tokens, int32_t exper
  *   counts[e] = assignments of indices to e,   live = tokens with a logit above -inf,
  *   loss = coef * experts * sum_e (counts[e] / sum of counts) * (sum over tokens of p[e] / live),
  * coef for a router that is even.  A logit of -inf masks its expert, and a token of
- * which all are masked (padding) counts nowhere; an index outside [0, experts) is
- * no assignment; without assignments or live tokens the loss is 0.  A NaN logit makes
- * the loss NaN.  logits and indices as muon_gate takes and gives them; loss: fp32 [1];
+ * which all are masked (padding) has no probabilities and is not live; every index in
+ * [0, experts) is an assignment, any other none (muon_gate gives a padded token -1 only);
+ * without assignments or live tokens the loss is 0.  A NaN or +inf logit makes the loss
+ * NaN.  logits and indices as muon_gate takes and gives them; loss: fp32 [1];
  * counts: int32 [experts]; live: int32 [1].  Errors: INVALID_ARG (as muon_gate; coef
  * not finite; tokens * top_k > 2^31 - 1; workspace), CUDA. */
 MUON_API muon_status_t muon_balance_loss(int32_t dtype, int64_t tokens, int32_t experts, int32_t top_k,
@@ -253,7 +258,8 @@ MUON_API muon_status_t muon_balance_loss(int32_t dtype, int64_t tokens, int32_t 
  *   dlogits = dloss * coef * experts / live * p * (f - <p, f>) + residual.
  * counts and live as muon_balance_loss gave them; dloss: fp32 [1] on the device;
  * residual (nullable): `dtype` [tokens, experts], the logits' gradient through the gate's
- * weights.  A masked expert gets the residual alone.  dlogits: `dtype`, contiguous.
+ * weights.  A masked expert gets the residual alone; in a token with a NaN or +inf logit
+ * all others come out NaN.  dlogits: `dtype`, contiguous.
  * Errors: as muon_balance_loss. */
 MUON_API muon_status_t muon_balance_loss_backward(int32_t dtype, int64_t tokens, int32_t experts,
                                                   float coef, const float* dloss, const void* logits,

@@ -11,9 +11,11 @@
 // experts' probabilities over its tokens, in two levels (kRun tokens, then their
 // sums), so that long batches keep their digits; lanes, warps and blocks are then
 // added in a fixed order, and counts are whole numbers: the same bits every time.
-// Bound by issue (the exponentials and a token's reductions), not by HBM: 131072 tokens of 64
-// experts, fp32, 34 MB, take 21 us (back, 67 MB, 18), 32768 of 512 44 (49); 16384 of 64 9.7
-// (4.7), where the latency of the two launches counts.
+// Bound by the latency of its loads: a lane has one token ahead on its way, and none on the
+// way back, so that DRAM is at 25% (back 22%) and the SM's busiest unit at 51% (60%) of their
+// peaks, and waiting for loads is the largest stall.  131072 tokens of 64 experts, fp32, 34 MB,
+// take 21 us (back, 67 MB, 18), 32768 of 512 44 (49); 16384 of 64 9.3 (4.7), where the
+// latency of the two launches counts.
 #include "common.cuh"
 #include "ops.h"
 #include "tcgen05.cuh"

@@ -2,22 +2,25 @@
 // gradient: with xh = (x - mean) rstd and g = dy w,
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + r,   dw = sum over rows of dy xh,   db = sum of dy.
 //
-// Every tensor crosses HBM once: a row stays in the registers of its threads (16 or 32
-// elements each) between the sums over it and its result, and the next rows are on their
-// way meanwhile: several, by bulk copies into a ring in shared memory, where a row belongs
-// to a block; else the next one, into registers.  Rows of up to 512 elements belong to 1
-// to 32 lanes of a warp, longer ones to a block.  The variance is the sum of squares about
-// the mean, not a difference of two large sums.  Blocks stay for many rows, so that the
-// weights are read once a block and the sums over rows (dw, db) grow in registers too;
-// each part of rows leaves one partial sum, and a second kernel adds the parts in a fixed
-// order.  No atomics: the same bits every time.
+// Rows of up to 16384 elements cross HBM once.  Up to 512 of them belong to 1 to 32 lanes
+// of a warp, more to a block.  A row stays in the registers of its threads (16 or 32
+// elements each) between the sums over it and its result; where those hold the sums over
+// rows already (back, beyond 8192 elements) it stays in shared memory and is read twice from
+// there.  The next rows are on their way meanwhile: several, by bulk copies into a ring in
+// shared memory, where a row belongs to a block; else the next one, into registers.  Rows
+// beyond 16384 elements are read again for each sum (from L2, where they are not too long).
+// The variance is the sum of squares about the mean, not a difference of two large sums.
+// Blocks stay for many rows, so that the weights are read once a block and the sums over
+// rows (dw, db) grow in registers too; each part of rows leaves one partial sum, and a second
+// kernel adds the parts in a fixed order.  No atomics: the same bits every time.
 //
-// Bound by HBM where rows are whole 16-byte pieces ([8192, 4096] bf16 24.5 us, 5.5 TB/s; its
-// gradient with a residual 50, without 43; [65536, 512] fp32 gradient 73, 5.5 TB/s), and by
-// issue where they are not and an element is a load from the ring and a store of its own
-// ([8192, 4095] bf16 50 and 81 us, fp32 48 and 71; read from memory by the lanes, without the
-// ring: 106 and 188, 123 and 206).  Few rows are bound by latency: one of 4096 3.1 us, its
-// gradient 5.7 in two launches.
+// Bound by HBM where rows are whole 16-byte pieces ([8192, 4096] bf16 24.1 us, 5.6 TB/s; its
+// gradient with a residual 51, without 43; [65536, 512] fp32 gradient 73, 5.5 TB/s).  Where
+// they are not, an element is a load from the ring and a store of its own: loads of one
+// element and fixed latencies are what warps wait for, at 52% (back 62%) of the SM's busiest
+// unit ([8192, 4095] bf16 50.5 and 82 us, fp32 49 and 72; read from memory by the lanes,
+// without the ring: 106 and 188, 123 and 206).  Few rows are bound by latency: one of 4096
+// 3.1 us, its gradient 5.5 in two launches.
 #include <mutex>
 #include <type_traits>
 
@@ -33,7 +36,7 @@ constexpr int kEach = 16;        // elements of a row that a thread holds
 constexpr int kSmallBlock = 128; // threads of a block whose warps hold whole rows
 // Blocks of them on an SM, by the elements of a load: as many as the registers allow
 // without spills that cost more than a block less ([131072, 256] bf16 back: 45 us with
-// four, 60 with three; [131072, 255]: 142 with four, 93 with two; forward: 51 with four,
+// four, 47 with three; [131072, 255]: 142 with four, 88 with two; forward: 51 with four,
 // 116 with six).
 constexpr int small_blocks(int n, bool backward) { return backward ? (n == 1 ? 2 : n == 4 ? 3 : 4) : (n == 1 ? 4 : 6); }
 constexpr int kMostThreads = 512;
@@ -865,9 +868,10 @@ __global__ void __launch_bounds__(1024) k_norm_join(NormArgs a) {
 // How rows of this width are held: by lanes of a warp, by a block (`each` elements a
 // thread, `blocks` blocks an SM), in the ring, or by none.  Forward, rows but fp32 ones in
 // whole pieces take 32 elements a thread where there are rows enough to fill the GPU: the
-// sums over a row then cost half as much of a thread ([8192, 4096] bf16: 25.5 us against 31;
-// fp32 in whole pieces is bound by HBM, 47 against 45).  Rows that 512 threads of 16 do not
-// hold take 32 too ([2000, 12001] bf16 47 us; read again for each sum 83).
+// sums over a row then cost half as much of a thread ([8192, 4096] bf16: 24.1 us, 29.2 with
+// 16; fp32 in whole pieces is bound by HBM with either, 48.4 with 16, 47.7 with 32).  Rows
+// that 256 threads of 16 do not hold take 32 too ([2000, 12001] bf16 47.7 us; read again for
+// each sum 83).
 struct Form {
   bool warp, held, wide;
   int lanes, threads, each, blocks;

@@ -22,7 +22,7 @@ struct TcProduct {
   int rows, K;              // rows form: token rows; the sum's length (GROUP_SUM: all rows)
   int M, N;                 // rows form: features (M); sum form: the output
   int tiles_m, tiles_n;     // sum form; rows form: feature tiles (tiles_m)
-  int tile_rows;            // rows form: most token rows of a tile (64, 128 or 256)
+  int tile_rows;            // rows form: most token rows of a tile (64, 128 or 256; 4-bit operands 64, 128 or 192)
   int stages;               // rows form: ring depth, more for smaller tiles
   int type, act, vec;       // DType; vec: output rows (and the epilogue's tensors) start on 16 bytes
   void* D;                  // rows form: [rows][M]; sum form: [M][N] per expert

@@ -21,7 +21,7 @@ muon_status_t check_pitch(const char* what, int64_t stride, int64_t width) {
     return fail(MUON_ERR_INVALID_ARG, "%s: a row stride must be in [width, 2^36]", what);
   return MUON_OK;
 }
-// Column blocks of the widest rows times parts of the sum over rows.
+// The parts' sums over rows: dw and db of every column, fp32.
 size_t norm_bytes(int64_t rows, int64_t width) {
   return align256((size_t)norm_part_rows(rows, width) * 2 * width * sizeof(float));
 }

